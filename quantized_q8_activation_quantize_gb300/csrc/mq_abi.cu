@@ -45,14 +45,6 @@ __global__ void forced_timeout_kernel(unsigned int *err, uint64_t timeout_ns) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// whether the byte ranges [a, a + na) and [b, b + nb) share a byte
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return na != 0 && nb != 0 && a0 < b0 + nb && b0 < a0 + na;
-}
-
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 // the tensor-core GEMMs put their token tiles (128 tokens) in grid.y, the fused gate|up GEMM its
 // output tiles (64 rows of gate and of up) there; CUDA caps grid.y at 65535
@@ -70,7 +62,7 @@ int set_error(int code, const char *fmt, ...) {
 
 namespace {
 int g_sm_count[kMaxDevices] = {0};
-constexpr int kAttrSlots = kAttrSlotSmall + 16;     // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM
+constexpr int kAttrSlots = kAttrSlotKv + 32;        // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM; cache
 bool g_attr_done[kMaxDevices][kAttrSlots] = {};
 }  // namespace
 
@@ -134,7 +126,7 @@ int cuda_error(cudaError_t e, const char *what) {
 }
 
 // Current device must be compute capability 10.3; resolves its error-word address once.
-static int device_state(unsigned int **err) {
+int device_state(unsigned int **err) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");

@@ -45,6 +45,17 @@ struct Dump {
 
 int set_error(int code, const char *fmt, ...);
 
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// whether the byte ranges [a, a + na) and [b, b + nb) share a byte
+inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return na != 0 && nb != 0 && a0 < b0 + nb && b0 < a0 + na;
+}
+
+// MQ_OK if the current device is compute capability 10.3, with the address of its error word
+int device_state(unsigned int **err);
+
 // SM count of the current device (cached per device)
 int sm_count();
 
@@ -107,5 +118,7 @@ int launch_quantize_grouped(int nj, const float *const *x, const Plane *p, int64
 void *tensor_map_encoder();
 // attribute slots of the small-M GEMM: kAttrSlotSmall + 2 * (3 fmt + NT/32) + dump
 constexpr int kAttrSlotSmall = kAttrSlotSwiglu + 8;
+// attribute slots of the cache's attention: 2 * dtype + (head_dim == 128), 8 per kernel
+constexpr int kAttrSlotKv = kAttrSlotSmall + 16;
 
 }  // namespace mq

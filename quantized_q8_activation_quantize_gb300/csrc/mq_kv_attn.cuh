@@ -1,0 +1,52 @@
+// mq_kv_attn.cuh -- what the attention kernels share.
+#pragma once
+
+#include "mq_kv.cuh"
+
+namespace mq {
+
+constexpr float kLog2e = 1.44269504088896341f;
+// the softmax weights enter the tensor cores as exp2(s - m + kPShift) times the V scale over the running largest V
+// scale, at most 2^kPShift: the shift keeps small weights out of f16's subnormals
+constexpr float kPShift = 12.0f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// four codes of a word as two f16 pairs, exactly: byte b becomes the f16 1024 + b, minus 1152
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off), y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+    lo = *reinterpret_cast<uint32_t *>(&x);
+    hi = *reinterpret_cast<uint32_t *>(&y);
+}
+
+// 2^e with e such that amax * 2^-e lies in [2^14, 2^15) (1 where amax is 0); a row is multiplied by 2^-e before it
+// becomes f16.  Exponents stay where 2^e and 2^-e are normal numbers.
+__device__ __forceinline__ int row_exponent(float amax) {
+    const int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127 - 14;
+    return amax == 0.0f ? 0 : min(max(e, -120), 120);
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// positions [lo, hi) that the row at position p of a sequence of len tokens sees
+__device__ __forceinline__ void row_range(int64_t p, int64_t len, int causal, int64_t window, int64_t &lo, int64_t &hi) {
+    hi = causal ? min(p + 1, len) : len;
+    lo = window > 0 ? max(p - window + 1, (int64_t)0) : 0;
+    if (hi <= lo) lo = hi = 0;
+}
+
+// 5-D tiled copy global -> shared through a CUtensorMap
+__device__ __forceinline__ void tma_load_5d(void *dst_smem, const void *tmap, int32_t x, int32_t y, int32_t z, int32_t w, int32_t v, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            smem_u32(dst_smem)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
+
+}  // namespace mq
