@@ -467,6 +467,9 @@ int kv_tensor_map(CUtensorMap *tm, const mqkv_cache &c, const mqkv_layout &lay) 
 
 int64_t tiles_of(int dtype, int64_t rows) { return dtype == MQKV_F32 ? (rows + 7) / 8 : (rows + 15) / 16; }
 
+// rows per KV head from which the tcgen05 tiles of mq_kv_prefill.cu are taken
+bool use_tiles(int64_t rows) { return rows > 64; }
+
 int splits_of(int32_t n_seqs, int32_t H, int64_t tiles, int64_t max_kv) {
     const int64_t ctas = (int64_t)n_seqs * H * tiles, blocks = (max_kv + kKB - 1) / kKB;
     int64_t s = (2 * sm_count() + ctas - 1) / ctas;
@@ -493,6 +496,7 @@ int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t n_tokens, unsigned in
 
 size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t n_q_heads, int64_t n_tokens, int64_t max_q,
                        int64_t max_kv) {
+    if (use_tiles(max_q * (n_q_heads / H))) return 256;
     const int n = splits_of(n_seqs, H, tiles_of(dtype, max_q * (n_q_heads / H)), max_kv);
     return n == 1 ? 256 : (size_t)n_tokens * n_q_heads * n * (D + 2) * 4;
 }
@@ -502,6 +506,7 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
     CUtensorMap tm;
     int rc = kv_tensor_map(&tm, cache, lay);
     if (rc != MQ_OK) return rc;
+    if (use_tiles(p.max_q * p.group)) return kv_launch_prefill(tm, layer, c, r, p, err, s);
     AtArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
     a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = p.max_q, a.window = p.window;
