@@ -503,10 +503,10 @@ size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t 
 
 int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int layer, const KvView &c, const KvRows &r,
                         const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
+    if (use_tiles(p.max_q * p.group)) return kv_launch_prefill(c, r, p, err, s);
     CUtensorMap tm;
     int rc = kv_tensor_map(&tm, cache, lay);
     if (rc != MQ_OK) return rc;
-    if (use_tiles(p.max_q * p.group)) return kv_launch_prefill(tm, layer, c, r, p, err, s);
     AtArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
     a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = p.max_q, a.window = p.window;

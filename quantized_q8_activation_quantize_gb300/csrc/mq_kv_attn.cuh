@@ -8,8 +8,7 @@
 namespace mq {
 
 // the tiled kernel for many rows (mq_kv_prefill.cu)
-int kv_launch_prefill(const CUtensorMap &tm, int layer, const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err,
-                      cudaStream_t s);
+int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err, cudaStream_t s);
 
 constexpr float kLog2e = 1.44269504088896341f;
 // the softmax weights enter the tensor cores as exp2(s - m + kPShift) times the V scale over the running largest V

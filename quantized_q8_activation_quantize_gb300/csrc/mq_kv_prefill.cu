@@ -2,17 +2,24 @@
 // tcgen05: the products bound it, so everything else is arranged to keep the tensor core fed.
 //
 // Mathematics: that of mq_kv_attn.cu, in tiles of 128 rows x 128 tokens.  K and V codes are exact in f16, so
-// S = Q K^T accumulates exact products; a tile's score is S times (row scale) (K scale of the token's block), the
-// weights enter the second product as p' = 2^(s - m + shift) dv / g in f16.  f32 rows use two f16 parts of q and
-// of p' (twice the MMAs, f32 accuracy).  The reference m of a row moves only when its maximum grows by more than
-// kTau (powers of two, so the result does not depend on it beyond rounding), and g only when a V scale exceeds it, then to
-// twice that: O is rescaled a few times per row instead of at every tile.
+// S = Q K^T accumulates exact products; a tile's score is S times (row scale) (K scale of the token's block).
 //
-// CTA = 16 warps, two row tiles that share every K / V tile: warps 0-3 and 4-7 softmax of tile 0 and 1 (a thread
-// per row, the whole row of S in registers), 8-11 widen codes (raw bytes -> f16 operand tiles, 128-byte swizzle),
-// 12 TMA of the raw pages and the scales, 13 MMA issuer.  Order on the tensor core: PV0(j) S0(j+1) PV1(j) S1(j+1), so
-// the softmax of one tile runs under the products of the other.  P replaces S in TMEM (f16, A operand from TMEM);
-// V is the MN-major B operand, so it needs no transposition.
+// Both kernels: 16 warps; 8-11 widen codes (global memory -> registers -> f16 operand tiles with the 128-byte swizzle, a
+// ring of five), 12 looks up pages and scales ahead of everyone, 13 issues the MMAs; a softmax thread owns a row and
+// holds its 128 scores in registers.  P replaces S in TMEM (f16, the A operand comes from TMEM); V is the MN-major B
+// operand, so nothing is transposed.
+//
+// 16-bit rows (kv_tiles_kernel): two row tiles (256 rows) share every K / V tile, warps 0-3 and 4-7 their softmax; the
+// tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), the softmax of one tile under the products of the other.  A row's
+// reference maximum moves only when the maximum grows by more than kTau (a factor that cancels in o / l), and the V
+// scale reference g only when a scale exceeds it, to twice that, so O in TMEM is rescaled a few times per row
+// instead of at every tile.  V enters as f16(code * f16(256 dv / g)): its rounding is of the size of P's and it costs half a
+// multiplication per code and 256 rows, on P it cost as much per weight.
+//
+// f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
+// The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
+// each tile's P V goes to a fresh accumulator and warps 4-7 add it to the row's sum in registers, rounding to nearest,
+// under the products of the next tile: one row tile per CTA, S and O double-buffered.
 #include <cuda.h>
 
 #include <climits>
@@ -24,8 +31,10 @@ namespace mq {
 namespace {
 
 constexpr int kPfThreads = 512;
-constexpr int kPfRows = 256, kPfN = 128;       // rows of a CTA, tokens of a tile
-constexpr float kTau = 8.0f, kPfShift = 6.0f;   // p' <= 2^(6 + 8) in f16
+constexpr int kPfN = 128;                      // tokens of a tile
+constexpr int kPfSlots = 5;                    // f16 operand tiles in flight
+constexpr int kPfInfo = 4;                     // tiles that the lookup runs ahead
+constexpr float kTau = 8.0f, kPfShift = 6.0f;   // 16-bit rows: p <= 2^(6 + 8) in f16
 
 struct PfArgs {
     KvView c;
@@ -33,25 +42,31 @@ struct PfArgs {
     const void *q;
     void *out;
     int64_t qt, qh, ot, oh;
-    int32_t group, causal, tiles, layer;
+    int32_t group, causal, tiles;
     int64_t max_q, window;
     float c_log2;               // |scale| * log2(e)
     float sign;                 // of scale: folded into q, so that the score factors are not negative
 };
 
+// what the lookup leaves for a tile of four blocks
+struct PfInfo {
+    float dk[4], pv[4];         // K scales; V scales over g
+    int page[4];                // -1: no such block (codes of zero)
+    float gf, g;                // factor of what was summed before, g from here on
+    float pad[2];
+};
+
 template <int D, bool TWO>
 struct PfCfg {
-    static constexpr int PARTS = TWO ? 2 : 1;
-    static constexpr int NS = TWO ? 2 : 4;                     // f16 operand tiles in flight (K0 V0 K1 V1 ...)
-    static constexpr int OPT = kPfN * D * 2, RAWT = kPfN * D;
+    static constexpr int PARTS = TWO ? 2 : 1, TILES = TWO ? 1 : 2, ROWS = 128 * TILES;
+    static constexpr int OPT = kPfN * D * 2;
     static constexpr int QT = 128 * D * 2;                     // one part of one row tile
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_OP = OFF_Q + PARTS * 2 * QT;
-    static constexpr int OFF_RAW = OFF_OP + NS * OPT;
-    static constexpr int OFF_RS = OFF_RAW + 2 * RAWT;          // row scales [256]
-    static constexpr int OFF_INFO = OFF_RS + kPfRows * 4;      // [4 tiles][dk[4], dv[4]]
-    static constexpr int OFF_BAR = OFF_INFO + 4 * 8 * 4;
-    static constexpr int NBAR = 2 + 2 + 2 * NS + 4 + 2 + 2 + 2 + 1;
+    static constexpr int OFF_OP = OFF_Q + PARTS * TILES * QT;
+    static constexpr int OFF_RS = OFF_OP + kPfSlots * OPT;     // row scales [ROWS]; f32 rows: then factors [2][128]
+    static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 256 * 4 : 0);
+    static constexpr int OFF_BAR = OFF_INFO + kPfInfo * (int)sizeof(PfInfo);
+    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 4 * 2 + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA exceeds the per-CTA limit");
@@ -111,92 +126,116 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t m
     return d;
 }
 
-// a wait whose outcome is the same for the whole warp (a warp gives up together)
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned int *err, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait_prompt(bar, parity, err, KV_ERR_WAIT, abort));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const __grid_constant__ CUtensorMap tm, PfArgs a, unsigned int *err) {
-    constexpr bool TWO = sizeof(T) == 4;
-    using C = PfCfg<D, TWO>;
-    constexpr int NS = C::NS;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *s_rs = reinterpret_cast<float *>(sm + C::OFF_RS);
-    float *s_info = reinterpret_cast<float *>(sm + C::OFF_INFO);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
-    uint64_t *raw_full = bar, *raw_empty = bar + 2, *op_full = bar + 4, *op_empty = op_full + NS, *info_full = op_empty + NS,
-             *s_full = info_full + 4, *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The instruction cache is a resource here: four roles run their own straight-line code, and a fully unrolled version stalled on
+// instruction fetch more than on anything but memory.  So loops are unrolled only as far as the latencies ask.
 
-    grid_dep_launch();
-    grid_dep_wait();
-    // the CTA's rows: KV head fastest, then the sequence, the latest (longest) row tiles first
-    int64_t u = blockIdx.x;
-    const int h = (int)(u % a.c.H);
-    u /= a.c.H;
-    const int b = (int)(u % a.c.n_seqs), tile = a.tiles - 1 - (int)(u / a.c.n_seqs);
-    int64_t lo, hi;
-    a.r.of(b, lo, hi);
-    int64_t n = hi - lo;
-    if (n > a.max_q) {
-        if (threadIdx.x == 0) kv_error(err, KV_ERR_ROWS);
-        n = a.max_q;
-    }
-    const int64_t len = a.c.len[b], first = len - (hi - lo);
-    const int G = a.group;
-    const int64_t rows = n * G, r0 = (int64_t)tile * kPfRows;
-    if (r0 >= rows) return;
-    const bool bad = len < 0 || (len > 0 && ((len - 1) >> a.c.tshift) >= a.c.max_pages);
-    if (bad && threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
-    const int nrow = (int)min((int64_t)kPfRows, rows - r0);
-    const int nt = nrow > 128 ? 2 : 1;                         // row tiles
-    // what the rows see: the ranges' ends do not fall from row to row
-    int64_t t_lo = 0, t_hi = 0, all_lo = 0, all_hi = 0;
-    if (!bad) {
-        int64_t x0, y0, x1, y1;
-        row_range(first + r0 / G, len, a.causal, a.window, x0, y0);
-        row_range(first + (r0 + nrow - 1) / G, len, a.causal, a.window, x1, y1);
-        all_lo = max(x0, x1), all_hi = y0 > x0 ? min(y0, y1) : 0;
-        // the first row that sees anything starts no later than any other
-        t_hi = y1;
-        t_lo = y0 > x0 ? x0 : 0;
-        if (y1 <= x1) {                                        // the last row sees nothing: nor does any other
-            t_hi = 0;
-            if (y0 > x0) t_hi = y0, t_lo = x0;                   // (a window past the cache's end, without causality)
+// A bounded wait whose outcome is the same for the whole warp (a warp gives up together).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned int *err, volatile int *abort) {
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(at, parity)); ++i) {
+        if ((i & 255u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > kWaitTimeoutNs;
+            if (__any_sync(0xffffffffu, late || *abort)) {
+                if (late) kv_error(err, KV_ERR_WAIT);
+                *abort = 1;
+                return false;
+            }
         }
     }
-    const int64_t b_lo = t_lo / kKB, b_hi = (t_hi + kKB - 1) / kKB;
-    const int nj = (int)((b_hi - b_lo + 3) / 4);               // token tiles
-    const int64_t base = b_lo * kKB;
+    return true;
+}
+// one arrival for the warp, after what its lanes did
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 128);
-            mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 128);
-            mbar_init(o_done + i, 1);
-        }
-        for (int i = 0; i < NS; ++i) mbar_init(op_full + i, 128), mbar_init(op_empty + i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(info_full + i, 1);
+struct PfBars {
+    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *drain, *l_full;
+    __device__ __forceinline__ explicit PfBars(uint64_t *b) {
+        op_full = b, op_empty = op_full + kPfSlots, info_full = op_empty + kPfSlots, info_empty = info_full + kPfInfo;
+        s_full = info_empty + kPfInfo, p_full = s_full + 2, o_done = p_full + 2, o_free = o_done + 2, drain = o_free + 2, l_full = drain + 1;
+    }
+    // info_readers: warps that read a tile's lookup
+    __device__ __forceinline__ void init(int info_readers) {
+        for (int i = 0; i < kPfSlots; ++i) mbar_init(op_full + i, 2), mbar_init(op_empty + i, 1);
+        for (int i = 0; i < kPfInfo; ++i) mbar_init(info_full + i, 1), mbar_init(info_empty + i, info_readers);
+        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 4), mbar_init(o_done + i, 1), mbar_init(o_free + i, 4);
         mbar_init(drain, 1);
-        *abort_flag = 0;
+        mbar_init(l_full, 4);
         mbar_init_fence();
     }
-    if (warp == 13) tmem_alloc(tmem_holder, 512);
-    // q of the rows as f16 parts in the K-major swizzled layout, a warp per row; rows that are not there are zeros
-#pragma unroll 1
-    for (int r = warp; r < nt * 128; r += kPfThreads / 32) {
+};
+
+// the rows of a CTA and what they see; false if there are none
+struct PfTile {
+    int64_t lo, first, len, r0;      // row 0's token row, its position; the sequence's tokens; the first row
+    int64_t base, b_lo, b_hi;        // first tile's first token; blocks that are read
+    int64_t all_lo, all_hi;          // positions that every row sees
+    int b, h, nrow, nj;
+    bool bad;
+    __device__ __forceinline__ bool init(const PfArgs &a, int per, unsigned int *err) {
+        // KV head fastest, then the sequence, the latest (longest) row tiles first
+        int64_t u = blockIdx.x;
+        h = (int)(u % a.c.H);
+        u /= a.c.H;
+        b = (int)(u % a.c.n_seqs);
+        const int tile = a.tiles - 1 - (int)(u / a.c.n_seqs);
+        int64_t hi;
+        a.r.of(b, lo, hi);
+        int64_t n = hi - lo;
+        if (n > a.max_q) {
+            if (threadIdx.x == 0) kv_error(err, KV_ERR_ROWS);
+            n = a.max_q;
+        }
+        len = a.c.len[b], first = len - (hi - lo);
+        const int G = a.group;
+        const int64_t rows = n * G;
+        r0 = (int64_t)tile * per;
+        if (r0 >= rows) return false;
+        bad = len < 0 || (len > 0 && ((len - 1) >> a.c.tshift) >= a.c.max_pages);
+        if (bad && threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
+        nrow = (int)min((int64_t)per, rows - r0);
+        // the ends of what the rows see do not fall from row to row (rows that see nothing come first)
+        int64_t t_lo = 0, t_hi = 0;
+        all_lo = all_hi = 0;
+        if (!bad) {
+            int64_t x0, y0, x1, y1;
+            row_range(first + r0 / G, len, a.causal, a.window, x0, y0);
+            row_range(first + (r0 + nrow - 1) / G, len, a.causal, a.window, x1, y1);
+            t_lo = x0, t_hi = max(y0, y1);
+            if (y0 > x0) all_lo = x1, all_hi = y0;
+        }
+        b_lo = t_lo / kKB, b_hi = (t_hi + kKB - 1) / kKB;
+        nj = (int)((b_hi - b_lo + 3) / 4);
+        base = b_lo * kKB;
+        return true;
+    }
+};
+
+// q of the rows as f16 parts in the K-major swizzled layout, a warp per row; rows that are not there are zeros
+template <typename T, int D>
+__device__ __forceinline__ void pf_stage_q(const PfArgs &a, const PfTile &w, uint8_t *sm, float *s_rs, int count) {
+    constexpr bool TWO = sizeof(T) == 4;
+    using C = PfCfg<D, TWO>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
+#pragma unroll 2
+    for (int r = warp; r < count; r += kPfThreads / 32) {
         float x[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-        if (r < nrow) {
-            const int64_t rr = r0 + r, i = rr / G;
-            const T *p = static_cast<const T *>(a.q) + (lo + i) * a.qt + (int64_t)(h * G + (int)(rr - i * G)) * a.qh + lane * (D / 32);
+        if (r < w.nrow) {
+            const int64_t rr = w.r0 + r, i = rr / G;
+            const T *p = static_cast<const T *>(a.q) + (w.lo + i) * a.qt + (int64_t)(w.h * G + (int)(rr - i * G)) * a.qh + lane * (D / 32);
             if constexpr (D == 128) {
                 load4(p, x);
             } else {
@@ -227,206 +266,398 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const __grid_
             *reinterpret_cast<uint32_t *>(dst + 2 * e) = p0;
             if constexpr (TWO) {
                 const float2 f = unpack_f16(p0);
-                *reinterpret_cast<uint32_t *>(dst + 2 * C::QT + 2 * e) = pack_f16(x[e] - f.x, x[e + 1] - f.y);
+                *reinterpret_cast<uint32_t *>(dst + C::TILES * C::QT + 2 * e) = pack_f16(x[e] - f.x, x[e + 1] - f.y);
             }
         }
         if (lane == 0) s_rs[r] = pow2i(ex) * a.c_log2;
     }
-    fence_proxy_async_smem();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+}
 
-    if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12) {
-            // ---------------------------------------------------------------- raw pages and scales
-            int pg = -1;
-            float dk = 0.0f, dv = 0.0f;
-            auto fetch = [&](int64_t blk0) {                   // one block a lane, from blk0 on
-                pg = -1, dk = dv = 0.0f;
-                const int64_t blk = blk0 + lane;
-                if (blk < b_hi) {
-                    pg = a.c.table[(int64_t)b * a.c.max_pages + ((blk * kKB) >> a.c.tshift)];
-                    if (pg < 0 || pg >= a.c.n_pages) {
-                        kv_error(err, KV_ERR_PAGE);
-                        pg = -1;
-                    } else {
-                        const float *sc = reinterpret_cast<const float *>(a.c.pool + pg * a.c.page_bytes + a.c.off_s);
-                        const int sb = (int)((blk * kKB) & (a.c.T - 1)) / kKB, spp = a.c.T / kKB;
-                        dk = sc[h * spp + sb];
-                        dv = sc[(a.c.H + h) * spp + sb];
-                    }
-                }
-            };
-            int issued = 0;
-            for (int i = 0; i < 2 * nj; ++i) {
-                const int j = i >> 1, half = i & 1, slot = i & 1;
-                if (half == 0 && (j & 7) == 0) fetch(b_lo + 4 * (int64_t)j);
-                const int l0 = 4 * (j & 7);
-                const int nb = (int)min((int64_t)4, b_hi - (b_lo + 4 * (int64_t)j));
-                if (i >= 2 && !warp_wait(raw_empty + slot, ((i >> 1) - 1) & 1, err, abort_flag)) break;
-                if (half == 0) {
-                    const int e = lane - l0;
-                    if (e >= 0 && e < 4) s_info[(j & 3) * 8 + e] = dk, s_info[(j & 3) * 8 + 4 + e] = dv;
-                    __threadfence_block();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(info_full + (j & 3));
-                }
-                if (lane == 0) mbar_arrive_expect_tx(raw_full + slot, nb * kKB * D);
-                __syncwarp();
-                const int e = lane - l0;
-                if (e >= 0 && e < nb) {
-                    const int64_t blk = b_lo + 4 * (int64_t)j + e;
-                    tma_load_5d(sm + C::OFF_RAW + slot * C::RAWT + e * kKB * D, &tm, 0, (int)((blk * kKB) & (a.c.T - 1)), half * a.c.H + h, a.layer,
-                                pg, raw_full + slot);
-                }
-                issued = i + 1;
+// warp 12: pages and scales of the tiles, 32 blocks at a time, one a lane
+template <bool TWO>
+__device__ __forceinline__ void pf_lookup(const PfArgs &a, const PfTile &w, PfInfo *info, const PfBars &bar, unsigned int *err, volatile int *abort) {
+    const int lane = threadIdx.x & 31;
+    int pg = -1, pg_n = -1;
+    float dk = 0.0f, dv = 0.0f, dk_n = 0.0f, dv_n = 0.0f;
+    auto fetch = [&](int64_t blk) {                            // into the next batch
+        pg_n = -1, dk_n = dv_n = 0.0f;
+        if (blk < w.b_hi) {
+            pg_n = a.c.table[(int64_t)w.b * a.c.max_pages + ((blk * kKB) >> a.c.tshift)];
+            if (pg_n < 0 || pg_n >= a.c.n_pages) {
+                kv_error(err, KV_ERR_PAGE);
+                pg_n = -1;
+            } else {
+                const float *sc = reinterpret_cast<const float *>(a.c.pool + pg_n * a.c.page_bytes + a.c.off_s);
+                const int sb = (int)((blk * kKB) & (a.c.T - 1)) / kKB, spp = a.c.T / kKB;
+                dk_n = sc[w.h * spp + sb];
+                dv_n = sc[(a.c.H + w.h) * spp + sb];
             }
-            if (*abort_flag)                                   // copies in flight land before the CTA ends
-                for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(raw_full + (i & 1), (i >> 1) & 1, err, KV_ERR_WAIT, nullptr);
-        } else if (warp == 13) {
-            // ---------------------------------------------------------------- MMA issuer
-            constexpr uint32_t id_s = idesc_f16_f32(128, kPfN);
-            constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);       // B (V) MN-major
-            const uint32_t q0 = smem_u32(sm + C::OFF_Q), op0 = smem_u32(sm + C::OFF_OP);
-            auto scores = [&](int t, int slot) {
+        }
+    };
+    fetch(w.b_lo + lane);
+    float g = 0.0f;
+    for (int j = 0; j < w.nj; ++j) {
+        if ((j & 7) == 0) {
+            pg = pg_n, dk = dk_n, dv = dv_n;
+            fetch(w.b_lo + 4 * (int64_t)(j + 8) + lane);
+        }
+        const int l0 = 4 * (j & 7), e = lane - l0;
+        float dmax = dv;
+        dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 1));
+        dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 2));
+        dmax = __shfl_sync(0xffffffffu, dmax, l0);
+        const float to = TWO ? dmax : 2.0f * dmax;
+        float gf = 1.0f;
+        if (dmax > g) {
+            gf = g / to;
+            g = to;
+        }
+        if (j >= kPfInfo && !warp_wait(bar.info_empty + j % kPfInfo, (j / kPfInfo - 1) & 1, err, abort)) break;
+        PfInfo &o = info[j % kPfInfo];
+        if (e >= 0 && e < 4) {
+            o.dk[e] = dk;
+            o.pv[e] = g > 0.0f ? dv / g : 0.0f;
+            o.page[e] = pg;
+            if (e == 0) o.gf = gf, o.g = g;
+        }
+        __threadfence_block();
+        warp_arrive(bar.info_full + j % kPfInfo, lane);
+    }
+}
+
+// Place of an operand tile in the ring's order K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
+__device__ __forceinline__ int pf_order(int j, int half, int nj) { return half ? (j == nj - 1 ? 2 * nj - 1 : 2 * j + 2) : (j == 0 ? 0 : 2 * j - 1); }
+
+// warps 8-11: codes widened into the operand ring, two warps for K, two for V, two blocks of 32 tokens each per tile.  A lane turns 8
+// bytes into one 16-byte unit, eight lanes the eight units of a 128-byte line; the next tile's bytes are in flight meanwhile.
+template <int D, bool TWO>
+__device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8_t *ops, const PfInfo *info, const PfBars &bar, unsigned int *err,
+                                         volatile int *abort) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = kKB / RPI, NV = 8 / RPI, OPT = PfCfg<D, TWO>::OPT;   // lanes per row, rows per load, loads
+    const int wi = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, half = wi >> 1, blk0 = 2 * (wi & 1), u = lane % LPR;
+    uint32_t off[NV];                                          // this lane's unit in rows 0 .. 7 of its first block
 #pragma unroll
-                for (int part = 0; part < C::PARTS; ++part)
+    for (int v = 0; v < NV; ++v) {
+        const int row = v * RPI + lane / LPR;
+        off[v] = smem_u32(ops) + (u >> 3) * 16384 + (32 * blk0 + row) * 128 + (((u & 7) ^ row) << 4);
+    }
+    const int64_t in0 = (half ? a.c.off_v : 0) + (int64_t)w.h * a.c.T * D + lane * 8;
+    const int tmask = a.c.T - 1, tok0 = (int)((w.base + 32 * blk0) & tmask);
+    uint2 raw[2][IT];
+    const uint8_t *src[2];
+    float pv[2] = {0.0f, 0.0f}, pn[2];
+    auto locate = [&](int j) -> bool {
+        if (!warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort)) return false;
+        const PfInfo &o = info[j % kPfInfo];
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                        mma_f16_warp(tmem + C::COL_S + t * 128, sw128_kmajor_desc(q0 + (part * 2 + t) * C::QT + off),
-                                     sw128_kmajor_desc(op0 + slot * C::OPT + off), id_s, part + ks > 0);
-                    }
-                mma_commit_warp(s_full + t);
-            };
-            auto output = [&](int t, int slot, int j) {
+        for (int z = 0; z < 2; ++z) {
+            const int page = o.page[blk0 + z];
+            pn[z] = o.pv[blk0 + z];
+            src[z] = page >= 0 ? a.c.pool + page * a.c.page_bytes + in0 + ((tok0 + (4 * j + z) * kKB) & tmask) * D : nullptr;
+        }
+        warp_arrive(bar.info_empty + j % kPfInfo, lane);
+        return true;
+    };
+    auto load = [&](int z, int k) { return src[z] != nullptr ? __ldg(reinterpret_cast<const uint2 *>(src[z] + k * 256)) : make_uint2(0x80808080u, 0x80808080u); };
+    if (w.nj == 0 || !locate(0)) return;
 #pragma unroll
-                for (int part = 0; part < C::PARTS; ++part)
+    for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int ks = 0; ks < kPfN / 16; ++ks)
-                        mma_f16_ts_warp(tmem + C::COL_O + t * D, tmem + C::COL_S + t * 128 + part * 64 + ks * 8,
-                                        sw128_mnmajor_desc(op0 + slot * C::OPT + ks * 2048, 16384), id_o, j + part + ks > 0);
-                mma_commit_warp(o_done + t);
-            };
-            bool ok = nj > 0;
-            if (ok) {
-                ok = warp_wait(op_full, 0, err, abort_flag);
-                tc_fence_after();
-                if (ok) {
-                    for (int t = 0; t < nt; ++t) scores(t, 0);
-                    mma_commit_warp(op_empty);
+        for (int k = 0; k < IT; ++k) raw[z][k] = load(z, k);
+    for (int j = 0; j < w.nj; ++j) {
+        pv[0] = pn[0], pv[1] = pn[1];
+        const bool more = j + 1 < w.nj;
+        if (more) {
+            if (!locate(j + 1)) break;
+        }
+        const int n = pf_order(j, half, w.nj), slot = n % kPfSlots;
+        if (n >= kPfSlots && !warp_wait(bar.op_empty + slot, (n / kPfSlots - 1) & 1, err, abort)) break;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const __half2 f = __float2half2_rn(256.0f * pv[z]);
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                uint4 x;
+                codes_f16(raw[z][k].x, x.x, x.y);
+                codes_f16(raw[z][k].y, x.z, x.w);
+                if (!TWO && half) {
+                    __half2 *h = reinterpret_cast<__half2 *>(&x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
                 }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(off[k % NV] + slot * OPT + z * 4096 + (k / NV) * 1024), "r"(x.x),
+                             "r"(x.y), "r"(x.z), "r"(x.w)
+                             : "memory");
+            }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(bar.op_full + slot, lane);
+        // all loads at once: issued one by one between the conversions, each conversion waited for the loads just issued
+        if (more) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int k = 0; k < IT; ++k) raw[z][k] = load(z, k);
+        }
+    }
+}
+
+// MMAs of one tile: scores (A = q from shared memory) and outputs (A = the weights from TMEM).  Descriptors are made once; a
+// step adds to their address fields (16-byte units).
+template <int D, bool TWO>
+struct PfMma {
+    using C = PfCfg<D, TWO>;
+    static constexpr uint32_t ID_S = idesc_f16_f32(128, kPfN), ID_O = idesc_f16_f32(128, D) | (1u << 16);     // B of O is MN-major
+    static constexpr uint32_t HI = (1024 >> 4) | (1u << 14) | (2u << 29);        // the upper words of both descriptors: stride, version, swizzle
+    uint32_t dq, dk, dv;                                       // the lower words: address and leading stride
+    __device__ __forceinline__ explicit PfMma(uint8_t *sm) {
+        dq = (uint32_t)sw128_kmajor_desc(smem_u32(sm + C::OFF_Q)), dk = (uint32_t)sw128_kmajor_desc(smem_u32(sm + C::OFF_OP));
+        dv = (uint32_t)sw128_mnmajor_desc(smem_u32(sm + C::OFF_OP), 16384);
+    }
+    static __device__ __forceinline__ uint64_t desc(uint32_t lo) {
+        uint64_t d;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(HI));
+        return d;
+    }
+    __device__ __forceinline__ void scores(uint32_t d, int t, uint32_t slot) const {
+        const uint32_t q = dq + t * (C::QT >> 4), k = dk + slot * (C::OPT >> 4);
+        uint32_t acc = 0;
+#pragma unroll 1
+        for (int i = 0; i < C::PARTS * (D / 64); ++i) {        // 64 columns of one part; the smaller part first
+            const uint32_t part = i < D / 64 ? C::PARTS - 1 : 0, hc = i & (D / 64 - 1);
+            const uint32_t qi = q + part * C::TILES * (C::QT >> 4) + hc * 1024, ki = k + hc * 1024;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mma_f16_warp(d, desc(qi + 2 * e), desc(ki + 2 * e), ID_S, acc);
+                acc = 1;
+            }
+        }
+    }
+    __device__ __forceinline__ void output(uint32_t d, uint32_t p, uint32_t slot, uint32_t more) const {
+        const uint32_t v = dv + slot * (C::OPT >> 4);
+#pragma unroll 1
+        for (int i = 0; i < 2 * C::PARTS; ++i) {               // 64 tokens of one part; the smaller part first
+            const uint32_t part = i < 2 ? C::PARTS - 1 : 0, ht = i & 1;
+            const uint32_t pi = p + (TWO ? ht * 64 + part * 32 : ht * 32), vi = v + ht * 512;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mma_f16_ts_warp(d, pi + 8 * e, desc(vi + 128 * e), ID_O, more);
+                more = 1;
+            }
+        }
+    }
+};
+
+// minus infinity over the row's scores outside positions x0 <= k < x1 (tiles that are not seen whole)
+__device__ __forceinline__ void pf_mask(uint32_t ts, int x0, int x1) {
+#pragma unroll 1
+    for (int e = 0; e < kPfN; e += 16) {
+        uint32_t s[16];
+        tmem_ld16(ts + e, s, 0);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (e + k < x0 || e + k >= x1) s[k] = 0xff800000u;
+        tmem_st16(ts + e, s);
+    }
+    tmem_st_wait();
+}
+// 64 scores of the row as they lie in TMEM
+__device__ __forceinline__ void pf_load_scores(uint32_t ts, uint32_t (&s)[2][32]) {
+    tmem_ld32(ts, s[0]);
+    tmem_ld32(ts + 32, s[1]);
+    tmem_ld_wait();
+}
+__device__ __forceinline__ float pf_max32(const uint32_t (&s)[32]) {
+    float y[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        y[z] = max3(__uint_as_float(s[8 * z]), __uint_as_float(s[8 * z + 1]), __uint_as_float(s[8 * z + 2]));
+        y[z] = max3(y[z], __uint_as_float(s[8 * z + 3]), __uint_as_float(s[8 * z + 4]));
+        y[z] = max3(y[z], __uint_as_float(s[8 * z + 5]), __uint_as_float(s[8 * z + 6]));
+        y[z] = fmaxf(y[z], __uint_as_float(s[8 * z + 7]));
+    }
+    return fmaxf(max3(y[0], y[1], y[2]), y[3]);
+}
+
+// The softmax reads a tile's scores twice from TMEM, 64 at a time: once for the maximum, once for the weights.  Holding all 128 in
+// registers left the compiler none to overlap the elements' chains with (3600 clocks a tile for f32 rows).
+__device__ __forceinline__ float pf_tile_max(uint32_t ts, const float (&kb)[4]) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        uint32_t s[2][32];
+        pf_load_scores(ts + 64 * e, s);
+        mx = max3(mx, pf_max32(s[0]) * (e ? kb[2] : kb[0]), pf_max32(s[1]) * (e ? kb[3] : kb[1]));
+    }
+    return mx;
+}
+// the weights of 32 scores: 2^(s kb + off) summed into l2 and, times pv (f32 rows), packed to f16: leading parts w, the rest v
+template <bool TWO>
+__device__ __forceinline__ void pf_weights(const uint32_t (&s)[32], float kb, uint64_t off2, float pv, uint64_t &l2, uint32_t (&w)[16],
+                                           uint32_t (&v)[16]) {
+    const uint64_t kk = f2_pack(kb, kb), pp = f2_pack(pv, pv);
+    uint64_t acc[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+        float x, y;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), kk, off2), x, y);
+        x = exp2_approx(x), y = exp2_approx(y);
+        const uint64_t p = f2_pack(x, y);
+        acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1], p);
+        if constexpr (TWO) {
+            f2_unpack(f2_mul(p, pp), x, y);
+            w[k >> 1] = pack_f16(x, y);
+            const float2 z = unpack_f16(w[k >> 1]);
+            v[k >> 1] = pack_f16(x - z.x, y - z.y);
+        } else {
+            w[k >> 1] = pack_f16(x, y);
+        }
+    }
+    l2 = f2_add(l2, f2_add(acc[0], acc[1]));
+}
+// the weights of the tile, written over the scores that have been read: f16 rows 32 columns per 64 scores from the front, f32 rows 32 of leading parts and
+// 32 of the rest in place of each 64
+template <bool TWO>
+__device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4], const float (&pb)[4], float off, uint64_t &l2) {
+    const uint64_t off2 = f2_pack(off, off);
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        uint32_t s[2][32], w[16], v[16];
+        pf_load_scores(ts + 64 * e, s);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            pf_weights<TWO>(s[z], e ? kb[2 + z] : kb[z], off2, e ? pb[2 + z] : pb[z], l2, w, v);
+            tmem_st16(ts + (TWO ? 64 : 32) * e + 16 * z, w);
+            if constexpr (TWO) tmem_st16(ts + 64 * e + 32 + 16 * z, v);
+        }
+    }
+}
+
+#define PF_PROLOGUE(T, D, INFO_READERS)                                                                                       \
+    using C = PfCfg<D, sizeof(T) == 4>;                                                                                       \
+    extern __shared__ uint8_t smem_raw[];                                                                                     \
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));             \
+    float *s_rs = reinterpret_cast<float *>(sm + C::OFF_RS);                                                                  \
+    PfInfo *info = reinterpret_cast<PfInfo *>(sm + C::OFF_INFO);                                                              \
+    const PfBars bar(reinterpret_cast<uint64_t *>(sm + C::OFF_BAR));                                                          \
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);                                                   \
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::OFF_MISC + 4);                                        \
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;                                                               \
+    grid_dep_launch();                                                                                                        \
+    grid_dep_wait();                                                                                                          \
+    PfTile w;                                                                                                                 \
+    if (!w.init(a, C::ROWS, err)) return;                                                                                     \
+    const int nt = w.nrow > 128 ? 2 : 1, nj = w.nj;                                                                           \
+    if (threadIdx.x == 0) {                                                                                                   \
+        *abort_flag = 0;                                                                                                      \
+        const_cast<PfBars &>(bar).init(INFO_READERS);                                                                         \
+    }                                                                                                                         \
+    if (warp == 13) tmem_alloc(tmem_holder, 512);                                                                             \
+    pf_stage_q<T, D>(a, w, sm, s_rs, nt * 128);                                                                               \
+    fence_proxy_async_smem();                                                                                                 \
+    __syncthreads();                                                                                                          \
+    tc_fence_after();                                                                                                         \
+    const uint32_t tmem = *tmem_holder
+
+// 16-bit rows: two row tiles per CTA
+template <typename T, int D>
+__global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsigned int *err) {
+    PF_PROLOGUE(T, D, 4 * nt + 4);
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 12) {
+            pf_lookup<false>(a, w, info, bar, err, abort_flag);
+        } else if (warp == 13) {
+            const PfMma<D, false> mma(sm);
+            const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
+            uint32_t slot = 0, ph = 0;
+            auto next = [&]() {
+                if (++slot == kPfSlots) slot = 0, ph ^= 1;
+            };
+            bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
+            if (ok) {
+                tc_fence_after();
+                mma.scores(s0, 0, 0);
+                mma_commit_warp(bar.s_full);
+                if (nt == 2) {
+                    mma.scores(s0 + 128, 1, 0);
+                    mma_commit_warp(bar.s_full + 1);
+                }
+                mma_commit_warp(bar.op_empty);
+                next();
             }
             for (int j = 0; ok && j < nj; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                if (!(ok = warp_wait(op_full + iv % NS, (iv / NS) & 1, err, abort_flag))) break;
-                for (int t = 0; t < nt; ++t) {
-                    if (!(ok = warp_wait(p_full + t, j & 1, err, abort_flag))) break;
-                    tc_fence_after();
-                    output(t, iv % NS, j);
-                    if (t == nt - 1) mma_commit_warp(op_empty + iv % NS);
-                    if (j + 1 < nj) {
-                        if (t == 0) {
-                            if (!(ok = warp_wait(op_full + ik % NS, (ik / NS) & 1, err, abort_flag))) break;
-                            tc_fence_after();
-                        }
-                        scores(t, ik % NS);
-                        if (t == nt - 1) mma_commit_warp(op_empty + ik % NS);
-                    }
+                const bool more = j + 1 < nj;
+                const uint32_t sk = slot;
+                if (more) {
+                    if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
+                    next();
                 }
+                const uint32_t sv = slot;
+                if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
+                next();
+                if (!(ok = warp_wait(bar.p_full, j & 1, err, abort_flag))) break;
+                tc_fence_after();
+                mma.output(o0, s0, sv, j > 0);
+                mma_commit_warp(bar.o_done);
+                if (more) {
+                    mma.scores(s0, 0, sk);
+                    mma_commit_warp(bar.s_full);
+                }
+                if (nt == 2) {
+                    if (!(ok = warp_wait(bar.p_full + 1, j & 1, err, abort_flag))) break;
+                    tc_fence_after();
+                    mma.output(o0 + D, s0 + 128, sv, j > 0);
+                    mma_commit_warp(bar.o_done + 1);
+                    mma_commit_warp(bar.op_empty + sv);
+                    if (more) {
+                        mma.scores(s0 + 128, 1, sk);
+                        mma_commit_warp(bar.s_full + 1);
+                    }
+                } else {
+                    mma_commit_warp(bar.op_empty + sv);
+                }
+                if (more) mma_commit_warp(bar.op_empty + sk);
             }
             if (*abort_flag) {                                 // products in flight end before the TMEM is freed
-                mma_commit_warp(drain);
-                mbar_wait(drain, 0, err, KV_ERR_WAIT, nullptr);
+                mma_commit_warp(bar.drain);
+                mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
             }
         }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // -------------------------------------------------------------------- widen codes: a thread per token
-        const int row = threadIdx.x - 256;
-        for (int i = 0; i < 2 * nj; ++i) {
-            const int rs = i & 1, slot = i % NS;
-            if (!mbar_wait_prompt(raw_full + rs, (i >> 1) & 1, err, KV_ERR_WAIT, abort_flag)) break;
-            if (i >= NS && !mbar_wait_prompt(op_empty + slot, (i / NS - 1) & 1, err, KV_ERR_WAIT, abort_flag)) break;
-            const uint8_t *src = sm + C::OFF_RAW + rs * C::RAWT + row * D;
-            uint8_t *dst = sm + C::OFF_OP + slot * C::OPT + row * 128;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const int pc = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-                const uint4 w = *reinterpret_cast<const uint4 *>(src + pc * 16);
-                uint4 x, y;
-                codes_f16(w.x, x.x, x.y);
-                codes_f16(w.y, x.z, x.w);
-                codes_f16(w.z, y.x, y.y);
-                codes_f16(w.w, y.z, y.w);
-                uint8_t *d = dst + (c >> 2) * 16384;
-                const int unit = 2 * (c & 3);
-                *reinterpret_cast<uint4 *>(d + ((unit ^ (row & 7)) << 4)) = x;
-                *reinterpret_cast<uint4 *>(d + (((unit + 1) ^ (row & 7)) << 4)) = y;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(op_full + slot);
-            mbar_arrive(raw_empty + rs);
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        pf_widen<D, false>(a, w, sm + C::OFF_OP, info, bar, err, abort_flag);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        // -------------------------------------------------------------------- softmax: a thread per row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int t = warp >> 2, r = threadIdx.x;
         if (t < nt) {
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t ts = tmem + C::COL_S + t * 128 + lanes, to = tmem + C::COL_O + t * D + lanes;
             int v0 = 0, v1 = 0;                                 // what the row sees, from the first tile's start
-            if (r < nrow && !bad) {
+            if (r < w.nrow && !w.bad) {
                 int64_t x, y;
-                row_range(first + (r0 + r) / G, len, a.causal, a.window, x, y);
-                v0 = (int)max(x - base, (int64_t)0), v1 = (int)max(y - base, (int64_t)0);
+                row_range(w.first + (w.r0 + r) / a.group, w.len, a.causal, a.window, x, y);
+                v0 = (int)max(x - w.base, (int64_t)0), v1 = (int)max(y - w.base, (int64_t)0);
             }
-            const int i_lo = (int)max(all_lo - base, (int64_t)INT_MIN), i_hi = (int)max(all_hi - base, (int64_t)INT_MIN);
+            const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
             const float rs = s_rs[r];
-            float m = -INFINITY, g = 0.0f;
+            float m = -INFINITY;
             uint64_t l2 = f2_pack(0.0f, 0.0f);
             bool ok = true;
             for (int j = 0; j < nj; ++j) {
-                if (!(ok = warp_wait(info_full + (j & 3), (j >> 2) & 1, err, abort_flag))) break;
-                float kb[4], dv[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
-                    kb[e] = fmaxf(rs * s_info[(j & 3) * 8 + e], 0x1p-120f);
-                    dv[e] = s_info[(j & 3) * 8 + 4 + e];
-                }
-                const float dmax = fmaxf(fmaxf(dv[0], dv[1]), fmaxf(dv[2], dv[3]));
-                float gf = 1.0f;
-                if (dmax > g) {
-                    gf = g / (2.0f * dmax);
-                    g = 2.0f * dmax;
-                }
-                const float ig = g > 0.0f ? 1.0f / g : 0.0f;
-                if (!(ok = warp_wait(s_full + t, j & 1, err, abort_flag))) break;
+                if (!(ok = warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag))) break;
+                const PfInfo &o = info[j % kPfInfo];
+                const float4 dk = *reinterpret_cast<const float4 *>(o.dk);
+                const float gf = o.gf;
+                // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
+                const float kb[4] = {fmaxf(rs * dk.x, 0x1p-120f), fmaxf(rs * dk.y, 0x1p-120f), fmaxf(rs * dk.z, 0x1p-120f), fmaxf(rs * dk.w, 0x1p-120f)};
+                warp_arrive(bar.info_empty + j % kPfInfo, lane);
+                if (!(ok = warp_wait(bar.s_full + t, j & 1, err, abort_flag))) break;
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tmem_ld32(ts + 32 * e, s[e]);
-                tmem_ld_wait();
                 const int t0 = j * kPfN;
-                if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) {
-                    const int x0 = v0 - t0, x1 = v1 - t0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * e + k < x0 || 32 * e + k >= x1) s[e][k] = 0xff800000u;
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y = __uint_as_float(s[e][0]);
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) y = fmaxf(y, __uint_as_float(s[e][k]));
-                    mx = fmaxf(mx, y * kb[e]);
-                }
+                if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) pf_mask(ts, v0 - t0, v1 - t0);
+                const float mx = pf_tile_max(ts, kb);
                 const bool grow = mx > m + kTau || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, grow || gf != 1.0f)) {
                     const float mn = grow ? mx : m;
@@ -434,88 +665,53 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const __grid_
                     m = mn;
                     l2 = f2_mul(l2, f2_pack(f, f));
                     if (j > 0) {
-                        if (!(ok = warp_wait(o_done + t, (j - 1) & 1, err, abort_flag))) break;
+                        if (!(ok = warp_wait(bar.o_done + t, (j - 1) & 1, err, abort_flag))) break;
                         tc_fence_after();
                         const uint64_t ff = f2_pack(f * gf, f * gf);
-#pragma unroll
+#pragma unroll 1
                         for (int e = 0; e < D / 16; ++e) {
-                            uint32_t o[16];
-                            tmem_ld16(to + 16 * e, o, 0);
+                            uint32_t x[16];
+                            tmem_ld16(to + 16 * e, x, 0);
                             tmem_ld_wait();
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
-                                float x, y;
-                                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), ff), x, y);
-                                o[k] = __float_as_uint(x), o[k + 1] = __float_as_uint(y);
+                                float y, z;
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff), y, z);
+                                x[k] = __float_as_uint(y), x[k + 1] = __float_as_uint(z);
                             }
-                            tmem_st16(to + 16 * e, o);
+                            tmem_st16(to + 16 * e, x);
                         }
                     }
                 }
-                const float off = kPfShift - (m == -INFINITY ? 0.0f : m);
-                const uint64_t off2 = f2_pack(off, off);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint64_t kk = f2_pack(kb[e], kb[e]);
-                    const float pv = dv[e] * ig;
-                    const uint64_t pp = f2_pack(pv, pv);
-                    uint64_t acc = f2_pack(0.0f, 0.0f);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float x, y;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e][k]), __uint_as_float(s[e][k + 1])), kk, off2), x, y);
-                        const uint64_t p = f2_pack(exp2_approx(x), exp2_approx(y));
-                        acc = f2_add(acc, p);
-                        f2_unpack(f2_mul(p, pp), x, y);
-                        const uint32_t w = pack_f16(x, y);
-                        s[e][k] = w;                           // the parts take the places of the two scores
-                        if constexpr (TWO) {
-                            const float2 z = unpack_f16(w);
-                            s[e][k + 1] = pack_f16(x - z.x, y - z.y);
-                        }
-                    }
-                    l2 = f2_add(l2, acc);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = s[e][2 * k], w[16 + k] = s[e + 1][2 * k];
-                    tmem_st32(ts + 16 * e, w);
-                    if constexpr (TWO) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = s[e][2 * k + 1], w[16 + k] = s[e + 1][2 * k + 1];
-                        tmem_st32(ts + 64 + 16 * e, w);
-                    }
-                }
+                pf_tile_weights<false>(ts, kb, kb, kPfShift - (m == -INFINITY ? 0.0f : m), l2);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(p_full + t);
+                warp_arrive(bar.p_full + t, lane);
             }
             // ---------------------------------------------------------------- the rows' outputs
-            if (nj > 0 && ok) ok = warp_wait(o_done + t, (nj - 1) & 1, err, abort_flag);
+            if (nj > 0 && ok) ok = warp_wait(bar.o_done + t, (nj - 1) & 1, err, abort_flag);
             tc_fence_after();
             float l, l1;
             f2_unpack(l2, l, l1);
             l += l1;
-            const float inv = l == 0.0f ? 0.0f : g / l;
-            const int64_t i = (r0 + r) / G;
-            const int gq = (int)(r0 + r - i * G);
-            T *dst = static_cast<T *>(a.out) + (lo + i) * a.ot + (int64_t)(h * G + gq) * a.oh;
-#pragma unroll
+            const float inv = l == 0.0f ? 0.0f : info[(nj + kPfInfo - 1) % kPfInfo].g * (1.0f / 256.0f) / l;
+            const int64_t i = (w.r0 + r) / a.group;
+            const int gq = (int)(w.r0 + r - i * a.group);
+            T *dst = static_cast<T *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh;
+#pragma unroll 1
             for (int e = 0; e < D / 32; ++e) {
-                uint32_t o[32];
+                uint32_t x[32];
                 if (nj > 0) {
-                    tmem_ld32(to + 32 * e, o);
+                    tmem_ld32(to + 32 * e, x);
                     tmem_ld_wait();
                 }
-                if (r < nrow) {
+                if (r < w.nrow) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        float x[4];
+                        float y[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) x[z] = nj > 0 && l != 0.0f ? __uint_as_float(o[k + z]) * inv : 0.0f;
-                        store4(dst + 32 * e + k, x);
+                        for (int z = 0; z < 4; ++z) y[z] = nj > 0 && l != 0.0f ? __uint_as_float(x[k + z]) * inv : 0.0f;
+                        store4(dst + 32 * e + k, y);
                     }
                 }
             }
@@ -529,34 +725,183 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const __grid_
     }
 }
 
-}  // namespace
-
-template <typename T, int D>
-int kv_prefill_t(const CUtensorMap &tm, const PfArgs &a, unsigned int *err, cudaStream_t s) {
-    using C = PfCfg<D, sizeof(T) == 4>;
-    const int slot = kAttrSlotKv + 8 + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128);
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(&kv_prefill_kernel<T, D>), C::SMEM, slot);
-    if (rc != MQ_OK) return rc;
-    return cuda_error(launch_pdl(kv_prefill_kernel<T, D>, dim3((unsigned)((int64_t)a.c.H * a.c.n_seqs * a.tiles)), dim3(kPfThreads), C::SMEM, s, tm,
-                                 a, err),
-                      "mqkv_attention (tiles) launch");
+// f32 rows: one row tile per CTA, every tile's P V summed in registers
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, unsigned int *err) {
+    PF_PROLOGUE(float, D, 4 + 4);
+    float *s_f = s_rs + 128;                                   // [2][128] factors of what was summed before
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 12) {
+            pf_lookup<true>(a, w, info, bar, err, abort_flag);
+        } else if (warp == 13) {
+            const PfMma<D, true> mma(sm);
+            const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
+            uint32_t slot = 0, ph = 0;
+            auto next = [&]() {
+                if (++slot == kPfSlots) slot = 0, ph ^= 1;
+            };
+            bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
+            if (ok) {
+                tc_fence_after();
+                mma.scores(s0, 0, 0);
+                mma_commit_warp(bar.s_full);
+                mma_commit_warp(bar.op_empty);
+                next();
+            }
+            for (int j = 0; ok && j < nj; ++j) {
+                const uint32_t at = j & 1, nx = at ^ 1;
+                if (j + 1 < nj) {                              // P(j - 1) in this buffer was read by products issued before
+                    if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
+                    tc_fence_after();
+                    mma.scores(s0 + nx * 128, 0, slot);
+                    mma_commit_warp(bar.s_full + nx);
+                    mma_commit_warp(bar.op_empty + slot);
+                    next();
+                }
+                if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
+                if (j >= 2 && !(ok = warp_wait(bar.o_free + at, ((j >> 1) - 1) & 1, err, abort_flag))) break;
+                if (!(ok = warp_wait(bar.p_full + at, (j >> 1) & 1, err, abort_flag))) break;
+                tc_fence_after();
+                mma.output(o0 + at * D, s0 + at * 128, slot, 0);
+                mma_commit_warp(bar.o_done + at);
+                mma_commit_warp(bar.op_empty + slot);
+                next();
+            }
+            if (*abort_flag) {                                 // products in flight end before the TMEM is freed
+                mma_commit_warp(bar.drain);
+                mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
+            }
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        pf_widen<D, true>(a, w, sm + C::OFF_OP, info, bar, err, abort_flag);
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const int r = threadIdx.x;
+        const uint32_t ts = tmem + C::COL_S + ((uint32_t)(32 * warp) << 16);
+        int v0 = 0, v1 = 0;                                    // what the row sees, from the first tile's start
+        if (r < w.nrow && !w.bad) {
+            int64_t x, y;
+            row_range(w.first + (w.r0 + r) / a.group, w.len, a.causal, a.window, x, y);
+            v0 = (int)max(x - w.base, (int64_t)0), v1 = (int)max(y - w.base, (int64_t)0);
+        }
+        const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
+        const float rs = s_rs[r];
+        float m = -INFINITY, g = 0.0f;
+        uint64_t l2 = f2_pack(0.0f, 0.0f);
+        for (int j = 0; j < nj; ++j) {
+            const int at = j & 1;
+            if (!warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag)) break;
+            const PfInfo &o = info[j % kPfInfo];
+            const float4 dk = *reinterpret_cast<const float4 *>(o.dk), pv = *reinterpret_cast<const float4 *>(o.pv);
+            const float gf = o.gf;
+            g = o.g;
+            // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
+            const float kb[4] = {fmaxf(rs * dk.x, 0x1p-120f), fmaxf(rs * dk.y, 0x1p-120f), fmaxf(rs * dk.z, 0x1p-120f), fmaxf(rs * dk.w, 0x1p-120f)};
+            const float pb[4] = {pv.x, pv.y, pv.z, pv.w};
+            warp_arrive(bar.info_empty + j % kPfInfo, lane);
+            if (!warp_wait(bar.s_full + at, (j >> 1) & 1, err, abort_flag)) break;
+            tc_fence_after();
+            const int t0 = j * kPfN;
+            if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) pf_mask(ts + at * 128, v0 - t0, v1 - t0);
+            const float mx = pf_tile_max(ts + at * 128, kb);
+            const float mn = fmaxf(m, mx), mb = mn == -INFINITY ? 0.0f : mn;
+            const float f = exp2_approx(m - mb);
+            m = mn;
+            l2 = f2_mul(l2, f2_pack(f, f));
+            // the factor's place is free once tile j - 2 has been summed
+            if (j >= 2 && !warp_wait(bar.o_free + at, ((j >> 1) - 1) & 1, err, abort_flag)) break;
+            s_f[at * 128 + r] = f * gf;
+            pf_tile_weights<true>(ts + at * 128, kb, pb, kPShift - mb, l2);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(bar.p_full + at, lane);
+        }
+        float l, l1;
+        f2_unpack(l2, l, l1);
+        l += l1;
+        s_rs[r] = l == 0.0f ? 0.0f : g / l;                     // (this thread alone read the row's scale)
+        warp_arrive(bar.l_full, lane);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        const int r = threadIdx.x - 128;
+        const uint32_t to = tmem + C::COL_O + ((uint32_t)(32 * (warp - 4)) << 16);
+        uint64_t acc[D / 2];
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) acc[k] = f2_pack(0.0f, 0.0f);
+        for (int j = 0; j < nj; ++j) {
+            const int at = j & 1;
+            if (!warp_wait(bar.p_full + at, (j >> 1) & 1, err, abort_flag)) break;     // the factors
+            const float f = s_f[at * 128 + r];
+            const uint64_t ff = f2_pack(f, f);
+            if (!warp_wait(bar.o_done + at, (j >> 1) & 1, err, abort_flag)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                uint32_t x[32];
+                tmem_ld32(to + at * D + 32 * e, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                    acc[16 * e + (k >> 1)] = f2_fma(acc[16 * e + (k >> 1)], ff, f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+            }
+            tc_fence_before();
+            warp_arrive(bar.o_free + at, lane);
+        }
+        warp_wait(bar.l_full, 0, err, abort_flag);
+        const float inv = s_rs[r];
+        if (r < w.nrow) {
+            const int64_t i = (w.r0 + r) / a.group;
+            const int gq = (int)(w.r0 + r - i * a.group);
+            float *dst = static_cast<float *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh;
+#pragma unroll
+            for (int k = 0; k < D; k += 4) {
+                float y[4];
+                f2_unpack(acc[k / 2], y[0], y[1]);
+                f2_unpack(acc[k / 2 + 1], y[2], y[3]);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) y[z] *= inv;
+                store4(dst + k, y);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
-int kv_launch_prefill(const CUtensorMap &tm, int layer, const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err,
-                      cudaStream_t s) {
+template <typename T, int D>
+int prefill_t(PfArgs &a, unsigned int *err, cudaStream_t s) {
+    using C = PfCfg<D, sizeof(T) == 4>;
+    const int slot = kAttrSlotKv + 8 + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128);
+    void (*fn)(PfArgs, unsigned int *);
+    if constexpr (sizeof(T) == 4) fn = kv_tiles_f32_kernel<D>;
+    else fn = kv_tiles_kernel<T, D>;
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), C::SMEM, slot);
+    if (rc != MQ_OK) return rc;
+    a.tiles = (int)((a.max_q * a.group + C::ROWS - 1) / C::ROWS);
+    const int64_t grid = (int64_t)a.c.H * a.c.n_seqs * a.tiles;
+    return cuda_error(launch_pdl(fn, dim3((unsigned)grid), dim3(kPfThreads), C::SMEM, s, a, err), "mqkv_attention (tiles) launch");
+}
+
+}  // namespace
+
+int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err, cudaStream_t s) {
     PfArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
-    a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = p.max_q, a.window = p.window;
-    a.tiles = (int)((p.max_q * p.group + kPfRows - 1) / kPfRows);
+    a.group = p.group, a.causal = p.causal, a.max_q = p.max_q, a.window = p.window;
     a.c_log2 = fabsf(p.scale) * kLog2e;
     a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
     if (c.D == 128)
-        return p.dtype == MQKV_F32   ? kv_prefill_t<float, 128>(tm, a, err, s)
-               : p.dtype == MQKV_F16 ? kv_prefill_t<__half, 128>(tm, a, err, s)
-                                     : kv_prefill_t<__nv_bfloat16, 128>(tm, a, err, s);
-    return p.dtype == MQKV_F32   ? kv_prefill_t<float, 64>(tm, a, err, s)
-           : p.dtype == MQKV_F16 ? kv_prefill_t<__half, 64>(tm, a, err, s)
-                                 : kv_prefill_t<__nv_bfloat16, 64>(tm, a, err, s);
+        return p.dtype == MQKV_F32   ? prefill_t<float, 128>(a, err, s)
+               : p.dtype == MQKV_F16 ? prefill_t<__half, 128>(a, err, s)
+                                     : prefill_t<__nv_bfloat16, 128>(a, err, s);
+    return p.dtype == MQKV_F32   ? prefill_t<float, 64>(a, err, s)
+           : p.dtype == MQKV_F16 ? prefill_t<__half, 64>(a, err, s)
+                                 : prefill_t<__nv_bfloat16, 64>(a, err, s);
 }
 
 }  // namespace mq
