@@ -62,7 +62,7 @@ int set_error(int code, const char *fmt, ...) {
 
 namespace {
 int g_sm_count[kMaxDevices] = {0};
-constexpr int kAttrSlots = kAttrSlotKv + 32;        // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM; cache
+constexpr int kAttrSlots = kAttrSlotKv + 32;       // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM; cache
 bool g_attr_done[kMaxDevices][kAttrSlots] = {};
 }  // namespace
 

@@ -21,7 +21,8 @@
 namespace mq {
 namespace {
 
-constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps, kAtRing = 3;
+constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
+constexpr int kAtSmemSeqs = 256;                // sequences whose plan fits the CTA's shared memory beside two CTAs' rings
 
 struct AtArgs {
     KvView c;
@@ -29,10 +30,31 @@ struct AtArgs {
     const void *q;
     void *out;
     int64_t qt, qh, ot, oh;
-    int32_t group, causal, tiles, nsplit, layer;
-    int64_t max_q, window;
-    float c_log2;               // scale * log2(e)
-    float *part;                // [row][split][D + 2]: o, m, l
+    int32_t group, causal, layer, workers;
+    int32_t max_q;
+    int64_t window;
+    float c_log2, sign;         // |scale| * log2(e), the sign of scale (it goes into q: score factors are not negative)
+    uint32_t *total;            // units of the call, for the join
+    uint32_t *prefix;           // [n_seqs + 1]: units before each sequence
+    struct AtJoin *join;        // [workers]
+    float *part;                // [worker][2][R rows][D + 4]: o, m, l
+};
+
+// a row pass that began with a worker and ends with another: its partials are number 1 of workers first .. last - 1 and number 0 of the last
+struct AtJoin {
+    int32_t nrow, last, h, r0;      // nrow 0: none
+    int64_t tok;
+};
+
+// equal shares of the units: the first rem of them have one more
+struct AtShare {
+    uint32_t base, rem;
+    __device__ __forceinline__ AtShare(uint32_t total, uint32_t n) : base(total / n), rem(total - total / n * n) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * base + min(c, rem); }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+        const uint32_t big = (base + 1) * rem;
+        return u < big ? u / (base + 1) : rem + (u - big) / base;
+    }
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -41,279 +63,443 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// MT: 16-row MMA tiles that share the codes
+template <typename T, int D, int MT>
 struct AtCfg {
-    static constexpr int BLK = kKB * D;                       // bytes of one 32-token block of K or V
-    static constexpr int SLOT = 2 * BLK;
-    static constexpr int OFF_BAR = kAtWarps * kAtRing * SLOT;
-    static constexpr int SMEM = OFF_BAR + kAtWarps * kAtRing * 8 + 1024;
-    static constexpr int LD = D + 4;                          // merge buffer row (floats)
-    static_assert(kAtWarps * 16 * LD * 4 + kAtWarps * 16 * 8 <= OFF_BAR, "the merge buffer reuses the ring");
+    static constexpr bool TWO = sizeof(T) == 4;
+    static constexpr int RT = TWO ? 8 : 16, R = RT * MT;      // rows of an MMA tile, of a pass
+    static constexpr int RING = MT == 1 || D == 64 ? 3 : 2;   // blocks in flight per warp
+    static constexpr int BLK = kKB * D, SLOT = 2 * BLK;       // bytes of one 32-token block of K or V
+    static constexpr bool QS = MT > 1 && D == 128;            // q fragments in shared memory: the registers hold 2 x 64 sums
+    static constexpr int LD = D + 4;                          // floats of a row of sums
+    static constexpr int OFF_Q = kAtWarps * RING * SLOT;
+    static constexpr int OFF_BAR = OFF_Q + (QS ? kAtWarps * MT * (D / 16) * 512 : 0);
+    static constexpr int OFF_PLAN = OFF_BAR + kAtWarps * RING * 8 + 64;
+    static constexpr int SMEM = OFF_PLAN + 1008;              // then the plan
 };
 
-// One CTA: (split, KV head, row tile, sequence).
-template <typename T, int D>
-__global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_constant__ CUtensorMap tm, AtArgs a, unsigned int *err) {
-    using C = AtCfg<D>;
-    constexpr bool TWO = sizeof(T) == 4;                      // two f16 parts per operand
-    constexpr int R = TWO ? 8 : 16;                           // rows of a tile
-    constexpr int NT = D / 8;                                 // n-tiles of the output
-    constexpr int KS = D / 16;                                // k-steps of the scores
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
-    uint8_t *ring = sm + warp * kAtRing * C::SLOT;
-    uint64_t *bar = bars + warp * kAtRing;
-    if (lane == 0) {
-        for (int i = 0; i < kAtRing; ++i) mbar_init(bar + i, 1);
-        mbar_init_fence();
+// what the call's sequences have to do: R-row passes over the blocks that any of a sequence's rows sees (one block where none
+// sees anything, so that its rows are written)
+struct AtSeq {
+    int64_t lo;                                 // first token row
+    int32_t n, len, tiles;                      // new tokens (max_q at most), cached ones, passes
+    uint32_t b_lo, nb;                          // first block, blocks
+    int64_t first;                              // position of row 0's token
+    __device__ __forceinline__ void init(const AtArgs &a, int b, int R, unsigned int *err, bool tell) {
+        int64_t hi;
+        a.r.of(b, lo, hi);
+        n = (int)min(hi - lo, (int64_t)a.max_q), len = a.c.len[b], first = len - (hi - lo);
+        if (tell && hi - lo > a.max_q) kv_error(err, KV_ERR_ROWS);
+        tiles = (n * a.group + R - 1) / R;
+        if (len < 0 || (len > 0 && ((len - 1) >> a.c.tshift) >= a.c.max_pages)) {
+            if (tell && n > 0) kv_error(err, KV_ERR_LEN);
+            len = 0;
+        }
+        int64_t x0, y0, x1, y1;
+        row_range(first, len, a.causal, a.window, x0, y0);
+        row_range(first + n - 1, len, a.causal, a.window, x1, y1);
+        b_lo = (uint32_t)((y0 > x0 ? x0 : 0) / kKB);
+        nb = max((uint32_t)((max(y0, y1) + kKB - 1) / kKB) - b_lo, 1u);
     }
-    __syncwarp();
+    __device__ __forceinline__ uint32_t units(int H) const { return (uint32_t)(tiles * H) * nb; }
+};
+
+// units before each sequence into prefix[0 .. n_seqs], by one CTA of THREADS threads.  (Their sum stays below 2^32: the host has
+// checked it for max_kv, and a table row holds no more tokens than its pages.)
+template <int THREADS>
+__device__ __forceinline__ void at_plan(const AtArgs &a, int R, uint32_t *prefix, uint32_t *s_warp, unsigned int *err, bool tell) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t before = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.c.n_seqs; base += THREADS) {
+        const int b = base + threadIdx.x;
+        uint32_t v = 0;
+        if (b < a.c.n_seqs) {
+            AtSeq q;
+            q.init(a, b, R, err, tell);
+            v = q.units(a.c.H);
+        }
+        uint32_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        uint32_t w = 0, all = 0;
+#pragma unroll 4
+        for (int i = 0; i < THREADS / 32; ++i) {
+            if (i < warp) w += s_warp[i];
+            all += s_warp[i];
+        }
+        if (b < a.c.n_seqs) prefix[b] = before + w + x - v;
+        before += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) prefix[a.c.n_seqs] = before;
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(1024) kv_attn_plan_kernel(AtArgs a, int R, unsigned int *err) {
+    __shared__ uint32_t s_warp[32];
     grid_dep_launch();
     grid_dep_wait();
+    at_plan<1024>(a, R, a.prefix, s_warp, err, true);
+    if (threadIdx.x == 0) *a.total = a.prefix[a.c.n_seqs];
+}
 
-    int64_t u = blockIdx.x;
-    const int split = (int)(u % a.nsplit);
-    u /= a.nsplit;
-    const int h = (int)(u % a.c.H);
-    u /= a.c.H;
-    const int tile = (int)(u % a.tiles), b = (int)(u / a.tiles);
-    int64_t lo, hi;
-    a.r.of(b, lo, hi);
-    int64_t n = hi - lo;
-    if (n > a.max_q) {
-        if (threadIdx.x == 0) kv_error(err, KV_ERR_ROWS);
-        n = a.max_q;
+// the last sequence that begins at or before unit u (one with units)
+__device__ __forceinline__ int at_find(const uint32_t *prefix, int n_seqs, uint32_t u) {
+    int lo = 0, hi = n_seqs - 1;
+#pragma unroll 1
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
     }
-    const int64_t len = a.c.len[b], first = len - (hi - lo);  // position of row lo
-    const int G = a.group;
-    const int64_t rows = n * G, r0 = (int64_t)tile * R;
-    if (r0 >= rows) return;
-    const bool bad = len < 0 || (len > 0 && ((len - 1) >> a.c.tshift) >= a.c.max_pages);
-    if (bad && threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
-    const int nrow = (int)min((int64_t)R, rows - r0);
+    return lo;
+}
 
-    // what the tile sees, and what each of this thread's rows does
-    int64_t t_lo = INT64_MAX, t_hi = 0, all_lo = 0, all_hi = INT64_MAX;
-    if (!bad) {
-        const int64_t i0 = r0 / G, i1 = (r0 + nrow - 1) / G;
-        int64_t x, y;
-        for (int64_t i = i0; i <= i1; ++i) {
-            row_range(first + i, len, a.causal, a.window, x, y);
-            if (y > x) t_lo = min(t_lo, x), t_hi = max(t_hi, y);
-            all_lo = max(all_lo, x), all_hi = min(all_hi, y);
+// Work is split by units of one block of 32 tokens for one KV head and row pass.  Every warp of the grid (a worker) takes an equal,
+// contiguous share of all units, whatever the lengths, and walks it through its own ring of K / V blocks; loads run ahead over the ends
+// of row passes and no warp waits for another.  Where a row pass ends, or the share does, the sums leave: divided where the pass lies
+// in the share whole, else as a partial for the join kernel.  (Shares of whole CTAs, their warps joined in shared memory at the end of
+// each pass, left fewer partials but made every end of a pass cost 5 us: 77 us against 49 for a ragged batch of 48 sequences.)
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_constant__ CUtensorMap tm, AtArgs a, unsigned int *err) {
+    using C = AtCfg<T, D, MT>;
+    constexpr bool TWO = C::TWO;
+    constexpr int NT = D / 8, KS = D / 16, RING = C::RING;    // n-tiles of the output, k-steps of the scores
+    constexpr int RT = TWO ? 1 : 2;                           // rows of this thread in an MMA tile: g (and g + 8)
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
+    uint8_t *ring = sm + warp * RING * C::SLOT;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR) + warp * RING;
+    if (lane == 0) {
+        for (int i = 0; i < RING; ++i) mbar_init(bar + i, 1);
+        mbar_init_fence();
+        if (warp == 0) prefetch_tmap(&tm);
+    }
+    grid_dep_launch();
+    grid_dep_wait();
+    const uint32_t *prefix = a.prefix;
+    if (a.c.n_seqs <= kAtSmemSeqs) {
+        uint32_t *mine = reinterpret_cast<uint32_t *>(sm + C::OFF_PLAN);
+        at_plan<kAtThreads>(a, C::R, mine, reinterpret_cast<uint32_t *>(sm + C::OFF_BAR + kAtWarps * RING * 8), err, blockIdx.x == 0);
+        prefix = mine;
+        if (blockIdx.x == 0) {                                // for the join
+            for (int i = threadIdx.x; i <= a.c.n_seqs; i += kAtThreads) a.prefix[i] = mine[i];
+            if (threadIdx.x == 0) *a.total = mine[a.c.n_seqs];
         }
     }
-    if (t_hi == 0) t_lo = 0;
-    const int64_t b_lo = t_lo / kKB, b_hi = (t_hi + kKB - 1) / kKB, nb = b_hi - b_lo;
-    const int64_t s_lo = b_lo + nb * split / a.nsplit, s_hi = b_lo + nb * (split + 1) / a.nsplit;
+    __syncthreads();
+    const uint32_t total = prefix[a.c.n_seqs], workers = min((uint32_t)a.workers, total), worker = blockIdx.x * kAtWarps + warp;
+    if (worker >= workers) return;                            // every share has a unit at least
+    const AtShare shares(total, workers);
+    const uint32_t u0 = shares.begin(worker);
+    const int H = a.c.H, G = a.group, mine = (int)(shares.begin(worker + 1) - u0);
 
-    // rows of this thread: g and (one part) g + 8
-    constexpr int RT = TWO ? 1 : 2;
-    int64_t v_lo[RT], v_hi[RT];
-    uint32_t qa[KS][4];
-    float rs[RT];
-#pragma unroll
-    for (int e = 0; e < RT; ++e) {
-        const int rr = g + 8 * e;
-        v_lo[e] = v_hi[e] = 0;
-        rs[e] = 0.0f;
-        float x[D / 4];
-        const bool in = rr < nrow;
-        if (in) {
-            const int64_t r = r0 + rr, i = r / G;
-            const int gq = (int)(r - i * G);
-            row_range(first + i, len, a.causal, a.window, v_lo[e], v_hi[e]);
-            const T *p = static_cast<const T *>(a.q) + (lo + i) * a.qt + (int64_t)(h * G + gq) * a.qh + cc * (D / 4);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) load4(p + 4 * j, x + 4 * j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < D / 4; ++j) x[j] = 0.0f;
-        }
-        float amax = 0.0f;
-        bool fin = true;
-#pragma unroll
-        for (int j = 0; j < D / 4; ++j) {
-            amax = fmaxf(amax, fabsf(x[j]));
-            fin = fin && fabsf(x[j]) <= 3.402823466e38f;
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        fin = (__ballot_sync(0xffffffffu, fin) >> (lane & ~3) & 15u) == 15u;
-        const int ex = fin ? row_exponent(amax) : 0;
-        const float down = pow2i(-ex);
-        rs[e] = fin ? pow2i(ex) * a.c_log2 : __int_as_float(0x7fc00000);    // a row with a NaN or an infinity becomes NaN
-        // k order of the products: k-step ks = 4 hh + s takes the values 16 (2 cc + hh) + 4 s ..+3 (D = 128)
-        // or 16 cc + 4 s ..+3 (D = 64) of the row: the 16 bytes that one shared-memory load of K gives
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const float y0 = fin ? x[4 * ks] * down : 0.0f, y1 = fin ? x[4 * ks + 1] * down : 0.0f;
-            const float y2 = fin ? x[4 * ks + 2] * down : 0.0f, y3 = fin ? x[4 * ks + 3] * down : 0.0f;
-            const uint32_t p0 = pack_f16(y0, y1), p1 = pack_f16(y2, y3);
-            qa[ks][e] = p0;
-            qa[ks][2 + e] = p1;
-            if constexpr (TWO) {
-                const float2 h0 = unpack_f16(p0), h1 = unpack_f16(p1);
-                qa[ks][1] = pack_f16(y0 - h0.x, y1 - h0.y);
-                qa[ks][3] = pack_f16(y2 - h1.x, y3 - h1.y);
+    // 32 of the warp's units at a time, one a lane: page, scales, where in the page and which head
+    int pg = -1, at = 0;
+    float dk = 0.0f, dv = 0.0f;
+    auto fetch = [&](int k) {
+        pg = -1, at = 0, dk = dv = 0.0f;
+        if (k + lane < mine) {
+            const uint32_t u = u0 + k + lane;
+            const int b = at_find(prefix, a.c.n_seqs, u);
+            AtSeq q;
+            q.init(a, b, C::R, err, false);
+            const uint32_t r = u - prefix[b], it = r / q.nb, blk = q.b_lo + (r - it * q.nb);
+            const int h = (int)(it % H), spp = a.c.T / kKB, sb = (int)blk & (spp - 1);
+            at = h << 3 | sb;
+            if ((int64_t)blk * kKB < q.len) {
+                pg = a.c.table[(int64_t)b * a.c.max_pages + (blk >> (a.c.tshift - 5))];
+                if (pg < 0 || pg >= a.c.n_pages) {
+                    kv_error(err, KV_ERR_PAGE);
+                    pg = -1;
+                } else {
+                    const float *sc = reinterpret_cast<const float *>(a.c.pool + pg * a.c.page_bytes + a.c.off_s);
+                    dk = sc[h * spp + sb];
+                    dv = sc[(H + h) * spp + sb];
+                }
             }
         }
-    }
+    };
+    auto issue = [&](int k, int slot) {                       // the warp's unit k into its ring (a page of -1 reads as zeros)
+        const int page = __shfl_sync(0xffffffffu, pg, k & 31), w = __shfl_sync(0xffffffffu, at, k & 31);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar + slot, C::SLOT);
+            tma_load_5d(ring + slot * C::SLOT, &tm, 0, (w & 7) * kKB, w >> 3, a.layer, page, bar + slot);
+            tma_load_5d(ring + slot * C::SLOT + C::BLK, &tm, 0, (w & 7) * kKB, H + (w >> 3), a.layer, page, bar + slot);
+        }
+    };
+    fetch(0);
+    for (int k = 0; k < RING && k < mine; ++k) issue(k, k);
+    float dk0 = dk, dv0 = dv;                                 // scales of the batch that is being consumed
 
-    float o[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    float m[RT], l[RT];
-#pragma unroll
-    for (int e = 0; e < RT; ++e) m[e] = -INFINITY, l[e] = 0.0f;
+    // the current row pass
+    int b = at_find(prefix, a.c.n_seqs, u0);
+    uint32_t blk = 0;                                         // its first block in this share
+    int h = 0, nrow = 0, r0 = 0;                              // first row
+    int64_t tok = 0;                                          // token row of row 0's token
+    int64_t all_lo = 0, all_hi = 0;                           // what every row of the pass sees
+    int64_t v_lo[MT][RT], v_hi[MT][RT];
+    uint32_t qa[C::QS ? 1 : MT][KS][4];
+    uint32_t *qs = reinterpret_cast<uint32_t *>(sm + C::OFF_Q) + warp * MT * KS * 128 + lane * 4;
+    float rs[MT][RT], m[MT][RT], l[MT][RT];
+    float o[MT][NT][4];
     float gmax = 0.0f;                                        // the largest V scale so far
 
-    // this warp's blocks: s_lo + warp, + kAtWarps, ...; pages and scales of 32 of them at a time, one a lane
-    const int64_t mine = s_hi - s_lo > warp ? (s_hi - s_lo - warp + kAtWarps - 1) / kAtWarps : 0;
-    int pg = -1;
-    float dk = 0.0f, dv = 0.0f;
-    auto fetch = [&](int64_t base) {
-        pg = -1, dk = dv = 0.0f;
-        if (base + lane < mine) {
-            const int64_t blk = s_lo + warp + (base + lane) * kAtWarps;
-            pg = a.c.table[(int64_t)b * a.c.max_pages + ((blk * kKB) >> a.c.tshift)];
-            if (pg < 0 || pg >= a.c.n_pages) {
-                kv_error(err, KV_ERR_PAGE);
-                pg = -1;
-            } else {
-                const float *sc = reinterpret_cast<const float *>(a.c.pool + pg * a.c.page_bytes + a.c.off_s);
-                const int sb = (int)((blk * kKB) & (a.c.T - 1)) / kKB, spp = a.c.T / kKB;
-                dk = sc[h * spp + sb];
-                dv = sc[(a.c.H + h) * spp + sb];
+    // the row pass of unit u: its rows' q and ranges; how many units of it are left
+    auto begin = [&](uint32_t u, bool &fresh) -> uint32_t {
+        while (u >= prefix[b + 1]) ++b;
+        AtSeq q;
+        q.init(a, b, C::R, err, false);
+        const uint32_t r = u - prefix[b], it = r / q.nb;
+        const int tile = (int)it / H;
+        h = (int)it - tile * H;
+        blk = q.b_lo + (r - it * q.nb);
+        fresh = blk == q.b_lo;                                // the pass begins here
+        const uint32_t left = q.nb - (r - it * q.nb);
+        tok = q.lo;
+        r0 = tile * C::R;
+        nrow = min(C::R, q.n * G - r0);
+        int64_t x0, y0, x1, y1;
+        row_range(q.first + r0 / G, q.len, a.causal, a.window, x0, y0);
+        row_range(q.first + (r0 + nrow - 1) / G, q.len, a.causal, a.window, x1, y1);
+        all_lo = x1, all_hi = y0 > x0 ? y0 : 0;
+        gmax = 0.0f;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int e = 0; e < RT; ++e) {
+                const int rr = t * C::RT + g + 8 * e;
+                v_lo[t][e] = v_hi[t][e] = 0;
+                m[t][e] = -INFINITY, l[t][e] = 0.0f;
+                float x[D / 4];
+                if (rr < nrow) {
+                    const int i = (r0 + rr) / G;
+                    row_range(q.first + i, q.len, a.causal, a.window, v_lo[t][e], v_hi[t][e]);
+                    const T *p = static_cast<const T *>(a.q) + (tok + i) * a.qt + (int64_t)(h * G + (r0 + rr - i * G)) * a.qh + cc * (D / 4);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) load4(p + 4 * j, x + 4 * j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < D / 4; ++j) x[j] = 0.0f;
+                }
+                float amax = 0.0f;
+                bool fin = true;
+#pragma unroll
+                for (int j = 0; j < D / 4; ++j) {
+                    amax = fmaxf(amax, fabsf(x[j]));
+                    fin = fin && fabsf(x[j]) <= 3.402823466e38f;
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                fin = (__ballot_sync(0xffffffffu, fin) >> (lane & ~3) & 15u) == 15u;
+                const int ex = fin ? row_exponent(amax) : 0;
+                // a row with a NaN or an infinity becomes NaN
+                const float down = fin ? pow2i(-ex) * a.sign : __int_as_float(0x7fc00000);
+                rs[t][e] = pow2i(ex) * a.c_log2;
+#pragma unroll
+                for (int j = 0; j < D / 4; ++j) x[j] = fin ? x[j] * down : down;
+                // k order of the products: k-step ks = 4 hh + s takes the values 16 (2 cc + hh) + 4 s ..+3 (D = 128) or
+                // 16 cc + 4 s ..+3 (D = 64) of the row: the 16 bytes that one shared-memory load of K gives
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const float y0 = x[4 * ks], y1 = x[4 * ks + 1], y2 = x[4 * ks + 2], y3 = x[4 * ks + 3];
+                    uint32_t w[4];
+                    w[e] = pack_f16(y0, y1);
+                    w[2 + e] = pack_f16(y2, y3);
+                    if constexpr (TWO) {
+                        const float2 h0 = unpack_f16(w[0]), h1 = unpack_f16(w[2]);
+                        w[1] = pack_f16(y0 - h0.x, y1 - h0.y);
+                        w[3] = pack_f16(y2 - h1.x, y3 - h1.y);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (TWO || (z & 1) == e) {
+                            if constexpr (C::QS) qs[(t * KS + ks) * 128 + z] = w[z];
+                            else qa[t][ks][z] = w[z];
+                        }
+                }
             }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
         }
+        if constexpr (C::QS) __syncwarp();
+        return left;
     };
-    auto issue = [&](int64_t i, int page) {                   // lane 0: block i of this warp into its ring slot
-        const int slot = (int)(i % kAtRing);
-        const int tok = (int)(((s_lo + warp + i * kAtWarps) * kKB) & (a.c.T - 1));
-        mbar_arrive_expect_tx(bar + slot, C::SLOT);
-        tma_load_5d(ring + slot * C::SLOT, &tm, 0, tok, h, a.layer, page, bar + slot);
-        tma_load_5d(ring + slot * C::SLOT + C::BLK, &tm, 0, tok, a.c.H + h, a.layer, page, bar + slot);
+    // the rows' sums leave: divided where the pass is whole, else as partial `which` of this worker
+    auto end = [&](bool whole, int which) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int e = 0; e < RT; ++e) {
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 1);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 2);
+                const int rr = t * C::RT + g + 8 * e;
+                if (rr < nrow) {
+                    const float f = whole ? (l[t][e] == 0.0f ? 0.0f : gmax / l[t][e]) : gmax;
+                    const int i = (r0 + rr) / G;
+                    float *part = a.part + ((int64_t)(2 * worker + which) * C::R + rr) * (D + 4);
+                    T *dst = static_cast<T *>(a.out) + (tok + i) * a.ot + (int64_t)(h * G + (r0 + rr - i * G)) * a.oh + cc * (D / 4);
+                    // this thread's values 32 cc .. 32 cc + 31 of the row (D = 128): column 2 cc + z of n-tile j is value (2 cc + z) D / 8 + j
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int j = 0; j < NT; j += 4) {
+                            float x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[k] = (TWO ? o[t][j + k][z] + o[t][j + k][2 + z] : o[t][j + k][2 * e + z]) * f;
+                            if (whole) store4(dst + z * NT + j, x);
+                            else store4(part + cc * (D / 4) + z * NT + j, x);
+                        }
+                    if (!whole && cc == 0) *reinterpret_cast<float2 *>(part + D) = make_float2(m[t][e], l[t][e]);
+                }
+            }
     };
 
-    // pages of the batch after the one in (pg, dk, dv), for loads issued ahead of their batch
-    fetch(0);
-    int pg_n = pg;
-    float dk_n = 0.0f, dv_n = 0.0f;
-    {
-        const int pg0 = pg;
-        const float dk0 = dk, dv0 = dv;
-        fetch(32);
-        pg_n = pg, dk_n = dk, dv_n = dv;
-        pg = pg0, dk = dk0, dv = dv0;
-    }
-    for (int i = 0; i < kAtRing && i < mine; ++i) {
-        const int page = __shfl_sync(0xffffffffu, pg, i);
-        if (lane == 0) issue(i, page);
-    }
-    bool dead = false;
-    for (int64_t i = 0; i < mine; ++i) {
-        const int li = (int)(i & 31), slot = (int)(i % kAtRing);
-        if (li == 0 && i > 0) {
-            pg = pg_n, dk = dk_n, dv = dv_n;
-            const int pg0 = pg;
-            const float dk0 = dk, dv0 = dv;
-            fetch(i + 32);
-            pg_n = pg, dk_n = dk, dv_n = dv;
-            pg = pg0, dk = dk0, dv = dv0;
-        }
-        if (!mbar_wait(bar + slot, (uint32_t)(i / kAtRing) & 1, err, KV_ERR_WAIT, nullptr)) {
-            dead = true;
-            break;
-        }
+    AtJoin join = {0, 0, 0, 0, 0};
+    int slot = 0;                                             // ring slot of the next unit
+    uint32_t phase = 0;
+    for (int k = 0; k < mine;) {
+      bool fresh;
+      const uint32_t left = begin(u0 + k, fresh);
+      const int k0 = k, stop = k + (int)min((uint32_t)(mine - k), left);
+#pragma unroll 1
+      for (; k < stop; ++k) {
+        const int li = k & 31;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar + slot, phase, err, KV_ERR_WAIT, nullptr))) return;
         const uint8_t *sk = ring + slot * C::SLOT, *sv = sk + C::BLK;
         // scores of 32 tokens: four n-tiles of 8
-        float s[4][4];
+        float s[MT][4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < MT; ++x) s[x][t][0] = s[x][t][1] = s[x][t][2] = s[x][t][3] = 0.0f;
             const int row = 8 * t + g;
 #pragma unroll
             for (int hh = 0; hh < D / 64; ++hh) {
                 const int chunk = D == 128 ? ((2 * cc + hh) ^ (row & 7)) : (cc ^ ((row >> 1) & 3));
                 const uint4 w = *reinterpret_cast<const uint4 *>(sk + row * D + chunk * 16);
-                uint32_t x, y;
-                codes_f16(w.x, x, y);
-                mma16816(s[t], qa[4 * hh + 0], x, y);
-                codes_f16(w.y, x, y);
-                mma16816(s[t], qa[4 * hh + 1], x, y);
-                codes_f16(w.z, x, y);
-                mma16816(s[t], qa[4 * hh + 2], x, y);
-                codes_f16(w.w, x, y);
-                mma16816(s[t], qa[4 * hh + 3], x, y);
-            }
-        }
-        const float dkb = __shfl_sync(0xffffffffu, dk, li), dvb = __shfl_sync(0xffffffffu, dv, li);
-        const int64_t t0 = (s_lo + warp + i * kAtWarps) * kKB;
-        const bool inner = t0 >= all_lo && t0 + kKB <= all_hi;
-        const float gnew = fmaxf(gmax, dvb);
-        const float gold = gnew > 0.0f ? gmax / gnew : 1.0f, pv = gnew > 0.0f ? dvb / gnew : 0.0f;
-        gmax = gnew;
-        float f[RT];
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < RT; ++e) {
-            const float k = rs[e] * dkb;
-            float mx = -INFINITY;
+                for (int z = 0; z < 4; ++z) {
+                    uint32_t x, y;
+                    codes_f16(ww[z], x, y);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    float y = TWO ? (s[t][z] + s[t][2 + z]) * k : s[t][2 * e + z] * k;
-                    if (!inner) {
-                        const int64_t pos = t0 + 8 * t + 2 * cc + z;
-                        if (pos < v_lo[e] || pos >= v_hi[e]) y = -INFINITY;
+                    for (int k = 0; k < MT; ++k) {
+                        if constexpr (C::QS) {
+                            const uint4 f = *reinterpret_cast<const uint4 *>(qs + (k * KS + 4 * hh + z) * 128);
+                            const uint32_t ff[4] = {f.x, f.y, f.z, f.w};
+                            mma16816(s[k][t], ff, x, y);
+                        } else {
+                            mma16816(s[k][t], qa[k][4 * hh + z], x, y);
+                        }
                     }
-                    s[t][2 * e + z] = y;
-                    mx = fmaxf(mx, y);
                 }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m[e], mx);
-            const float mb = mn == -INFINITY ? 0.0f : mn;
-            f[e] = exp2_approx(m[e] - mb);
-            m[e] = mn;
-            float sum = 0.0f;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float p = exp2_approx(s[t][2 * e + z] - mb + kPShift);
-                    sum += p;
-                    s[t][2 * e + z] = p * pv;
-                }
-            l[e] = l[e] * f[e] + sum;
-            f[e] *= gold;
-        }
-        bool same = f[0] == 1.0f;
-        if constexpr (RT == 2) same = same && f[1] == 1.0f;
-        if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                o[j][0] *= f[0], o[j][1] *= f[0];
-                o[j][2] *= f[RT - 1], o[j][3] *= f[RT - 1];
             }
         }
+        const float dkb = __shfl_sync(0xffffffffu, dk0, li), dvb = __shfl_sync(0xffffffffu, dv0, li);
+        const int64_t t0 = (int64_t)(blk + (k - k0)) * kKB;
+        const bool inner = t0 >= all_lo && t0 + kKB <= all_hi;
+        // the V scale reference moves to twice a scale that exceeds it
+        float gold = 1.0f;
+        if (dvb > gmax) {
+            gold = gmax / (2.0f * dvb);
+            gmax = 2.0f * dvb;
+        }
+        const float pv = gmax > 0.0f ? dvb / gmax : 0.0f;
+        bool grow = gold != 1.0f;
+        float mx[MT][RT], kk[MT][RT];
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+            for (int e = 0; e < RT; ++e) {
+                // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
+                kk[x][e] = fmaxf(rs[x][e] * dkb, 0x1p-120f);
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        f2_unpack(f2_add(f2_pack(s[x][t][0], s[x][t][1]), f2_pack(s[x][t][2], s[x][t][3])), s[x][t][0], s[x][t][1]);
+                }
+                if (!inner) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int64_t pos = t0 + 8 * t + 2 * cc + z;
+                            if (pos < v_lo[x][e] || pos >= v_hi[x][e]) s[x][t][2 * e + z] = -INFINITY;
+                        }
+                }
+                const int f = 2 * e;
+                float y = max3(s[x][0][f], s[x][0][f + 1], s[x][1][f]);
+                y = max3(y, s[x][1][f + 1], s[x][2][f]);
+                y = max3(y, s[x][2][f + 1], s[x][3][f]);
+                mx[x][e] = fmaxf(y, s[x][3][f + 1]) * kk[x][e];
+                grow = grow || mx[x][e] > m[x][e] + kTau || (m[x][e] == -INFINITY && mx[x][e] > m[x][e]);
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+                float f[RT];
+#pragma unroll
+                for (int e = 0; e < RT; ++e) {
+                    float y = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], 1));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                    y = fmaxf(y, m[x][e]);
+                    f[e] = y == -INFINITY ? 1.0f : exp2_approx(m[x][e] - y);
+                    m[x][e] = y;
+                    l[x][e] *= f[e];
+                    f[e] *= gold;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[x][j][0] *= f[0], o[x][j][1] *= f[0];
+                    o[x][j][2] *= f[RT - 1], o[x][j][3] *= f[RT - 1];
+                }
+            }
+        }
+        const uint64_t pv2 = f2_pack(pv, pv);
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+            for (int e = 0; e < RT; ++e) {
+                const float off = kLazyShift - (m[x][e] == -INFINITY ? 0.0f : m[x][e]);
+                const uint64_t off2 = f2_pack(off, off), k2 = f2_pack(kk[x][e], kk[x][e]);
+                uint64_t sum = f2_pack(0.0f, 0.0f);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float y, z;
+                    f2_unpack(f2_fma(f2_pack(s[x][t][2 * e], s[x][t][2 * e + 1]), k2, off2), y, z);
+                    const uint64_t p = f2_pack(exp2_approx(y), exp2_approx(z));
+                    sum = f2_add(sum, p);
+                    f2_unpack(f2_mul(p, pv2), s[x][t][2 * e], s[x][t][2 * e + 1]);
+                }
+                float y, z;
+                f2_unpack(sum, y, z);
+                l[x][e] += y + z;
+            }
         // o += p' v: two k-steps of 16 tokens
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
-            uint32_t pa[4];
-            pa[0] = pack_f16(s[2 * t2][0], s[2 * t2][1]);
-            pa[2] = pack_f16(s[2 * t2 + 1][0], s[2 * t2 + 1][1]);
-            if constexpr (TWO) {
-                float2 x = unpack_f16(pa[0]);
-                pa[1] = pack_f16(s[2 * t2][0] - x.x, s[2 * t2][1] - x.y);
-                x = unpack_f16(pa[2]);
-                pa[3] = pack_f16(s[2 * t2 + 1][0] - x.x, s[2 * t2 + 1][1] - x.y);
-            } else {
-                pa[1] = pack_f16(s[2 * t2][2], s[2 * t2][3]);
-                pa[3] = pack_f16(s[2 * t2 + 1][2], s[2 * t2 + 1][3]);
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+                float (&sx)[4][4] = s[x];
+                pa[x][0] = pack_f16(sx[2 * t2][0], sx[2 * t2][1]);
+                pa[x][2] = pack_f16(sx[2 * t2 + 1][0], sx[2 * t2 + 1][1]);
+                if constexpr (TWO) {
+                    float2 y = unpack_f16(pa[x][0]);
+                    pa[x][1] = pack_f16(sx[2 * t2][0] - y.x, sx[2 * t2][1] - y.y);
+                    y = unpack_f16(pa[x][2]);
+                    pa[x][3] = pack_f16(sx[2 * t2 + 1][0] - y.x, sx[2 * t2 + 1][1] - y.y);
+                } else {
+                    pa[x][1] = pack_f16(sx[2 * t2][2], sx[2 * t2][3]);
+                    pa[x][3] = pack_f16(sx[2 * t2 + 1][2], sx[2 * t2 + 1][3]);
+                }
             }
             uint32_t w[4][D / 32];                            // tokens 2cc, 2cc+1, 2cc+8, 2cc+9 of the step: D / 8 codes each
 #pragma unroll
@@ -335,115 +521,112 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
                 uint32_t p0, p1, q0, q1;
                 codes_f16(x0, p0, p1);
                 codes_f16(y0, q0, q1);
-                mma16816(o[4 * k + 0], pa, p0, q0);
-                mma16816(o[4 * k + 1], pa, p1, q1);
+#pragma unroll
+                for (int x = 0; x < MT; ++x) {
+                    mma16816(o[x][4 * k + 0], pa[x], p0, q0);
+                    mma16816(o[x][4 * k + 1], pa[x], p1, q1);
+                }
                 codes_f16(x1, p0, p1);
                 codes_f16(y1, q0, q1);
-                mma16816(o[4 * k + 2], pa, p0, q0);
-                mma16816(o[4 * k + 3], pa, p1, q1);
+#pragma unroll
+                for (int x = 0; x < MT; ++x) {
+                    mma16816(o[x][4 * k + 2], pa[x], p0, q0);
+                    mma16816(o[x][4 * k + 3], pa[x], p1, q1);
+                }
             }
         }
         // the slot goes back to the copy engine once every lane's loads are done
         __threadfence_block();
         __syncwarp();
-        if (i + kAtRing < mine) {
-            const int64_t nx = i + kAtRing;
-            const int page = __shfl_sync(0xffffffffu, (nx >> 5) == (i >> 5) ? pg : pg_n, (int)(nx & 31));
-            if (lane == 0) {
-                fence_proxy_async_smem();
-                issue(nx, page);
-            }
+        if (li == 31) dk0 = dk, dv0 = dv;                     // the next unit's batch is the one that was fetched last
+        if (k + RING < mine) {
+            if (((k + RING) & 31) == 0) fetch(k + RING);
+            if (lane == 0) fence_proxy_async_smem();
+            issue(k + RING, slot);
         }
+        if (++slot == RING) slot = 0, phase ^= 1;
+      }
+      const bool on = (uint32_t)(k - k0) < left;              // the pass goes on with the next workers
+      end(fresh && !on, on);
+      if (fresh && on) join = AtJoin{nrow, (int)shares.owner(u0 + k0 + left - 1), h, r0, tok};
     }
-    (void)dead;
-
-    // join the warps
-#pragma unroll
-    for (int e = 0; e < RT; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    }
-    __syncthreads();                                          // every warp is done with its ring
-    float *so = reinterpret_cast<float *>(sm);                // [warp][16][LD]
-    float *sml = so + kAtWarps * 16 * C::LD;                  // [warp][16][2]
-#pragma unroll
-    for (int e = 0; e < RT; ++e) {
-        float *row = so + (warp * 16 + g + 8 * e) * C::LD + cc * (D / 4);
-        if (cc == 0) sml[(warp * 16 + g + 8 * e) * 2] = m[e], sml[(warp * 16 + g + 8 * e) * 2 + 1] = l[e];
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float x = TWO ? o[j][z] + o[j][2 + z] : o[j][2 * e + z];
-                row[z * NT + j] = x * gmax;
-            }
-    }
-    __syncthreads();
-    // warp w writes rows w, w + 4, ...; a lane holds D / 32 values
-    for (int r = warp; r < nrow; r += kAtWarps) {
-        float mm = -INFINITY, ll = 0.0f, acc[D / 32];
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) mm = fmaxf(mm, sml[(w * 16 + r) * 2]);
-        const float mb = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) {
-            const float f = exp2_approx(sml[(w * 16 + r) * 2] - mb);
-            ll += f * sml[(w * 16 + r) * 2 + 1];
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) acc[j] += f * so[(w * 16 + r) * C::LD + (D / 32) * lane + j];
-        }
-        const int64_t rr = r0 + r, i = rr / G;
-        const int gq = (int)(rr - i * G);
-        if (a.nsplit == 1) {
-            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-            T *dst = static_cast<T *>(a.out) + (lo + i) * a.ot + (int64_t)(h * G + gq) * a.oh + (D / 32) * lane;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) acc[j] *= inv;
-            if constexpr (D == 128) {
-                store4(dst, acc);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) dst[j] = T(acc[j]);
-            }
-        } else {
-            float *dst = a.part + (((lo + i) * (int64_t)(a.c.H * G) + h * G + gq) * a.nsplit + split) * (D + 2);
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) dst[(D / 32) * lane + j] = acc[j];
-            if (lane == 0) dst[D] = mm, dst[D + 1] = ll;
-        }
-    }
+    if (lane == 0) a.join[worker] = join;
 }
 
-// joins the splits: a warp per row
+// Joins the partials of the row passes that several workers share.  A CTA looks at 8 workers (a lane each) and joins one row (the grid's
+// y) of the passes that those began; its warps take every eighth partial each.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv_attn_join_kernel(AtArgs a, int64_t n_rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(AtArgs a, int R) {
+    constexpr int V = D / 32, JW = kJoinWarps;
+    __shared__ float s_o[JW - 1][D], s_ml[JW][2];
     grid_dep_launch();
     grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= n_rows) return;
-    const int hq = a.c.H * a.group;
-    const float *p = a.part + row * a.nsplit * (D + 2);
-    float mm = -INFINITY;
-    for (int s = lane; s < a.nsplit; s += 32) mm = fmaxf(mm, p[s * (D + 2) + D]);
+    const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t workers = min((uint32_t)a.workers, *a.total), mine = blockIdx.x + lane * gridDim.x;
+    AtJoin w = {0, 0, 0, 0, 0};
+    if (mine < workers) w = a.join[mine];
+    for (uint32_t todo = __ballot_sync(0xffffffffu, row < w.nrow); todo != 0; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, first = blockIdx.x + from * gridDim.x;
+        const int last = __shfl_sync(0xffffffffu, w.last, from), n = last - first + 1;
+        const float *base = a.part + row * (int64_t)(D + 4);
+        auto part = [&](int c) { return base + (2 * (int64_t)c + (c < last)) * R * (D + 4); };
+        float mm = -INFINITY, ll = 0.0f, acc[V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    const float mb = mm == -INFINITY ? 0.0f : mm;
-    float ll = 0.0f, acc[D / 32];
+        for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+        // 32 of this warp's partials at a time: a lane has the maximum and the sum of one
+        for (int p0 = warp; p0 < n; p0 += 32 * JW) {
+            const int p = p0 + JW * lane;
+            const float2 ml = p < n ? *reinterpret_cast<const float2 *>(part(first + p) + D) : make_float2(-INFINITY, 0.0f);
+            float mn = fmaxf(ml.x, mm);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float f = exp2_approx(p[s * (D + 2) + D] - mb);
-        ll += f * p[s * (D + 2) + D + 1];
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            const float mb = mn == -INFINITY ? 0.0f : mn, old = exp2_approx(mm - mb), f = exp2_approx(ml.x - mb);
+            mm = mn;
+            float x = ml.y * f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] += f * p[s * (D + 2) + (D / 32) * lane + j];
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            ll = ll * old + x;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= old;
+            const int cnt = min(32, (n - p0 + JW - 1) / JW);
+#pragma unroll 8
+            for (int j = 0; j < cnt; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+                const float *src = part(first + p0 + JW * j) + V * lane;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] += fj * src[e];
+            }
+        }
+        if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = ll;
+        if (warp > 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) s_o[warp - 1][V * lane + e] = acc[e];
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float all = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < JW; ++x) all = fmaxf(all, s_ml[x][0]);
+            const float mb = all == -INFINITY ? 0.0f : all;
+            float sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < JW; ++x) {
+                const float f = exp2_approx(s_ml[x][0] - mb);
+                sum += s_ml[x][1] * f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = x == 0 ? acc[e] * f : acc[e] + s_o[x - 1][V * lane + e] * f;
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int r0 = __shfl_sync(0xffffffffu, w.r0, from), h = __shfl_sync(0xffffffffu, w.h, from);
+            const int64_t tok = __shfl_sync(0xffffffffu, w.tok, from);
+            const int i = (r0 + row) / a.group;
+            T *dst = static_cast<T *>(a.out) + (tok + i) * a.ot + (int64_t)(h * a.group + (r0 + row - i * a.group)) * a.oh + V * lane;
+#pragma unroll
+            for (int e = 0; e < V; ++e) dst[e] = T(acc[e] * inv);
+        }
+        __syncthreads();
     }
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    T *dst = static_cast<T *>(a.out) + (row / hq) * a.ot + (row % hq) * a.oh + (D / 32) * lane;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) dst[j] = T(acc[j] * inv);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -465,62 +648,73 @@ int kv_tensor_map(CUtensorMap *tm, const mqkv_cache &c, const mqkv_layout &lay) 
     return MQ_OK;
 }
 
-int64_t tiles_of(int dtype, int64_t rows) { return dtype == MQKV_F32 ? (rows + 7) / 8 : (rows + 15) / 16; }
-
 // rows per KV head from which the tcgen05 tiles of mq_kv_prefill.cu are taken
 bool use_tiles(int64_t rows) { return rows > 64; }
-
-int splits_of(int32_t n_seqs, int32_t H, int64_t tiles, int64_t max_kv) {
-    const int64_t ctas = (int64_t)n_seqs * H * tiles, blocks = (max_kv + kKB - 1) / kKB;
-    int64_t s = (2 * sm_count() + ctas - 1) / ctas;
-    const int64_t most = (blocks + 2 * kAtWarps - 1) / (2 * kAtWarps);
-    s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s);
+// MMA tiles per pass: two where the rows do not fit one
+int pass_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
+int pass_rows(int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(dtype, rows); }
+// CTAs: two per SM, or as many as there are units for their warps at most
+int64_t share_ctas(int32_t n_seqs, int32_t H, int dtype, int64_t rows, int64_t max_kv) {
+    const int64_t passes = (rows + pass_rows(dtype, rows) - 1) / pass_rows(dtype, rows), blocks = (max_kv + kKB - 1) / kKB;
+    const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = 2 * sm_count();
+    return (units + kAtWarps - 1) / kAtWarps < most ? (units + kAtWarps - 1) / kAtWarps : most;
 }
+size_t plan_bytes(int32_t n_seqs, size_t workers) { return (256 + (((size_t)n_seqs + 4) & ~size_t(3)) * 4 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
 
-template <typename T, int D>
-int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t n_tokens, unsigned int *err, cudaStream_t s) {
-    using C = AtCfg<D>;
-    const int slot = kAttrSlotKv + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128);
-    int rc = ensure_smem_attr(reinterpret_cast<const void *>(&kv_attn_kernel<T, D>), C::SMEM, slot);
+template <typename T, int D, int MT>
+int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t ctas, unsigned int *err, cudaStream_t s) {
+    using C = AtCfg<T, D, MT>;
+    const int slot = kAttrSlotKv + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128) + (MT == 2 ? 16 : 0);
+    const bool in_smem = a.c.n_seqs <= kAtSmemSeqs;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(&kv_attn_kernel<T, D, MT>), C::SMEM + 4 * (kAtSmemSeqs + 1), slot);
+    if (rc == MQ_OK && !in_smem)
+        rc = cuda_error(launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(1024), 0, s, a, (int)C::R, err), "mqkv_attention plan launch");
     if (rc != MQ_OK) return rc;
-    rc = cuda_error(launch_pdl(kv_attn_kernel<T, D>, dim3((unsigned)((int64_t)a.nsplit * a.c.H * a.tiles * a.c.n_seqs)), dim3(kAtThreads), C::SMEM, s, tm, a, err),
-                    "mqkv_attention launch");
-    if (rc != MQ_OK || a.nsplit == 1) return rc;
-    const int64_t rows = n_tokens * a.c.H * a.group;
-    return cuda_error(launch_pdl(kv_attn_join_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, rows),
+    const size_t smem = C::SMEM + (in_smem ? 4 * (a.c.n_seqs + 1) : 0);
+    rc = cuda_error(launch_pdl(kv_attn_kernel<T, D, MT>, dim3((unsigned)ctas), dim3(kAtThreads), smem, s, tm, a, err), "mqkv_attention launch");
+    if (rc != MQ_OK) return rc;
+    const int rows = a.max_q * a.group;
+    return cuda_error(launch_pdl(kv_attn_join_kernel<T, D>, dim3((unsigned)((a.workers + 7) / 8), (unsigned)(rows < C::R ? rows : C::R)), dim3(32 * kJoinWarps), 0, s, a, (int)C::R),
                       "mqkv_attention join launch");
+}
+template <typename T>
+int attn_d(const CUtensorMap &tm, const AtArgs &a, int tiles, int64_t ctas, unsigned int *err, cudaStream_t s) {
+    if (a.c.D == 128) return tiles == 1 ? attn_t<T, 128, 1>(tm, a, ctas, err, s) : attn_t<T, 128, 2>(tm, a, ctas, err, s);
+    return tiles == 1 ? attn_t<T, 64, 1>(tm, a, ctas, err, s) : attn_t<T, 64, 2>(tm, a, ctas, err, s);
 }
 
 }  // namespace
 
 size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t n_q_heads, int64_t n_tokens, int64_t max_q,
                        int64_t max_kv) {
-    if (use_tiles(max_q * (n_q_heads / H))) return 256;
-    const int n = splits_of(n_seqs, H, tiles_of(dtype, max_q * (n_q_heads / H)), max_kv);
-    return n == 1 ? 256 : (size_t)n_tokens * n_q_heads * n * (D + 2) * 4;
+    const int64_t rows = max_q * (n_q_heads / H);
+    if (use_tiles(rows)) return 256;
+    const size_t workers = (size_t)share_ctas(n_seqs, H, dtype, rows, max_kv) * kAtWarps;
+    return plan_bytes(n_seqs, workers) + workers * 2 * pass_rows(dtype, rows) * (D + 4) * 4;
 }
 
 int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int layer, const KvView &c, const KvRows &r,
                         const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
-    if (use_tiles(p.max_q * p.group)) return kv_launch_prefill(c, r, p, err, s);
+    const int64_t rows = p.max_q * p.group;
+    if (use_tiles(rows)) return kv_launch_prefill(c, r, p, err, s);
     CUtensorMap tm;
     int rc = kv_tensor_map(&tm, cache, lay);
     if (rc != MQ_OK) return rc;
     AtArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
-    a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = p.max_q, a.window = p.window;
-    a.tiles = (int)tiles_of(p.dtype, p.max_q * p.group);
-    a.nsplit = splits_of(c.n_seqs, c.H, a.tiles, p.max_kv);
-    a.c_log2 = p.scale * kLog2e;
-    a.part = static_cast<float *>(ws);
-    if (c.D == 128)
-        return p.dtype == MQKV_F32   ? attn_t<float, 128>(tm, a, r.n_tokens, err, s)
-               : p.dtype == MQKV_F16 ? attn_t<__half, 128>(tm, a, r.n_tokens, err, s)
-                                     : attn_t<__nv_bfloat16, 128>(tm, a, r.n_tokens, err, s);
-    return p.dtype == MQKV_F32   ? attn_t<float, 64>(tm, a, r.n_tokens, err, s)
-           : p.dtype == MQKV_F16 ? attn_t<__half, 64>(tm, a, r.n_tokens, err, s)
-                                 : attn_t<__nv_bfloat16, 64>(tm, a, r.n_tokens, err, s);
+    a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = (int32_t)p.max_q, a.window = p.window;
+    const int64_t ctas = share_ctas(c.n_seqs, c.H, p.dtype, rows, p.max_kv);
+    a.workers = (int)ctas * kAtWarps;
+    a.c_log2 = fabsf(p.scale) * kLog2e;
+    a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
+    a.total = static_cast<uint32_t *>(ws);
+    a.prefix = a.total + 64;
+    a.join = reinterpret_cast<AtJoin *>(a.prefix + ((c.n_seqs + 4) & ~3));
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes(c.n_seqs, (size_t)a.workers));
+    const int tiles = pass_tiles(p.dtype, rows);
+    return p.dtype == MQKV_F32   ? attn_d<float>(tm, a, tiles, ctas, err, s)
+           : p.dtype == MQKV_F16 ? attn_d<__half>(tm, a, tiles, ctas, err, s)
+                                 : attn_d<__nv_bfloat16>(tm, a, tiles, ctas, err, s);
 }
 
 }  // namespace mq

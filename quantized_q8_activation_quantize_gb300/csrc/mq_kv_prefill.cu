@@ -34,7 +34,6 @@ constexpr int kPfThreads = 512;
 constexpr int kPfN = 128;                      // tokens of a tile
 constexpr int kPfSlots = 5;                    // f16 operand tiles in flight
 constexpr int kPfInfo = 4;                     // tiles that the lookup runs ahead
-constexpr float kTau = 8.0f, kPfShift = 6.0f;   // 16-bit rows: p <= 2^(6 + 8) in f16
 
 struct PfArgs {
     KvView c;
@@ -73,28 +72,6 @@ struct PfCfg {
     static constexpr uint32_t COL_S = 0, COL_O = 256;
 };
 
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16: A holds two f16 per 32-bit column
 __device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -124,12 +101,6 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t m
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // The instruction cache is a resource here: four roles run their own straight-line code, and a fully unrolled version stalled on
@@ -683,7 +654,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                         }
                     }
                 }
-                pf_tile_weights<false>(ts, kb, kb, kPfShift - (m == -INFINITY ? 0.0f : m), l2);
+                pf_tile_weights<false>(ts, kb, kb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(bar.p_full + t, lane);
