@@ -22,6 +22,7 @@ namespace mq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
+constexpr uint32_t kAtExtra = 3;               // what the beginning and end of a row pass cost, in blocks
 constexpr int kAtSmemSeqs = 256;                // sequences whose plan fits the CTA's shared memory beside two CTAs' rings
 
 struct AtArgs {
@@ -35,7 +36,7 @@ struct AtArgs {
     int64_t window;
     float c_log2, sign;         // |scale| * log2(e), the sign of scale (it goes into q: score factors are not negative)
     uint32_t *total;            // units of the call, for the join
-    uint32_t *prefix;           // [n_seqs + 1]: units before each sequence
+    uint32_t *prefix;           // [n_seqs + 1][2]: places and units before each sequence
     struct AtJoin *join;        // [workers]
     float *part;                // [worker][2][R rows][D + 4]: o, m, l
 };
@@ -46,7 +47,7 @@ struct AtJoin {
     int64_t tok;
 };
 
-// equal shares of the units: the first rem of them have one more
+// equal shares of the places: the first rem of them have one more
 struct AtShare {
     uint32_t base, rem;
     __device__ __forceinline__ AtShare(uint32_t total, uint32_t n) : base(total / n), rem(total - total / n * n) {}
@@ -101,40 +102,41 @@ struct AtSeq {
         b_lo = (uint32_t)((y0 > x0 ? x0 : 0) / kKB);
         nb = max((uint32_t)((max(y0, y1) + kKB - 1) / kKB) - b_lo, 1u);
     }
-    __device__ __forceinline__ uint32_t units(int H) const { return (uint32_t)(tiles * H) * nb; }
+    // a row pass takes nb places for its blocks after kAtExtra for its beginning and end
+    __device__ __forceinline__ uint2 size(int H) const { return make_uint2((uint32_t)(tiles * H) * (nb + kAtExtra), (uint32_t)(tiles * H) * nb); }
 };
 
-// units before each sequence into prefix[0 .. n_seqs], by one CTA of THREADS threads.  (Their sum stays below 2^32: the host has
-// checked it for max_kv, and a table row holds no more tokens than its pages.)
+// places and units before each sequence into prefix[0 .. n_seqs], by one CTA of THREADS threads.  (Their sums stay below 2^32: the host
+// has checked it for max_kv, and a table row holds no more tokens than its pages.)
 template <int THREADS>
-__device__ __forceinline__ void at_plan(const AtArgs &a, int R, uint32_t *prefix, uint32_t *s_warp, unsigned int *err, bool tell) {
+__device__ __forceinline__ void at_plan(const AtArgs &a, int R, uint2 *prefix, uint2 *s_warp, unsigned int *err, bool tell) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t before = 0;
+    uint2 before = make_uint2(0, 0);
 #pragma unroll 1
     for (int base = 0; base < a.c.n_seqs; base += THREADS) {
         const int b = base + threadIdx.x;
-        uint32_t v = 0;
+        uint2 v = make_uint2(0, 0);
         if (b < a.c.n_seqs) {
             AtSeq q;
             q.init(a, b, R, err, tell);
-            v = q.units(a.c.H);
+            v = q.size(a.c.H);
         }
-        uint32_t x = v;
+        uint2 x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x.x, o), z = __shfl_up_sync(0xffffffffu, x.y, o);
+            if (lane >= o) x.x += y, x.y += z;
         }
         if (lane == 31) s_warp[warp] = x;
         __syncthreads();
-        uint32_t w = 0, all = 0;
+        uint2 w = before;
 #pragma unroll 4
         for (int i = 0; i < THREADS / 32; ++i) {
-            if (i < warp) w += s_warp[i];
-            all += s_warp[i];
+            const uint2 y = s_warp[i];
+            if (i < warp) w.x += y.x, w.y += y.y;
+            before.x += y.x, before.y += y.y;
         }
-        if (b < a.c.n_seqs) prefix[b] = before + w + x - v;
-        before += all;
+        if (b < a.c.n_seqs) prefix[b] = make_uint2(w.x + x.x - v.x, w.y + x.y - v.y);
         __syncthreads();
     }
     if (threadIdx.x == 0) prefix[a.c.n_seqs] = before;
@@ -142,26 +144,27 @@ __device__ __forceinline__ void at_plan(const AtArgs &a, int R, uint32_t *prefix
 }
 
 __global__ void __launch_bounds__(1024) kv_attn_plan_kernel(AtArgs a, int R, unsigned int *err) {
-    __shared__ uint32_t s_warp[32];
+    __shared__ uint2 s_warp[32];
     grid_dep_launch();
     grid_dep_wait();
-    at_plan<1024>(a, R, a.prefix, s_warp, err, true);
-    if (threadIdx.x == 0) *a.total = a.prefix[a.c.n_seqs];
+    uint2 *prefix = reinterpret_cast<uint2 *>(a.prefix);
+    at_plan<1024>(a, R, prefix, s_warp, err, true);
+    if (threadIdx.x == 0) *a.total = prefix[a.c.n_seqs].x;
 }
 
 // the last sequence that begins at or before unit u (one with units)
-__device__ __forceinline__ int at_find(const uint32_t *prefix, int n_seqs, uint32_t u) {
+__device__ __forceinline__ int at_find(const uint2 *prefix, int n_seqs, uint32_t u) {
     int lo = 0, hi = n_seqs - 1;
 #pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+        if (prefix[mid].y <= u) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
 
 // Work is split by units of one block of 32 tokens for one KV head and row pass.  Every warp of the grid (a worker) takes an equal,
-// contiguous share of all units, whatever the lengths, and walks it through its own ring of K / V blocks; loads run ahead over the ends
+// contiguous share of them (of their places: a pass has kAtExtra more than its blocks), whatever the lengths, and walks it through its own ring of K / V blocks; loads run ahead over the ends
 // of row passes and no warp waits for another.  Where a row pass ends, or the share does, the sums leave: divided where the pass lies
 // in the share whole, else as a partial for the join kernel.  (Shares of whole CTAs, their warps joined in shared memory at the end of
 // each pass, left fewer partials but made every end of a pass cost 5 us: 77 us against 49 for a ragged batch of 48 sequences.)
@@ -183,22 +186,44 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
     }
     grid_dep_launch();
     grid_dep_wait();
-    const uint32_t *prefix = a.prefix;
+    const uint2 *prefix = reinterpret_cast<const uint2 *>(a.prefix);
     if (a.c.n_seqs <= kAtSmemSeqs) {
-        uint32_t *mine = reinterpret_cast<uint32_t *>(sm + C::OFF_PLAN);
-        at_plan<kAtThreads>(a, C::R, mine, reinterpret_cast<uint32_t *>(sm + C::OFF_BAR + kAtWarps * RING * 8), err, blockIdx.x == 0);
+        uint2 *mine = reinterpret_cast<uint2 *>(sm + C::OFF_PLAN);
+        at_plan<kAtThreads>(a, C::R, mine, reinterpret_cast<uint2 *>(sm + C::OFF_BAR + kAtWarps * RING * 8), err, blockIdx.x == 0);
         prefix = mine;
         if (blockIdx.x == 0) {                                // for the join
-            for (int i = threadIdx.x; i <= a.c.n_seqs; i += kAtThreads) a.prefix[i] = mine[i];
-            if (threadIdx.x == 0) *a.total = mine[a.c.n_seqs];
+            if (threadIdx.x == 0) *a.total = mine[a.c.n_seqs].x;
         }
     }
     __syncthreads();
-    const uint32_t total = prefix[a.c.n_seqs], workers = min((uint32_t)a.workers, total), worker = blockIdx.x * kAtWarps + warp;
-    if (worker >= workers) return;                            // every share has a unit at least
+    const uint32_t total = prefix[a.c.n_seqs].x, workers = min((uint32_t)a.workers, total), worker = blockIdx.x * kAtWarps + warp;
+    if (worker >= workers) {                                  // every share has a place at least
+        if (lane == 0) a.join[worker].nrow = 0;
+        return;
+    }
     const AtShare shares(total, workers);
-    const uint32_t u0 = shares.begin(worker);
-    const int H = a.c.H, G = a.group, mine = (int)(shares.begin(worker + 1) - u0);
+    const int H = a.c.H, G = a.group;
+    // the first unit at or after a place
+    auto unit_at = [&](uint32_t place) -> uint32_t {
+        if (place >= total) return prefix[a.c.n_seqs].y;
+        int lo = 0, hi = a.c.n_seqs - 1;
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid].x <= place) lo = mid; else hi = mid - 1;
+        }
+        AtSeq q;
+        q.init(a, lo, C::R, err, false);
+        const uint32_t r = place - prefix[lo].x, it = r / (q.nb + kAtExtra), in = r - it * (q.nb + kAtExtra);
+        return prefix[lo].y + it * q.nb + (in > kAtExtra ? in - kAtExtra : 0);
+    };
+    uint32_t edge = lane < 2 ? unit_at(shares.begin(worker + lane)) : 0;
+    const uint32_t u0 = __shfl_sync(0xffffffffu, edge, 0);
+    const int mine = (int)(__shfl_sync(0xffffffffu, edge, 1) - u0);
+    if (mine == 0) {
+        if (lane == 0) a.join[worker].nrow = 0;
+        return;
+    }
 
     // 32 of the warp's units at a time, one a lane: page, scales, where in the page and which head
     int pg = -1, at = 0;
@@ -210,7 +235,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
             const int b = at_find(prefix, a.c.n_seqs, u);
             AtSeq q;
             q.init(a, b, C::R, err, false);
-            const uint32_t r = u - prefix[b], it = r / q.nb, blk = q.b_lo + (r - it * q.nb);
+            const uint32_t r = u - prefix[b].y, it = r / q.nb, blk = q.b_lo + (r - it * q.nb);
             const int h = (int)(it % H), spp = a.c.T / kKB, sb = (int)blk & (spp - 1);
             at = h << 3 | sb;
             if ((int64_t)blk * kKB < q.len) {
@@ -243,6 +268,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
     uint32_t blk = 0;                                         // its first block in this share
     int h = 0, nrow = 0, r0 = 0;                              // first row
     int64_t tok = 0;                                          // token row of row 0's token
+    uint32_t last = 0;                                        // the pass's last place
     int64_t all_lo = 0, all_hi = 0;                           // what every row of the pass sees
     int64_t v_lo[MT][RT], v_hi[MT][RT];
     uint32_t qa[C::QS ? 1 : MT][KS][4];
@@ -253,15 +279,16 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
 
     // the row pass of unit u: its rows' q and ranges; how many units of it are left
     auto begin = [&](uint32_t u, bool &fresh) -> uint32_t {
-        while (u >= prefix[b + 1]) ++b;
+        while (u >= prefix[b + 1].y) ++b;
         AtSeq q;
         q.init(a, b, C::R, err, false);
-        const uint32_t r = u - prefix[b], it = r / q.nb;
+        const uint32_t r = u - prefix[b].y, it = r / q.nb;
         const int tile = (int)it / H;
         h = (int)it - tile * H;
         blk = q.b_lo + (r - it * q.nb);
         fresh = blk == q.b_lo;                                // the pass begins here
         const uint32_t left = q.nb - (r - it * q.nb);
+        last = prefix[b].x + (it + 1) * (q.nb + kAtExtra) - 1;
         tok = q.lo;
         r0 = tile * C::R;
         nrow = min(C::R, q.n * G - r0);
@@ -548,26 +575,25 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
       }
       const bool on = (uint32_t)(k - k0) < left;              // the pass goes on with the next workers
       end(fresh && !on, on);
-      if (fresh && on) join = AtJoin{nrow, (int)shares.owner(u0 + k0 + left - 1), h, r0, tok};
+      if (fresh && on) join = AtJoin{nrow, (int)shares.owner(last), h, r0, tok};
     }
     if (lane == 0) a.join[worker] = join;
 }
 
-// Joins the partials of the row passes that several workers share.  A CTA looks at 8 workers (a lane each) and joins one row (the grid's
-// y) of the passes that those began; its warps take every eighth partial each.
-constexpr int kJoinWarps = 8;
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(AtArgs a, int R) {
-    constexpr int V = D / 32, JW = kJoinWarps;
-    __shared__ float s_o[JW - 1][D], s_ml[JW][2];
+// Joins one row (the grid's y) of the row passes that several workers share.  Few partials each (FEW): a warp looks at one worker and joins
+// what it began alone.  Many: a CTA looks at 8 workers, a lane each, and its 8 warps take every eighth partial.
+template <typename T, int D, bool FEW>
+__global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a, int R) {
+    constexpr int V = D / 32, JW = FEW ? 1 : 8;
+    __shared__ float s_o[FEW ? 1 : JW - 1][D], s_ml[JW][2];
     grid_dep_launch();
     grid_dep_wait();
-    const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t workers = min((uint32_t)a.workers, *a.total), mine = blockIdx.x + lane * gridDim.x;
+    const int row = blockIdx.y, lane = threadIdx.x & 31, warp = FEW ? 0 : threadIdx.x >> 5;
+    const int mine = FEW ? blockIdx.x * 4 + (threadIdx.x >> 5) : lane < 8 ? blockIdx.x * 8 + lane : a.workers;
     AtJoin w = {0, 0, 0, 0, 0};
-    if (mine < workers) w = a.join[mine];
+    if (mine < a.workers && (!FEW || lane == 0)) w = a.join[mine];
     for (uint32_t todo = __ballot_sync(0xffffffffu, row < w.nrow); todo != 0; todo &= todo - 1) {
-        const int from = __ffs(todo) - 1, first = blockIdx.x + from * gridDim.x;
+        const int from = __ffs(todo) - 1, first = __shfl_sync(0xffffffffu, mine, from);
         const int last = __shfl_sync(0xffffffffu, w.last, from), n = last - first + 1;
         const float *base = a.part + row * (int64_t)(D + 4);
         auto part = [&](int c) { return base + (2 * (int64_t)c + (c < last)) * R * (D + 4); };
@@ -594,38 +620,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(AtArgs a,
             for (int j = 0; j < cnt; ++j) {
                 const float fj = __shfl_sync(0xffffffffu, f, j);
                 const float *src = part(first + p0 + JW * j) + V * lane;
+                float y[V];
+                if constexpr (V == 4) load4(src, y);
+                else *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(src);
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] += fj * src[e];
+                for (int e = 0; e < V; ++e) acc[e] += fj * y[e];
             }
         }
-        if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = ll;
-        if (warp > 0) {
+        float sum = ll;
+        if constexpr (!FEW) {
+            if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = ll;
+            if (warp > 0) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) s_o[warp - 1][V * lane + e] = acc[e];
+                for (int e = 0; e < V; ++e) s_o[warp - 1][V * lane + e] = acc[e];
+            }
+            __syncthreads();
+            if (warp == 0) {
+                float all = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < JW; ++x) all = fmaxf(all, s_ml[x][0]);
+                const float mb = all == -INFINITY ? 0.0f : all;
+                sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < JW; ++x) {
+                    const float f = exp2_approx(s_ml[x][0] - mb);
+                    sum += s_ml[x][1] * f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = x == 0 ? acc[e] * f : acc[e] + s_o[x - 1][V * lane + e] * f;
+                }
+            }
         }
-        __syncthreads();
+        const int r0 = __shfl_sync(0xffffffffu, w.r0, from), h = __shfl_sync(0xffffffffu, w.h, from);
+        const int64_t tok = __shfl_sync(0xffffffffu, w.tok, from);
         if (warp == 0) {
-            float all = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < JW; ++x) all = fmaxf(all, s_ml[x][0]);
-            const float mb = all == -INFINITY ? 0.0f : all;
-            float sum = 0.0f;
-#pragma unroll
-            for (int x = 0; x < JW; ++x) {
-                const float f = exp2_approx(s_ml[x][0] - mb);
-                sum += s_ml[x][1] * f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = x == 0 ? acc[e] * f : acc[e] + s_o[x - 1][V * lane + e] * f;
-            }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int r0 = __shfl_sync(0xffffffffu, w.r0, from), h = __shfl_sync(0xffffffffu, w.h, from);
-            const int64_t tok = __shfl_sync(0xffffffffu, w.tok, from);
             const int i = (r0 + row) / a.group;
             T *dst = static_cast<T *>(a.out) + (tok + i) * a.ot + (int64_t)(h * a.group + (r0 + row - i * a.group)) * a.oh + V * lane;
 #pragma unroll
-            for (int e = 0; e < V; ++e) dst[e] = T(acc[e] * inv);
+            for (int e = 0; e < V; ++e) acc[e] *= inv;
+            if constexpr (V == 4) {
+                store4(dst, acc);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) dst[e] = T(acc[e]);
+            }
         }
-        __syncthreads();
+        if constexpr (!FEW) __syncthreads();
     }
 }
 
@@ -659,22 +699,26 @@ int64_t share_ctas(int32_t n_seqs, int32_t H, int dtype, int64_t rows, int64_t m
     const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = 2 * sm_count();
     return (units + kAtWarps - 1) / kAtWarps < most ? (units + kAtWarps - 1) / kAtWarps : most;
 }
-size_t plan_bytes(int32_t n_seqs, size_t workers) { return (256 + (((size_t)n_seqs + 4) & ~size_t(3)) * 4 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
+size_t plan_bytes(int32_t n_seqs, size_t workers) { return (256 + (((size_t)n_seqs + 4) & ~size_t(3)) * 8 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
 
 template <typename T, int D, int MT>
 int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t ctas, unsigned int *err, cudaStream_t s) {
     using C = AtCfg<T, D, MT>;
     const int slot = kAttrSlotKv + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128) + (MT == 2 ? 16 : 0);
     const bool in_smem = a.c.n_seqs <= kAtSmemSeqs;
-    int rc = ensure_smem_attr(reinterpret_cast<const void *>(&kv_attn_kernel<T, D, MT>), C::SMEM + 4 * (kAtSmemSeqs + 1), slot);
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(&kv_attn_kernel<T, D, MT>), C::SMEM + 8 * (kAtSmemSeqs + 1), slot);
     if (rc == MQ_OK && !in_smem)
         rc = cuda_error(launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(1024), 0, s, a, (int)C::R, err), "mqkv_attention plan launch");
     if (rc != MQ_OK) return rc;
-    const size_t smem = C::SMEM + (in_smem ? 4 * (a.c.n_seqs + 1) : 0);
+    const size_t smem = C::SMEM + (in_smem ? 8 * (a.c.n_seqs + 1) : 0);
     rc = cuda_error(launch_pdl(kv_attn_kernel<T, D, MT>, dim3((unsigned)ctas), dim3(kAtThreads), smem, s, tm, a, err), "mqkv_attention launch");
     if (rc != MQ_OK) return rc;
-    const int rows = a.max_q * a.group;
-    return cuda_error(launch_pdl(kv_attn_join_kernel<T, D>, dim3((unsigned)((a.workers + 7) / 8), (unsigned)(rows < C::R ? rows : C::R)), dim3(32 * kJoinWarps), 0, s, a, (int)C::R),
+    const unsigned rows = (unsigned)(a.max_q * a.group < C::R ? a.max_q * a.group : C::R);
+    // many partials to a pass: from 16 on
+    if (a.workers >= 16 * (int64_t)a.c.n_seqs * a.c.H)
+        return cuda_error(launch_pdl(kv_attn_join_kernel<T, D, false>, dim3((unsigned)(a.workers + 7) / 8, rows), dim3(256), 0, s, a, (int)C::R),
+                          "mqkv_attention join launch");
+    return cuda_error(launch_pdl(kv_attn_join_kernel<T, D, true>, dim3((unsigned)(a.workers + 3) / 4, rows), dim3(128), 0, s, a, (int)C::R),
                       "mqkv_attention join launch");
 }
 template <typename T>
@@ -709,7 +753,7 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
     a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
     a.total = static_cast<uint32_t *>(ws);
     a.prefix = a.total + 64;
-    a.join = reinterpret_cast<AtJoin *>(a.prefix + ((c.n_seqs + 4) & ~3));
+    a.join = reinterpret_cast<AtJoin *>(a.prefix + 2 * ((c.n_seqs + 4) & ~3));
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes(c.n_seqs, (size_t)a.workers));
     const int tiles = pass_tiles(p.dtype, rows);
     return p.dtype == MQKV_F32   ? attn_d<float>(tm, a, tiles, ctas, err, s)

@@ -169,39 +169,41 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(KvPages p, const 
         if (c >= 0 && c < p.n_seqs) atomicMin(&ws.src[c], i);
     }
     __syncthreads();
-    int need = 0;
-    for (int base = 0; base < n; base += kPlanThreads) {
-        const int i = base + threadIdx.x;
-        int k = 0, len = -1;
-        if (i < n) {
-            const int a = parent[i], c = child[i];
-            if (a < 0 || a >= p.n_seqs || c < 0 || c >= p.n_seqs || ws.src[c] != i || p.len[c] != 0) {
-                kv_error(err, KV_ERR_SEQ);
+    // a warp per pair: its ids, its parent's length and pages; blocks[] gets the length, -1 for a pair that is left out
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        const int a = parent[i], c = child[i];
+        int len = -1;
+        if (a < 0 || a >= p.n_seqs || c < 0 || c >= p.n_seqs || ws.src[c] != i || p.len[c] != 0) {
+            if (lane == 0) kv_error(err, KV_ERR_SEQ);
+        } else {
+            len = p.len[a];
+            const int64_t held = ((int64_t)len + T - 1) >> p.tshift;
+            if (len < 0 || held > p.max_pages) {
+                if (lane == 0) kv_error(err, KV_ERR_LEN);
+                len = -1;
             } else {
-                len = p.len[a];
-                const int64_t held = ((int64_t)len + T - 1) >> p.tshift;
-                if (len < 0 || held > p.max_pages) {
-                    kv_error(err, KV_ERR_LEN);
+                bool bad = false;
+                for (int s = lane; s < held; s += 32) {
+                    const int page = p.table[(int64_t)a * p.max_pages + s];
+                    bad = bad || page < 0 || page >= p.n_pages;
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+                    if (lane == 0) kv_error(err, KV_ERR_PAGE);
                     len = -1;
-                } else {
-                    for (int s = 0; s < held; ++s) {
-                        const int page = p.table[(int64_t)a * p.max_pages + s];
-                        if (page < 0 || page >= p.n_pages) {
-                            kv_error(err, KV_ERR_PAGE);
-                            len = -1;
-                            break;
-                        }
-                    }
-                    k = len > 0 && (len & (T - 1)) != 0;
                 }
             }
         }
+        if (lane == 0) ws.blocks[i] = len;
+    }
+    __syncthreads();
+    int need = 0;
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int i = base + threadIdx.x;
+        const int len = i < n ? ws.blocks[i] : -1, k = len > 0 && (len & (T - 1)) != 0;
         int total;
         const int at = need + block_scan(k, s_warp, &total);
-        if (i < n) {
-            ws.blocks[i] = len;
-            ws.prefix[i] = k ? at : -1;
-        }
+        if (i < n) ws.prefix[i] = k ? at : -1;
         need += total;
     }
     __syncthreads();
@@ -212,7 +214,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(KvPages p, const 
         }
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = warp; i < n; i += kPlanThreads / 32) {
         const int len = ws.blocks[i], at = ws.prefix[i];
         if (len <= 0) continue;
@@ -286,10 +287,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(KvPages p, Ws 
     if (threadIdx.x == 0) ws.plan->n = movers;
 }
 
-__global__ void __launch_bounds__(256) kv_remap_kernel(KvPages p, Ws ws, unsigned int *err) {
-    grid_dep_launch();
-    grid_dep_wait();
-    const int b = blockIdx.x, T = 1 << p.tshift;
+// the table row of sequence b after pages have moved
+__device__ __forceinline__ void remap_row(const KvPages &p, const Ws &ws, int b, unsigned int *err) {
+    const int T = 1 << p.tshift;
     const int64_t held = ((int64_t)p.len[b] + T - 1) >> p.tshift;
     if (held < 0 || held > p.max_pages) {
         if (threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
@@ -320,12 +320,14 @@ __device__ __forceinline__ void copy_span(uint8_t *dst, const uint8_t *src, int 
     }
 }
 
-// whole pages in pieces of 16 KB; n < 0: the count is the plan's
-__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages p, const int32_t *src, const int32_t *dst, int n, const CopyPlan *plan,
-                                                               unsigned int *err) {
+// whole pages in pieces of 16 KB; n < 0: a compaction's plan, whose tables it also brings up to date
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages p, const int32_t *src, const int32_t *dst, int n, Ws ws, unsigned int *err) {
     grid_dep_launch();
     grid_dep_wait();
-    if (n < 0) n = plan->n;
+    if (n < 0) {
+        for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) remap_row(p, ws, b, err);
+        n = ws.plan->n;
+    }
     const int64_t per = (p.page_bytes + kCopyChunk - 1) / kCopyChunk;
     for (int64_t u = blockIdx.x; u < n * per; u += gridDim.x) {
         const int64_t i = u / per, off = (u - i * per) * kCopyChunk;
@@ -339,23 +341,20 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages p, const 
     }
 }
 
-// the used blocks of partly filled pages: a unit is one (page, layer), its 2 H runs of codes and its scales
+// the used blocks of partly filled pages: a unit is one (page, layer) and one of its 2 H runs of codes (the first takes the scales too)
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_used_kernel(KvPages p, Ws ws) {
     grid_dep_launch();
     grid_dep_wait();
-    const int n = ws.plan->n, T = 1 << p.tshift;
-    for (int64_t u = blockIdx.x; u < (int64_t)n * p.n_layers; u += gridDim.x) {
-        const int i = (int)(u / p.n_layers), layer = (int)(u - (int64_t)i * p.n_layers);
+    const int n = ws.plan->n, T = 1 << p.tshift, runs = 2 * p.H;
+    for (int64_t u = blockIdx.x; u < (int64_t)n * p.n_layers * runs; u += gridDim.x) {
+        const int64_t page = u / runs;
+        const int run = (int)(u - page * runs), i = (int)(page / p.n_layers), layer = (int)(page - (int64_t)i * p.n_layers);
         const uint8_t *s = p.pool + ws.src[i] * p.page_bytes + layer * p.layer_bytes;
         uint8_t *d = p.pool + ws.dst[i] * p.page_bytes + layer * p.layer_bytes;
-        const int used = ws.list[i] * kKB * p.D, q = used >> 4;      // bytes, 16-byte pieces of one run
-        const int scales = 2 * p.H * (T / kKB);
-        for (int j = threadIdx.x; j < 2 * p.H * q; j += kCopyThreads) {
-            const int run = j / q, o = run * T * p.D + (j - run * q) * 16;
-            *reinterpret_cast<uint4 *>(d + o) = *reinterpret_cast<const uint4 *>(s + o);
-        }
-        for (int j = threadIdx.x; j < scales; j += kCopyThreads)
-            reinterpret_cast<uint32_t *>(d + p.off_s)[j] = reinterpret_cast<const uint32_t *>(s + p.off_s)[j];
+        copy_span(d + run * T * p.D, s + run * T * p.D, ws.list[i] * kKB * p.D);
+        if (run == 0)
+            for (int j = threadIdx.x; j < runs * (T / kKB); j += kCopyThreads)
+                reinterpret_cast<uint32_t *>(d + p.off_s)[j] = reinterpret_cast<const uint32_t *>(s + p.off_s)[j];
     }
 }
 
@@ -377,7 +376,7 @@ int kv_launch_fork(const KvPages &p, const int32_t *parent, const int32_t *child
     const Ws w(ws, p.n_pages, p.n_seqs);
     int rc = cuda_error(launch_pdl(kv_fork_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, parent, child, n, w, err), "mqkv_fork plan launch");
     if (rc != MQ_OK) return rc;
-    const int64_t units = (int64_t)n * p.n_layers;
+    const int64_t units = (int64_t)n * p.n_layers * 2 * p.H;
     const int grid = (int)(units < 8 * sm_count() ? units : 8 * sm_count());
     return cuda_error(launch_pdl(kv_copy_used_kernel, dim3(grid), dim3(kCopyThreads), 0, s, p, w), "mqkv_fork copy launch");
 }
@@ -386,15 +385,13 @@ int kv_launch_compact(const KvPages &p, void *ws, unsigned int *err, cudaStream_
     const Ws w(ws, p.n_pages, p.n_seqs);
     int rc = cuda_error(launch_pdl(kv_compact_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, w, err), "mqkv_compact plan launch");
     if (rc != MQ_OK) return rc;
-    rc = cuda_error(launch_pdl(kv_remap_kernel, dim3(p.n_seqs), dim3(256), 0, s, p, w, err), "mqkv_compact table launch");
-    if (rc != MQ_OK) return rc;
     return cuda_error(launch_pdl(kv_copy_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, (const int32_t *)w.src,
-                                 (const int32_t *)w.dst, -1, (const CopyPlan *)w.plan, err),
+                                 (const int32_t *)w.dst, -1, w, err),
                       "mqkv_compact copy launch");
 }
 
 int kv_launch_copy(const KvPages &p, const int32_t *src, const int32_t *dst, int n, unsigned int *err, cudaStream_t s) {
-    return cuda_error(launch_pdl(kv_copy_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, src, dst, n, (const CopyPlan *)nullptr, err),
+    return cuda_error(launch_pdl(kv_copy_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, src, dst, n, Ws(nullptr, 0, 0), err),
                       "mqkv_copy_pages launch");
 }
 

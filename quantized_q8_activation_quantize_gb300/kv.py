@@ -7,7 +7,6 @@ tensors they describe), ``alloc_*`` the memory a user owns.  As in ``binding``, 
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import re
 
@@ -75,17 +74,35 @@ def lib():
     return _L
 
 
-_DTYPES = None
+_DTYPES = {}
+_int32 = _raw_stream = None
+
+
+def _torch():
+    """What of torch the calls need, resolved on the first one (the package imports without torch)."""
+    global _int32, _raw_stream
+    import torch
+    _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    _int32 = torch.int32
+    # the current stream's handle without making a Stream object of it (3 us a call); the public way where there is none
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(stream, t):
+    """The handle of a stream, None: the current one of the tensor's device."""
+    if stream is None:
+        if _raw_stream is None:
+            _torch()
+        return _raw_stream(t.get_device())
+    return _stream(stream)
 
 
 def _dtype(t) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    d = _DTYPES.get(t if not hasattr(t, "dtype") else t.dtype)
+    if not _DTYPES:
+        _torch()
+    d = _DTYPES.get(t)
     if d is None:
-        raise MQError(MQ_ERR_ARG, f"dtype {getattr(t, 'dtype', t)} is none of float32, float16, bfloat16")
+        raise MQError(MQ_ERR_ARG, f"dtype {t} is none of float32, float16, bfloat16")
     return d
 
 
@@ -93,14 +110,14 @@ def _bad(message):
     raise MQError(MQ_ERR_ARG, message)
 
 
-def _rows(name, t, heads, dim, n=None):
-    """(pointer, token stride, head stride) of a [tokens, heads, dim] CUDA tensor."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (n is not None and t.shape[0] != n):
-        _bad(f"{name} has shape {tuple(t.shape)}, [{'tokens' if n is None else n}, {heads}, {dim}] wanted")
+def _rows(name, t, n, heads, dim):
+    """(pointer, token stride, head stride) of a [n, heads, dim] CUDA tensor."""
+    if t.shape != (n, heads, dim):
+        _bad(f"{name} has shape {tuple(t.shape)}, [{n}, {heads}, {dim}] wanted")
     if not t.is_cuda:
         _bad(f"{name} is not a CUDA tensor")
     a, b, c = t.stride()
-    if c != 1 and t.numel():
+    if c != 1 and n:
         _bad(f"{name}: head_dim is not contiguous (strides {t.stride()})")
     return t.data_ptr(), a, b
 
@@ -108,8 +125,9 @@ def _rows(name, t, heads, dim, n=None):
 def _i32(name, t, n=None):
     if t is None:
         return None
-    import torch
-    if t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda or (n is not None and t.numel() != n):
+    if _int32 is None:
+        _torch()
+    if t.dtype is not _int32 or not t.is_contiguous() or not t.is_cuda or (n is not None and t.numel() != n):
         _bad(f"{name} is not a contiguous int32 CUDA tensor{'' if n is None else f' of {n}'}")
     return t.data_ptr()
 
@@ -178,11 +196,12 @@ def alloc_pages_workspace(cache, seqs):
 def mqkv_append(cache, seqs, layer: int, k, v, cu=None, stream=None):
     """k, v [tokens, n_kv_heads, head_dim] are the last tokens of their sequences (cu int32 [n_seqs + 1], or as many
     for each)."""
-    n, H, D = k.shape[0], cache.n_kv_heads, cache.head_dim
-    if v.dtype is not k.dtype:
-        _bad(f"k is {k.dtype}, v is {v.dtype}")
-    return _check(lib().mqkv_append(cache, seqs, layer, _dtype(k), *_rows("k", k, H, D), *_rows("v", v, H, D, n),
-                                    _i32("cu", cu, seqs.n_seqs + 1), n, _stream(stream)))
+    n, H, D = len(k), cache.n_kv_heads, cache.head_dim
+    dtype = k.dtype
+    if v.dtype is not dtype:
+        _bad(f"k is {dtype}, v is {v.dtype}")
+    return _check((_L or lib()).mqkv_append(cache, seqs, layer, _dtype(dtype), *_rows("k", k, n, H, D), *_rows("v", v, n, H, D),
+                                            _i32("cu", cu, seqs.n_seqs + 1), n, _on(stream, k)))
 
 
 def mqkv_read(cache, seqs, layer: int, k, v, cu=None, start=None, stream=None):
@@ -191,49 +210,52 @@ def mqkv_read(cache, seqs, layer: int, k, v, cu=None, start=None, stream=None):
     t = k if k is not None else v
     if t is None:
         _bad("both outputs are None")
-    n, H, D = t.shape[0], cache.n_kv_heads, cache.head_dim
+    n, H, D = len(t), cache.n_kv_heads, cache.head_dim
     if k is not None and v is not None and v.dtype is not k.dtype:
         _bad(f"k is {k.dtype}, v is {v.dtype}")
     none = (None, 0, 0)
-    return _check(lib().mqkv_read(cache, seqs, layer, _dtype(t), *(none if k is None else _rows("k", k, H, D, n)),
-                                  *(none if v is None else _rows("v", v, H, D, n)), _i32("cu", cu, seqs.n_seqs + 1),
-                                  _i32("start", start, seqs.n_seqs), n, _stream(stream)))
+    return _check((_L or lib()).mqkv_read(cache, seqs, layer, _dtype(t.dtype), *(none if k is None else _rows("k", k, n, H, D)),
+                                          *(none if v is None else _rows("v", v, n, H, D)), _i32("cu", cu, seqs.n_seqs + 1),
+                                          _i32("start", start, seqs.n_seqs), n, _on(stream, t)))
 
 
 def mqkv_attention(cache, seqs, layer: int, q, out, cu, max_q: int, max_kv: int, workspace, causal: bool = True,
                    window: int = 0, scale: float | None = None, stream=None):
     """out = softmax(scale q K^T + mask) V for q, out [tokens, n_q_heads, head_dim]; scale None: 1 / sqrt(head_dim)."""
-    n, D = q.shape[0], cache.head_dim
-    heads = q.shape[1] if q.dim() == 3 else 0
-    if out.dtype is not q.dtype:
-        _bad(f"q is {q.dtype}, out is {out.dtype}")
-    return _check(lib().mqkv_attention(cache, seqs, layer, _dtype(q), *_rows("q", q, heads, D), *_rows("out", out, heads, D, n),
-                                       heads, _i32("cu", cu, seqs.n_seqs + 1), n, max_q, max_kv, bool(causal), window,
-                                       1 / math.sqrt(D) if scale is None else scale, workspace.data_ptr(), workspace.numel(),
-                                       _stream(stream)))
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        _bad(f"q has shape {tuple(shape)}, [tokens, heads, head_dim] wanted")
+    n, heads, D = shape[0], shape[1], cache.head_dim
+    if out.dtype is not dtype:
+        _bad(f"q is {dtype}, out is {out.dtype}")
+    return _check((_L or lib()).mqkv_attention(cache, seqs, layer, _dtype(dtype), *_rows("q", q, n, heads, D),
+                                               *_rows("out", out, n, heads, D), heads, _i32("cu", cu, seqs.n_seqs + 1), n, max_q,
+                                               max_kv, causal, window, D ** -0.5 if scale is None else scale,
+                                               workspace.data_ptr(), workspace.numel(), _on(stream, q)))
 
 
 def mqkv_extend(cache, seqs, add, workspace, stream=None):
     """kv_len += add (int32 [n_seqs]; None: 1), with pages for the new tokens."""
-    return _check(lib().mqkv_extend(cache, seqs, _i32("add", add, seqs.n_seqs), workspace.data_ptr(), workspace.numel(),
-                                    _stream(stream)))
+    return _check((_L or lib()).mqkv_extend(cache, seqs, _i32("add", add, seqs.n_seqs), workspace.data_ptr(), workspace.numel(),
+                                            _on(stream, workspace)))
 
 
 def mqkv_release(cache, seqs, ids, stream=None):
-    return _check(lib().mqkv_release(cache, seqs, _i32("ids", ids), ids.numel(), _stream(stream)))
+    return _check((_L or lib()).mqkv_release(cache, seqs, _i32("ids", ids), ids.numel(), _on(stream, ids)))
 
 
 def mqkv_fork(cache, seqs, parent, child, workspace, stream=None):
-    return _check(lib().mqkv_fork(cache, seqs, _i32("parent", parent), _i32("child", child, parent.numel()), parent.numel(),
-                                  workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    n = parent.numel()
+    return _check((_L or lib()).mqkv_fork(cache, seqs, _i32("parent", parent), _i32("child", child, n), n, workspace.data_ptr(),
+                                          workspace.numel(), _on(stream, workspace)))
 
 
 def mqkv_compact(cache, seqs, workspace, stream=None):
-    return _check(lib().mqkv_compact(cache, seqs, workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return _check((_L or lib()).mqkv_compact(cache, seqs, workspace.data_ptr(), workspace.numel(), _on(stream, workspace)))
 
 
 def mqkv_copy_pages(cache, src, dst, stream=None):
-    return _check(lib().mqkv_copy_pages(cache, _i32("src", src), _i32("dst", dst, src.numel()), src.numel(), _stream(stream)))
+    return _check((_L or lib()).mqkv_copy_pages(cache, _i32("src", src), _i32("dst", dst, src.numel()), src.numel(), _on(stream, src)))
 
 
 def mqkv_device_status(stream=None):
