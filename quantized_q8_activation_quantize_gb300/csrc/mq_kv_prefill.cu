@@ -18,8 +18,8 @@
 //
 // f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
 // The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
-// each tile's P V goes to a fresh accumulator and warps 4-7 add it to the row's sum in registers, rounding to nearest,
-// under the products of the next tile: one row tile per CTA, S and O double-buffered.
+// each tile's P V goes to a fresh accumulator and is added to the row's sum in registers, rounding to nearest, under the
+// products of the next tiles: one row tile per CTA, S and O double-buffered, warps 0-3 and 4-7 the softmax of the tiles in turn.
 #include <cuda.h>
 
 #include <climits>
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kPfThreads = 512;
 constexpr int kPfN = 128;                      // tokens of a tile
-constexpr int kPfSlots = 5;                    // f16 operand tiles in flight
+constexpr int kPfSlots = 5;                    // f16 operand tiles in flight at most
 constexpr int kPfInfo = 4;                     // tiles that the lookup runs ahead
 
 struct PfArgs {
@@ -58,16 +58,17 @@ struct PfInfo {
 template <int D, bool TWO>
 struct PfCfg {
     static constexpr int PARTS = TWO ? 2 : 1, TILES = TWO ? 1 : 2, ROWS = 128 * TILES;
+    static constexpr int SLOTS = TWO ? 4 : 5;                  // f16 operand tiles in flight
     static constexpr int OPT = kPfN * D * 2;
     static constexpr int QT = 128 * D * 2;                     // one part of one row tile
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_OP = OFF_Q + PARTS * TILES * QT;
-    static constexpr int OFF_RS = OFF_OP + kPfSlots * OPT;     // row scales [ROWS]; f32 rows: then factors [2][128]
-    static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 256 * 4 : 0);
+    static constexpr int OFF_RS = OFF_OP + SLOTS * OPT;     // row scales [ROWS]; f32 rows: then factors and maxima [4][128]
+    static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 2 * 512 * 4 : 0);
     static constexpr int OFF_BAR = OFF_INFO + kPfInfo * (int)sizeof(PfInfo);
-    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 4 * 2 + 2;
+    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int SMEM = OFF_MISC + 16 + 1008;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA exceeds the per-CTA limit");
     static constexpr uint32_t COL_S = 0, COL_O = 256;
 };
@@ -124,6 +125,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
     }
     return true;
 }
+// two barriers at once: each probe costs 130 to 150 clocks, side by side they cost one
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint64_t *bar2, uint32_t parity, uint32_t parity2, unsigned int *err, volatile int *abort) {
+    const bool one = mbar_try_wait(smem_u32(bar), parity), two = mbar_try_wait(smem_u32(bar2), parity2);
+    if (__all_sync(0xffffffffu, one && two)) return true;
+    return warp_wait(bar, parity, err, abort) && warp_wait(bar2, parity2, err, abort);
+}
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint64_t *bar2, uint32_t parity, unsigned int *err, volatile int *abort) {
+    return warp_wait2(bar, bar2, parity, parity, err, abort);
+}
 // one arrival for the warp, after what its lanes did
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -131,18 +141,19 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 }
 
 struct PfBars {
-    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *drain, *l_full;
+    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full;
     __device__ __forceinline__ explicit PfBars(uint64_t *b) {
         op_full = b, op_empty = op_full + kPfSlots, info_full = op_empty + kPfSlots, info_empty = info_full + kPfInfo;
-        s_full = info_empty + kPfInfo, p_full = s_full + 2, o_done = p_full + 2, o_free = o_done + 2, drain = o_free + 2, l_full = drain + 1;
+        s_full = info_empty + kPfInfo, p_full = s_full + 2, o_done = p_full + 2, o_free = o_done + 2, m_full = o_free + 2, drain = m_full + 2;
+        l_full = drain + 1;
     }
     // info_readers: warps that read a tile's lookup
     __device__ __forceinline__ void init(int info_readers) {
         for (int i = 0; i < kPfSlots; ++i) mbar_init(op_full + i, 2), mbar_init(op_empty + i, 1);
         for (int i = 0; i < kPfInfo; ++i) mbar_init(info_full + i, 1), mbar_init(info_empty + i, info_readers);
-        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 4), mbar_init(o_done + i, 1), mbar_init(o_free + i, 4);
+        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 4), mbar_init(o_done + i, 1), mbar_init(o_free + i, 8), mbar_init(m_full + i, 4);
         mbar_init(drain, 1);
-        mbar_init(l_full, 4);
+        mbar_init(l_full, 8);
         mbar_init_fence();
     }
 };
@@ -304,7 +315,7 @@ __device__ __forceinline__ int pf_order(int j, int half, int nj) { return half ?
 template <int D, bool TWO>
 __device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8_t *ops, const PfInfo *info, const PfBars &bar, unsigned int *err,
                                          volatile int *abort) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = kKB / RPI, NV = 8 / RPI, OPT = PfCfg<D, TWO>::OPT;   // lanes per row, rows per load, loads
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = kKB / RPI, NV = 8 / RPI, OPT = PfCfg<D, TWO>::OPT, SLOTS = PfCfg<D, TWO>::SLOTS;   // lanes per row, rows per load, loads
     const int wi = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, half = wi >> 1, blk0 = 2 * (wi & 1), u = lane % LPR;
     uint32_t off[NV];                                          // this lane's unit in rows 0 .. 7 of its first block
 #pragma unroll
@@ -341,8 +352,8 @@ __device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8
         if (more) {
             if (!locate(j + 1)) break;
         }
-        const int n = pf_order(j, half, w.nj), slot = n % kPfSlots;
-        if (n >= kPfSlots && !warp_wait(bar.op_empty + slot, (n / kPfSlots - 1) & 1, err, abort)) break;
+        const int n = pf_order(j, half, w.nj), slot = n % SLOTS;
+        if (n >= SLOTS && !warp_wait(bar.op_empty + slot, (n / SLOTS - 1) & 1, err, abort)) break;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const __half2 f = __float2half2_rn(256.0f * pv[z]);
@@ -409,10 +420,10 @@ struct PfMma {
 #pragma unroll 1
         for (int i = 0; i < 2 * C::PARTS; ++i) {               // 64 tokens of one part; the smaller part first
             const uint32_t part = i < 2 ? C::PARTS - 1 : 0, ht = i & 1;
-            const uint32_t pi = p + (TWO ? ht * 64 + part * 32 : ht * 32), vi = v + ht * 512;
+            const uint32_t pi = p + (TWO ? ht * 64 + part * 16 : ht * 32), vi = v + ht * 512;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                mma_f16_ts_warp(d, pi + 8 * e, desc(vi + 128 * e), ID_O, more);
+                mma_f16_ts_warp(d, pi + (TWO ? 32 * (e >> 1) + 8 * (e & 1) : 8 * e), desc(vi + 128 * e), ID_O, more);
                 more = 1;
             }
         }
@@ -480,17 +491,16 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&s)[32], float kb, ui
             f2_unpack(f2_mul(p, pp), x, y);
             w[k >> 1] = pack_f16(x, y);
             const float2 z = unpack_f16(w[k >> 1]);
-            v[k >> 1] = pack_f16(x - z.x, y - z.y);
+            f2_unpack(f2_fma(f2_pack(z.x, z.y), f2_pack(-1.0f, -1.0f), f2_pack(x, y)), x, y);
+            v[k >> 1] = pack_f16(x, y);
         } else {
             w[k >> 1] = pack_f16(x, y);
         }
     }
     l2 = f2_add(l2, f2_add(acc[0], acc[1]));
 }
-// the weights of the tile, written over the scores that have been read: f16 rows 32 columns per 64 scores from the front, f32 rows 32 of leading parts and
-// 32 of the rest in place of each 64
-template <bool TWO>
-__device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4], const float (&pb)[4], float off, uint64_t &l2) {
+// the weights of the tile, written over the scores that have been read.  16-bit rows: 32 columns per 64 scores, from the front
+__device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4], float off, uint64_t &l2) {
     const uint64_t off2 = f2_pack(off, off);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
@@ -498,10 +508,34 @@ __device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4
         pf_load_scores(ts + 64 * e, s);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            pf_weights<TWO>(s[z], e ? kb[2 + z] : kb[z], off2, e ? pb[2 + z] : pb[z], l2, w, v);
-            tmem_st16(ts + (TWO ? 64 : 32) * e + 16 * z, w);
-            if constexpr (TWO) tmem_st16(ts + 64 * e + 32 + 16 * z, v);
+            pf_weights<false>(s[z], e ? kb[2 + z] : kb[z], off2, 1.0f, l2, w, v);
+            tmem_st16(ts + 32 * e + 16 * z, w);
         }
+    }
+}
+// f32 rows, a block of 32 tokens at a time: its 16 columns of leading parts and 16 of the rest in the scores' place
+__device__ __forceinline__ float pf_score_factor(float rs, float dk) { return fmaxf(rs * dk, 0x1p-120f); }
+__device__ __forceinline__ float pf_tile_max_f32(uint32_t ts, float rs, const PfInfo &o) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int e = 0; e < 4; e += 2) {
+        uint32_t s[2][32];
+        pf_load_scores(ts + 32 * e, s);
+        mx = max3(mx, pf_max32(s[0]) * pf_score_factor(rs, o.dk[e]), pf_max32(s[1]) * pf_score_factor(rs, o.dk[e + 1]));
+    }
+    return mx;
+}
+__device__ __forceinline__ void pf_tile_weights_f32(uint32_t ts, float rs, const PfInfo &o, float off, uint64_t &l2) {
+    const uint64_t off2 = f2_pack(off, off);
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+        uint32_t s[32], w[16], v[16];
+        tmem_ld32(ts + 32 * e, s);
+        const float kb = pf_score_factor(rs, o.dk[e]), pv = o.pv[e];
+        tmem_ld_wait();
+        pf_weights<true>(s, kb, off2, pv, l2, w, v);
+        tmem_st16(ts + 32 * e, w);
+        tmem_st16(ts + 32 * e + 16, v);
     }
 }
 
@@ -544,7 +578,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
             uint32_t slot = 0, ph = 0;
             auto next = [&]() {
-                if (++slot == kPfSlots) slot = 0, ph ^= 1;
+                if (++slot == C::SLOTS) slot = 0, ph ^= 1;
             };
             bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
             if (ok) {
@@ -654,7 +688,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                         }
                     }
                 }
-                pf_tile_weights<false>(ts, kb, kb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
+                pf_tile_weights(ts, kb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(bar.p_full + t, lane);
@@ -696,13 +730,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
     }
 }
 
-// f32 rows: one row tile per CTA, every tile's P V summed in registers
+// f32 rows: one row tile per CTA, every tile's P V summed in registers.  The MMAs (2048 clocks per 128 tokens) leave one softmax
+// warpgroup no time (it took 4250, with a second one for the sums: 204 us for the 3314-token prompt), so two share the work.
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, unsigned int *err) {
     PF_PROLOGUE(float, D, 4 + 4);
-    float *s_f = s_rs + 128;                                   // [2][128] factors of what was summed before
+    float *s_f = s_rs + 128, *s_m = s_f + 512;                 // [4 tiles][128] factors of what was summed before, maxima
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 12) {
             pf_lookup<true>(a, w, info, bar, err, abort_flag);
         } else if (warp == 13) {
@@ -710,7 +745,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
             const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
             uint32_t slot = 0, ph = 0;
             auto next = [&]() {
-                if (++slot == kPfSlots) slot = 0, ph ^= 1;
+                if (++slot == C::SLOTS) slot = 0, ph ^= 1;
             };
             bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
             if (ok) {
@@ -747,10 +782,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         pf_widen<D, true>(a, w, sm + C::OFF_OP, info, bar, err, abort_flag);
-    } else if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        const int r = threadIdx.x;
-        const uint32_t ts = tmem + C::COL_S + ((uint32_t)(32 * warp) << 16);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // Two warpgroups take the tiles' softmax in turn, and each sums half of the columns of every tile's P V.
+        const int a2 = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, ts = tmem + C::COL_S + lanes, to = tmem + C::COL_O + a2 * (D / 2) + lanes;
         int v0 = 0, v1 = 0;                                    // what the row sees, from the first tile's start
         if (r < w.nrow && !w.bad) {
             int64_t x, y;
@@ -759,75 +795,79 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
         }
         const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
         const float rs = s_rs[r];
-        float m = -INFINITY, g = 0.0f;
+        float m = -INFINITY, g = 0.0f;                         // the maximum and V scale reference of this warpgroup's last tile
         uint64_t l2 = f2_pack(0.0f, 0.0f);
-        for (int j = 0; j < nj; ++j) {
+        uint64_t acc[D / 4];
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k) acc[k] = f2_pack(0.0f, 0.0f);
+        for (int j = 0; j < nj + 2; ++j) {
             const int at = j & 1;
-            if (!warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag)) break;
+            if (j >= 2) {                                      // half of tile j - 2's products
+                const uint32_t ph = ((j >> 1) - 1) & 1;
+                if (!warp_wait2(bar.p_full + at, bar.o_done + at, ph, err, abort_flag)) break;     // the factors, the products
+                const float f = s_f[((j - 2) & 3) * 128 + r];
+                const uint64_t ff = f2_pack(f, f);
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) {
+                    uint32_t x[32];
+                    tmem_ld32(to + at * D + 32 * e, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        acc[16 * e + (k >> 1)] = f2_fma(acc[16 * e + (k >> 1)], ff, f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                }
+                tc_fence_before();
+                warp_arrive(bar.o_free + at, lane);
+            }
+            if (j >= nj || at != a2) continue;
+            if (!warp_wait2(bar.info_full + j % kPfInfo, bar.s_full + at, (j / kPfInfo) & 1, (j >> 1) & 1, err, abort_flag)) break;
+            tc_fence_after();
             const PfInfo &o = info[j % kPfInfo];
-            const float4 dk = *reinterpret_cast<const float4 *>(o.dk), pv = *reinterpret_cast<const float4 *>(o.pv);
             const float gf = o.gf;
             g = o.g;
-            // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
-            const float kb[4] = {fmaxf(rs * dk.x, 0x1p-120f), fmaxf(rs * dk.y, 0x1p-120f), fmaxf(rs * dk.z, 0x1p-120f), fmaxf(rs * dk.w, 0x1p-120f)};
-            const float pb[4] = {pv.x, pv.y, pv.z, pv.w};
-            warp_arrive(bar.info_empty + j % kPfInfo, lane);
-            if (!warp_wait(bar.s_full + at, (j >> 1) & 1, err, abort_flag)) break;
-            tc_fence_after();
             const int t0 = j * kPfN;
             if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) pf_mask(ts + at * 128, v0 - t0, v1 - t0);
-            const float mx = pf_tile_max(ts + at * 128, kb);
-            const float mn = fmaxf(m, mx), mb = mn == -INFINITY ? 0.0f : mn;
+            const float mx = pf_tile_max_f32(ts + at * 128, rs, o);
+            float before = -INFINITY;                          // the maximum after tile j - 1, from the other warpgroup
+            if (j > 0) {
+                if (!warp_wait(bar.m_full + (at ^ 1), ((j - 1) >> 1) & 1, err, abort_flag)) break;
+                before = s_m[((j - 1) & 3) * 128 + r];
+            }
+            const float mn = fmaxf(before, mx), mb = mn == -INFINITY ? 0.0f : mn;
+            // their places: the other warpgroup has published tile j - 1's, so it has summed tile j - 4 and is done with these
+            s_m[(j & 3) * 128 + r] = mn;
+            s_f[(j & 3) * 128 + r] = exp2_approx(before - mb) * gf;
+            warp_arrive(bar.m_full + at, lane);
             const float f = exp2_approx(m - mb);
             m = mn;
             l2 = f2_mul(l2, f2_pack(f, f));
-            // the factor's place is free once tile j - 2 has been summed
-            if (j >= 2 && !warp_wait(bar.o_free + at, ((j >> 1) - 1) & 1, err, abort_flag)) break;
-            s_f[at * 128 + r] = f * gf;
-            pf_tile_weights<true>(ts + at * 128, kb, pb, kPShift - mb, l2);
+            pf_tile_weights_f32(ts + at * 128, rs, o, kPShift - mb, l2);
+            warp_arrive(bar.info_empty + j % kPfInfo, lane);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(bar.p_full + at, lane);
         }
+        // both warpgroups' sums of weights, relative to the last tile's maximum; V's reference is the last tile's
         float l, l1;
         f2_unpack(l2, l, l1);
         l += l1;
-        s_rs[r] = l == 0.0f ? 0.0f : g / l;                     // (this thread alone read the row's scale)
-        warp_arrive(bar.l_full, lane);
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        const int r = threadIdx.x - 128;
-        const uint32_t to = tmem + C::COL_O + ((uint32_t)(32 * (warp - 4)) << 16);
-        uint64_t acc[D / 2];
-#pragma unroll
-        for (int k = 0; k < D / 2; ++k) acc[k] = f2_pack(0.0f, 0.0f);
-        for (int j = 0; j < nj; ++j) {
-            const int at = j & 1;
-            if (!warp_wait(bar.p_full + at, (j >> 1) & 1, err, abort_flag)) break;     // the factors
-            const float f = s_f[at * 128 + r];
-            const uint64_t ff = f2_pack(f, f);
-            if (!warp_wait(bar.o_done + at, (j >> 1) & 1, err, abort_flag)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-                uint32_t x[32];
-                tmem_ld32(to + at * D + 32 * e, x);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; k += 2)
-                    acc[16 * e + (k >> 1)] = f2_fma(acc[16 * e + (k >> 1)], ff, f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-            }
-            tc_fence_before();
-            warp_arrive(bar.o_free + at, lane);
+        if (nj > 0) {
+            const float last = s_m[((nj - 1) & 3) * 128 + r];
+            l *= exp2_approx(m - (last == -INFINITY ? 0.0f : last));
         }
+        s_m[((nj + 1 - a2) & 3) * 128 + r] = l;                 // two of the places that tiles nj - 1 and nj - 2 did not use
+        if (a2 == ((nj - 1) & 1)) s_rs[r] = g;
+        warp_arrive(bar.l_full, lane);
         warp_wait(bar.l_full, 0, err, abort_flag);
-        const float inv = s_rs[r];
+        l = s_m[((nj + 1) & 3) * 128 + r] + s_m[(nj & 3) * 128 + r];
+        const float inv = l == 0.0f ? 0.0f : s_rs[r] / l;
         if (r < w.nrow) {
             const int64_t i = (w.r0 + r) / a.group;
             const int gq = (int)(w.r0 + r - i * a.group);
-            float *dst = static_cast<float *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh;
+            float *dst = static_cast<float *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh + a2 * (D / 2);
 #pragma unroll
-            for (int k = 0; k < D; k += 4) {
+            for (int k = 0; k < D / 2; k += 4) {
                 float y[4];
                 f2_unpack(acc[k / 2], y[0], y[1]);
                 f2_unpack(acc[k / 2 + 1], y[2], y[3]);

@@ -23,16 +23,16 @@ __device__ __forceinline__ int kv_find_seq(const KvRows &rows, int n_seqs, int64
     return lo;
 }
 
-constexpr int kAppendThreads = 256, kAppendVecs = 4;
+constexpr int kAppendThreads = 256, kAppendVecs = 2, kAppendWarps = 8 / kAppendVecs;    // vectors per CTA, warps per vector
 
-// One CTA per (block of 32 slots, four of the 2 H vectors (half, head)); two warps per vector, 16 slots each, all of a lane's values in
+// One CTA per (block of 32 slots, two of the 2 H vectors (half, head)); four warps per vector, 8 slots each, all of a lane's values in
 // registers between the maximum and the codes.  Unit u of the grid's x belongs to the last sequence b with U(b) <= u,
 // U(b) = begin(b) / 32 + 2 b: a sequence of n tokens touches at most n / 32 + 2 blocks, so the units of the sequences never
 // overlap and need no prefix sum.  Moves 5 (f32) or 3 bytes a value; the new values are asked for before the page is looked up.
 template <typename TIN, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvView c, KvRows rows, const TIN *k, int64_t kt, int64_t kh,
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(KvView c, KvRows rows, const TIN *k, int64_t kt, int64_t kh,
                                                                    const TIN *v, int64_t vt, int64_t vh, unsigned int *err) {
-    constexpr int LPR = D / 4, RPW = 32 / LPR, IT = 16 / RPW;             // lanes per row, rows per warp and step, steps
+    constexpr int LPR = D / 4, RPW = 32 / LPR, IT = kKB / kAppendWarps / RPW;   // lanes per row, rows per warp and step, steps
     __shared__ float s_amax[8];
     grid_dep_launch();
     grid_dep_wait();
@@ -60,19 +60,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvView c, KvR
     const int64_t p0 = len - n, blk = p0 / kKB + (u - u0), s0 = blk * kKB;
     if (s0 >= len) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane % LPR;
-    const int vec = blockIdx.y * kAppendVecs + (warp >> 1), half = vec >= c.H, h = vec - half * c.H;
+    const int vec = blockIdx.y * kAppendVecs + warp / kAppendWarps, half = vec >= c.H, h = vec - half * c.H;
     const bool in = vec < 2 * c.H;
     const TIN *src = half ? v + h * vh : k + h * kh;
     const int64_t st = half ? vt : kt;
-    const int r0 = 16 * (warp & 1) + lane / LPR;                          // this lane's first slot
+    const int r0 = kKB / kAppendWarps * (warp % kAppendWarps) + lane / LPR;                          // this lane's first slot
     const int new0 = (int)max(p0 - s0, (int64_t)0), new1 = (int)min(len - s0, (int64_t)kKB);   // slots of new tokens
 
-    float x[IT][4];
+    Raw4<TIN> raw[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int r = r0 + i * RPW;
-        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
-        if (in && r >= new0 && r < new1) load4(src + (lo + s0 + r - p0) * st + 4 * quad, x[i]);
+        raw[i].w = {};
+        if (in && r >= new0 && r < new1) raw[i] = *reinterpret_cast<const Raw4<TIN> *>(src + (lo + s0 + r - p0) * st + 4 * quad);
     }
     const int page = c.table[(int64_t)b * c.max_pages + (s0 >> c.tshift)];
     if (page < 0 || page >= c.n_pages) {
@@ -91,19 +91,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvView c, KvR
     if (!(d_old >= 0.0f && d_old <= FLT_MAX)) d_old = 0.0f;
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int i = 0; i < IT; ++i) {
+        float x[4];
+        unpack4(raw[i], x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (x[i][e] != x[i][e]) x[i][e] = 0.0f;
-            const float a = fabsf(x[i][e]);
-            amax = fmaxf(amax, a <= FLT_MAX ? a : 0.0f);
-        }
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[e]) <= FLT_MAX ? fabsf(x[e]) : 0.0f);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (lane == 0) s_amax[warp] = amax;
     __syncthreads();
     if (!in) return;
-    float d = __fmul_rn(fmaxf(amax, s_amax[warp ^ 1]), 1.0f / 127.0f);
+    const float *others = s_amax + warp / kAppendWarps * kAppendWarps;
+    float d = __fmul_rn(fmaxf(fmaxf(others[0], others[1]), fmaxf(others[2], others[3])), 1.0f / 127.0f);
     if (d < FLT_MIN) d = 0.0f;
     d = fmaxf(d, d_old);
     const float id = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
@@ -111,13 +111,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvView c, KvR
     for (int i = 0; i < IT; ++i) {
         const int r = r0 + i * RPW;
         if (r >= new0 && r < new1) {
-            uint32_t w = 0;
+            float x[4];
+            unpack4(raw[i], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float q = d > 0.0f ? fminf(fmaxf(roundf(__fmul_rn(x[i][e], id)), -127.0f), 127.0f) : 0.0f;
-                w |= (uint32_t)(__float2int_rn(q) + 128) << (8 * e);
-            }
-            *reinterpret_cast<uint32_t *>(codes + r * D + 4 * quad) = w;
+            for (int e = 0; e < 4; ++e) x[e] = x[e] == x[e] ? __fmul_rn(x[e], id) : 0.0f;
+            *reinterpret_cast<uint32_t *>(codes + r * D + 4 * quad) = d > 0.0f ? pack_codes(x) : 0x80808080u;
         }
     }
     if (new0 > 0 && d > d_old) {                                          // earlier codes under a larger scale
@@ -128,17 +126,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvView c, KvR
             if (r < new0) {
                 uint32_t *dst = reinterpret_cast<uint32_t *>(codes + r * D + 4 * quad);
                 const uint32_t old = *dst;
-                uint32_t w = 0;
+                float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float q = roundf(__fmul_rn((float)(int)((old >> (8 * e)) & 255u) - 128.0f, shrink));
-                    w |= (uint32_t)(__float2int_rn(q) + 128) << (8 * e);
-                }
-                *dst = w;
+                for (int e = 0; e < 4; ++e) y[e] = __fmul_rn(code_value(old, e), shrink);
+                *dst = pack_codes(y);
             }
         }
     }
-    if ((warp & 1) == 0 && lane == 0) *scale = d;
+    if (warp % kAppendWarps == 0 && lane == 0) *scale = d;
 }
 
 constexpr int kReadTokens = 16, kReadThreads = 256;
@@ -206,7 +201,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows 
                 if (vec >= heads || dst == nullptr) continue;
                 float x[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = __fmul_rn((float)((int)((w[i] >> (8 * e)) & 255u) - 128), d[i]);
+                for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(code_value(w[i], e), d[i]);
                 store4(dst + (t0 + t) * (half ? vt : kt) + h * (half ? vh : kh) + 4 * quad, x);
             }
         }
