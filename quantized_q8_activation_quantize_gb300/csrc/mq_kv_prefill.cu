@@ -134,6 +134,13 @@ __device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint64_t *bar2, uint32
 __device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint64_t *bar2, uint32_t parity, unsigned int *err, volatile int *abort) {
     return warp_wait2(bar, bar2, parity, parity, err, abort);
 }
+__device__ __forceinline__ bool warp_wait3(uint64_t *bar, uint64_t *bar2, uint64_t *bar3, uint32_t parity, uint32_t parity2, uint32_t parity3,
+                                           unsigned int *err, volatile int *abort) {
+    const bool one = mbar_test_wait(smem_u32(bar), parity), two = mbar_test_wait(smem_u32(bar2), parity2);
+    const bool three = mbar_try_wait(smem_u32(bar3), parity3);
+    if (__all_sync(0xffffffffu, one && two && three)) return true;
+    return warp_wait(bar, parity, err, abort) && warp_wait(bar2, parity2, err, abort) && warp_wait(bar3, parity3, err, abort);
+}
 // one arrival for the warp, after what its lanes did
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -462,15 +469,31 @@ __device__ __forceinline__ float pf_max32(const uint32_t (&s)[32]) {
     return fmaxf(max3(y[0], y[1], y[2]), y[3]);
 }
 
-// The softmax reads a tile's scores twice from TMEM, 64 at a time: once for the maximum, once for the weights.  Holding all 128 in
-// registers left the compiler none to overlap the elements' chains with (3600 clocks a tile for f32 rows).
+// the largest of 32 consecutive columns of the lane's row, found by the load itself (the values are not used)
+__device__ __forceinline__ float pf_load_max32(uint32_t taddr) {
+    uint32_t s[32];
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]), "=r"(s[9]), "=r"(s[10]),
+          "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15]), "=r"(s[16]), "=r"(s[17]), "=r"(s[18]), "=r"(s[19]), "=r"(s[20]),
+          "=r"(s[21]), "=r"(s[22]), "=r"(s[23]), "=r"(s[24]), "=r"(s[25]), "=r"(s[26]), "=r"(s[27]), "=r"(s[28]), "=r"(s[29]), "=r"(s[30]),
+          "=r"(s[31]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+    return m;
+}
+// The softmax reads a tile's scores twice from TMEM: once for the maximum, once, 64 or 32 at a time, for the weights.  Holding all 128
+// in registers left the compiler none to overlap the elements' chains with (3600 clocks a tile for f32 rows).
 __device__ __forceinline__ float pf_tile_max(uint32_t ts, const float (&kb)[4]) {
     float mx = -INFINITY;
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-        uint32_t s[2][32];
-        pf_load_scores(ts + 64 * e, s);
-        mx = max3(mx, pf_max32(s[0]) * (e ? kb[2] : kb[0]), pf_max32(s[1]) * (e ? kb[3] : kb[1]));
+        const float m0 = pf_load_max32(ts + 64 * e), m1 = pf_load_max32(ts + 64 * e + 32);
+        tmem_ld_wait();
+        mx = max3(mx, m0 * (e ? kb[2] : kb[0]), m1 * (e ? kb[3] : kb[1]));
     }
     return mx;
 }
@@ -594,15 +617,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             }
             for (int j = 0; ok && j < nj; ++j) {
                 const bool more = j + 1 < nj;
-                const uint32_t sk = slot;
-                if (more) {
-                    if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
-                    next();
-                }
-                const uint32_t sv = slot;
-                if (!(ok = warp_wait(bar.op_full + slot, ph, err, abort_flag))) break;
+                const uint32_t sk = slot, pk = ph;
+                if (more) next();
+                const uint32_t sv = slot, pv = ph;
                 next();
-                if (!(ok = warp_wait(bar.p_full, j & 1, err, abort_flag))) break;
+                if (!(ok = warp_wait3(bar.op_full + sk, bar.op_full + sv, bar.p_full, pk, pv, j & 1, err, abort_flag))) break;
                 tc_fence_after();
                 mma.output(o0, s0, sv, j > 0);
                 mma_commit_warp(bar.o_done);
@@ -651,7 +670,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             uint64_t l2 = f2_pack(0.0f, 0.0f);
             bool ok = true;
             for (int j = 0; j < nj; ++j) {
-                if (!(ok = warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag))) break;
+                if (!(ok = warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag))) break;      // under the products
                 const PfInfo &o = info[j % kPfInfo];
                 const float4 dk = *reinterpret_cast<const float4 *>(o.dk);
                 const float gf = o.gf;
