@@ -55,11 +55,38 @@ struct KvRows {
     }
 };
 
+// pairs of f32 in one register pair: half the issue slots
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // four consecutive values of a row: as they are stored, and as f32
 template <typename T>
@@ -79,6 +106,20 @@ __device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16> &r, float *x) 
     x[0] = __uint_as_float(r.w.x << 16), x[1] = __uint_as_float(r.w.x & 0xffff0000u);
     x[2] = __uint_as_float(r.w.y << 16), x[3] = __uint_as_float(r.w.y & 0xffff0000u);
 }
+// the largest magnitude of four values into amax (NaN aside), and z, which becomes NaN where one of them is a NaN or an infinity
+__device__ __forceinline__ void scan4(const Raw4<float> &r, float &amax, uint64_t &z) {
+    amax = fmaxf(fmaxf(amax, fabsf(r.w.x)), fabsf(r.w.y));
+    amax = fmaxf(fmaxf(amax, fabsf(r.w.z)), fabsf(r.w.w));
+    z = f2_fma(f2_pack(r.w.x, r.w.y), f2_pack(0.0f, 0.0f), z);
+    z = f2_fma(f2_pack(r.w.z, r.w.w), f2_pack(0.0f, 0.0f), z);
+}
+template <typename T2>
+__device__ __forceinline__ void scan2(uint32_t w, T2 &amax, T2 &z) {
+    const uint32_t none = 0;
+    const T2 a = *reinterpret_cast<const T2 *>(&w);
+    amax = __hmax2(amax, __habs2(a));
+    z = __hfma2(a, *reinterpret_cast<const T2 *>(&none), z);
+}
 template <typename T>
 __device__ __forceinline__ void load4(const T *p, float *x) {
     unpack4(*reinterpret_cast<const Raw4<T> *>(p), x);
@@ -92,20 +133,34 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *x) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Codes and values without conversion instructions (they run at a quarter of the rate): a byte in the low mantissa bits of 2^23.
+// Codes and values without conversion instructions (they run at a quarter of the rate) and with few ALU ones (half the rate): a byte in
+// the low mantissa bits of 2^23.
 __device__ __forceinline__ float code_value(uint32_t w, int e) {
     return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + e)) - 8388736.0f;              // byte e, minus 128
 }
-// 128 + round half away from zero of y, |y| clamped to 127; in the low byte.  y + (0.5 - 2^-25), cut to an integer, is that
-// rounding: the sum reaches the next integer exactly from the half on.
-__device__ __forceinline__ uint32_t value_code(float y) {
-    const float n = __fadd_rz(__fadd_rn(fminf(fabsf(y), 127.0f), 0.49999997f), 8388608.0f);
-    const uint32_t s = (uint32_t)(__float_as_int(y) >> 31);
-    return (__float_as_uint(n) ^ s) - s + 128u;
+__device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ uint32_t pack_codes(const float (&y)[4]) {
-    const uint32_t a = __byte_perm(value_code(y[0]), value_code(y[1]), 0x0040), b = __byte_perm(value_code(y[2]), value_code(y[3]), 0x0040);
-    return __byte_perm(a, b, 0x5410);
+// 128 + round half away from zero of two values of at most 127.4, in the low byte of each.  With s the value's sign: y + s (0.5 - 2^-25)
+// cut to an integer is that rounding (the sum reaches the next integer exactly from the half on), and adding s 2^23 toward zero cuts.
+__device__ __forceinline__ void value_codes2(uint64_t y, uint32_t &a, uint32_t &b) {
+    float y0, y1;
+    f2_unpack(y, y0, y1);
+    const uint64_t s = f2_pack(__uint_as_float((__float_as_uint(y0) & 0x80000000u) | 0x3f800000u),
+                               __uint_as_float((__float_as_uint(y1) & 0x80000000u) | 0x3f800000u));
+    const uint64_t t = f2_fma(s, f2_pack(0.49999997f, 0.49999997f), y);
+    const uint64_t u = f2_fma_rz(s, f2_pack(8388608.0f, 8388608.0f), t);
+    const uint64_t n = f2_fma(s, f2_pack(-8388608.0f, -8388608.0f), u);
+    f2_unpack(f2_add(n, f2_pack(8388736.0f, 8388736.0f)), y0, y1);
+    a = __float_as_uint(y0), b = __float_as_uint(y1);
+}
+__device__ __forceinline__ uint32_t pack_codes(uint64_t y01, uint64_t y23) {
+    uint32_t a, b, c, d;
+    value_codes2(y01, a, b);
+    value_codes2(y23, c, d);
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 __device__ __forceinline__ void kv_error(unsigned int *err, unsigned int bit) { atomicOr(err, bit); }
