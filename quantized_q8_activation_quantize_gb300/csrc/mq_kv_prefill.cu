@@ -13,8 +13,8 @@
 // tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), the softmax of one tile under the products of the other.  A row's
 // reference maximum moves only when the maximum grows by more than kTau (a factor that cancels in o / l), and the V
 // scale reference g only when a scale exceeds it, to twice that, so O in TMEM is rescaled a few times per row
-// instead of at every tile.  V enters as f16(code * f16(256 dv / g)): its rounding is of the size of P's and it costs half a
-// multiplication per code and 256 rows, on P it cost as much per weight.
+// instead of at every tile.  (V as f16(code * f16(256 dv / g)) took the factor off the weights and 3% off the time, but its two
+// roundings showed in f16 outputs.)
 //
 // f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
 // The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
@@ -334,14 +334,12 @@ __device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8
     const int tmask = a.c.T - 1, tok0 = (int)((w.base + 32 * blk0) & tmask);
     uint2 raw[2][IT];
     const uint8_t *src[2];
-    float pv[2] = {0.0f, 0.0f}, pn[2];
     auto locate = [&](int j) -> bool {
         if (!warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort)) return false;
         const PfInfo &o = info[j % kPfInfo];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int page = o.page[blk0 + z];
-            pn[z] = o.pv[blk0 + z];
             src[z] = page >= 0 ? a.c.pool + page * a.c.page_bytes + in0 + ((tok0 + (4 * j + z) * kKB) & tmask) * D : nullptr;
         }
         warp_arrive(bar.info_empty + j % kPfInfo, lane);
@@ -354,7 +352,6 @@ __device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8
 #pragma unroll
         for (int k = 0; k < IT; ++k) raw[z][k] = load(z, k);
     for (int j = 0; j < w.nj; ++j) {
-        pv[0] = pn[0], pv[1] = pn[1];
         const bool more = j + 1 < w.nj;
         if (more) {
             if (!locate(j + 1)) break;
@@ -363,17 +360,11 @@ __device__ __forceinline__ void pf_widen(const PfArgs &a, const PfTile &w, uint8
         if (n >= SLOTS && !warp_wait(bar.op_empty + slot, (n / SLOTS - 1) & 1, err, abort)) break;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            const __half2 f = __float2half2_rn(256.0f * pv[z]);
 #pragma unroll
             for (int k = 0; k < IT; ++k) {
                 uint4 x;
                 codes_f16(raw[z][k].x, x.x, x.y);
                 codes_f16(raw[z][k].y, x.z, x.w);
-                if (!TWO && half) {
-                    __half2 *h = reinterpret_cast<__half2 *>(&x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
-                }
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(off[k % NV] + slot * OPT + z * 4096 + (k / NV) * 1024), "r"(x.x),
                              "r"(x.y), "r"(x.z), "r"(x.w)
                              : "memory");
@@ -510,8 +501,8 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&s)[32], float kb, ui
         x = exp2_approx(x), y = exp2_approx(y);
         const uint64_t p = f2_pack(x, y);
         acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1], p);
+        f2_unpack(f2_mul(p, pp), x, y);
         if constexpr (TWO) {
-            f2_unpack(f2_mul(p, pp), x, y);
             w[k >> 1] = pack_f16(x, y);
             const float2 z = unpack_f16(w[k >> 1]);
             f2_unpack(f2_fma(f2_pack(z.x, z.y), f2_pack(-1.0f, -1.0f), f2_pack(x, y)), x, y);
@@ -523,7 +514,7 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&s)[32], float kb, ui
     l2 = f2_add(l2, f2_add(acc[0], acc[1]));
 }
 // the weights of the tile, written over the scores that have been read.  16-bit rows: 32 columns per 64 scores, from the front
-__device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4], float off, uint64_t &l2) {
+__device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4], const float (&pb)[4], float off, uint64_t &l2) {
     const uint64_t off2 = f2_pack(off, off);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
@@ -531,7 +522,7 @@ __device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4
         pf_load_scores(ts + 64 * e, s);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            pf_weights<false>(s[z], e ? kb[2 + z] : kb[z], off2, 1.0f, l2, w, v);
+            pf_weights<false>(s[z], e ? kb[2 + z] : kb[z], off2, e ? pb[2 + z] : pb[z], l2, w, v);
             tmem_st16(ts + 32 * e + 16 * z, w);
         }
     }
@@ -672,8 +663,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             for (int j = 0; j < nj; ++j) {
                 if (!(ok = warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag))) break;      // under the products
                 const PfInfo &o = info[j % kPfInfo];
-                const float4 dk = *reinterpret_cast<const float4 *>(o.dk);
-                const float gf = o.gf;
+                const float4 dk = *reinterpret_cast<const float4 *>(o.dk), pv = *reinterpret_cast<const float4 *>(o.pv);
+                const float gf = o.gf, pb[4] = {pv.x, pv.y, pv.z, pv.w};
                 // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
                 const float kb[4] = {fmaxf(rs * dk.x, 0x1p-120f), fmaxf(rs * dk.y, 0x1p-120f), fmaxf(rs * dk.z, 0x1p-120f), fmaxf(rs * dk.w, 0x1p-120f)};
                 warp_arrive(bar.info_empty + j % kPfInfo, lane);
@@ -707,7 +698,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                         }
                     }
                 }
-                pf_tile_weights(ts, kb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
+                pf_tile_weights(ts, kb, pb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(bar.p_full + t, lane);
@@ -718,7 +709,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             float l, l1;
             f2_unpack(l2, l, l1);
             l += l1;
-            const float inv = l == 0.0f ? 0.0f : info[(nj + kPfInfo - 1) % kPfInfo].g * (1.0f / 256.0f) / l;
+            const float inv = l == 0.0f ? 0.0f : info[(nj + kPfInfo - 1) % kPfInfo].g / l;
             const int64_t i = (w.r0 + r) / a.group;
             const int gq = (int)(w.r0 + r - i * a.group);
             T *dst = static_cast<T *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh;
