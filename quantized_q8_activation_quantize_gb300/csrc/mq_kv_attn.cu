@@ -64,11 +64,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int at_ctas_per_sm(int D, int MT) { return D == 64 && MT == 1 ? 3 : 2; }
+
 // MT: 16-row MMA tiles that share the codes
 template <typename T, int D, int MT>
 struct AtCfg {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int RT = TWO ? 8 : 16, R = RT * MT;      // rows of an MMA tile, of a pass
+    // CTAs per SM: as many as the registers leave room for without spills (three with them took 76 us where two take 49)
+    static constexpr int CPS = at_ctas_per_sm(D, MT);
     static constexpr int RING = MT == 1 || D == 64 ? 3 : 2;   // blocks in flight per warp
     static constexpr int BLK = kKB * D, SLOT = 2 * BLK;       // bytes of one 32-token block of K or V
     static constexpr bool QS = MT > 1 && D == 128;            // q fragments in shared memory: the registers hold 2 x 64 sums
@@ -169,7 +173,7 @@ __device__ __forceinline__ int at_find(const uint2 *prefix, int n_seqs, uint32_t
 // in the share whole, else as a partial for the join kernel.  (Shares of whole CTAs, their warps joined in shared memory at the end of
 // each pass, left fewer partials but made every end of a pass cost 5 us: 77 us against 49 for a ragged batch of 48 sequences.)
 template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_constant__ CUtensorMap tm, AtArgs a, unsigned int *err) {
+__global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_kernel(const __grid_constant__ CUtensorMap tm, AtArgs a, unsigned int *err) {
     using C = AtCfg<T, D, MT>;
     constexpr bool TWO = C::TWO;
     constexpr int NT = D / 8, KS = D / 16, RING = C::RING;    // n-tiles of the output, k-steps of the scores
@@ -269,8 +273,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
     int h = 0, nrow = 0, r0 = 0;                              // first row
     int64_t tok = 0;                                          // token row of row 0's token
     uint32_t last = 0;                                        // the pass's last place
-    int64_t all_lo = 0, all_hi = 0;                           // what every row of the pass sees
-    int64_t v_lo[MT][RT], v_hi[MT][RT];
+    int all_lo = 0, all_hi = 0;                               // what every row of the pass sees
+    int v_lo[MT][RT], v_hi[MT][RT];
     uint32_t qa[C::QS ? 1 : MT][KS][4];
     uint32_t *qs = reinterpret_cast<uint32_t *>(sm + C::OFF_Q) + warp * MT * KS * 128 + lane * 4;
     float rs[MT][RT], m[MT][RT], l[MT][RT];
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
         int64_t x0, y0, x1, y1;
         row_range(q.first + r0 / G, q.len, a.causal, a.window, x0, y0);
         row_range(q.first + (r0 + nrow - 1) / G, q.len, a.causal, a.window, x1, y1);
-        all_lo = x1, all_hi = y0 > x0 ? y0 : 0;
+        all_lo = (int)x1, all_hi = y0 > x0 ? (int)y0 : 0;
         gmax = 0.0f;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -307,7 +311,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
                 float x[D / 4];
                 if (rr < nrow) {
                     const int i = (r0 + rr) / G;
-                    row_range(q.first + i, q.len, a.causal, a.window, v_lo[t][e], v_hi[t][e]);
+                    row_range(q.first + i, q.len, a.causal, a.window, x0, y0);
+                    v_lo[t][e] = (int)x0, v_hi[t][e] = (int)y0;
                     const T *p = static_cast<const T *>(a.q) + (tok + i) * a.qt + (int64_t)(h * G + (r0 + rr - i * G)) * a.qh + cc * (D / 4);
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) load4(p + 4 * j, x + 4 * j);
@@ -430,8 +435,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
             }
         }
         const float dkb = __shfl_sync(0xffffffffu, dk0, li), dvb = __shfl_sync(0xffffffffu, dv0, li);
-        const int64_t t0 = (int64_t)(blk + (k - k0)) * kKB;
-        const bool inner = t0 >= all_lo && t0 + kKB <= all_hi;
+        const int t0 = (int)(blk + (k - k0)) * kKB;
+        const bool inner = t0 >= all_lo && t0 <= all_hi - kKB;
         // the V scale reference moves to twice a scale that exceeds it
         float gold = 1.0f;
         if (dvb > gmax) {
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) kv_attn_kernel(const __grid_con
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const int64_t pos = t0 + 8 * t + 2 * cc + z;
+                            const int pos = t0 + 8 * t + 2 * cc + z;
                             if (pos < v_lo[x][e] || pos >= v_hi[x][e]) s[x][t][2 * e + z] = -INFINITY;
                         }
                 }
@@ -693,10 +698,10 @@ bool use_tiles(int64_t rows) { return rows > 64; }
 // MMA tiles per pass: two where the rows do not fit one
 int pass_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
 int pass_rows(int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(dtype, rows); }
-// CTAs: two per SM, or as many as there are units for their warps at most
-int64_t share_ctas(int32_t n_seqs, int32_t H, int dtype, int64_t rows, int64_t max_kv) {
+// CTAs: as many as are resident, or as there are units for their warps at most
+int64_t share_ctas(int32_t n_seqs, int32_t H, int D, int dtype, int64_t rows, int64_t max_kv) {
     const int64_t passes = (rows + pass_rows(dtype, rows) - 1) / pass_rows(dtype, rows), blocks = (max_kv + kKB - 1) / kKB;
-    const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = 2 * sm_count();
+    const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = at_ctas_per_sm(D, pass_tiles(dtype, rows)) * sm_count();
     return (units + kAtWarps - 1) / kAtWarps < most ? (units + kAtWarps - 1) / kAtWarps : most;
 }
 size_t plan_bytes(int32_t n_seqs, size_t workers) { return (256 + (((size_t)n_seqs + 4) & ~size_t(3)) * 8 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
@@ -733,7 +738,7 @@ size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t 
                        int64_t max_kv) {
     const int64_t rows = max_q * (n_q_heads / H);
     if (use_tiles(rows)) return 256;
-    const size_t workers = (size_t)share_ctas(n_seqs, H, dtype, rows, max_kv) * kAtWarps;
+    const size_t workers = (size_t)share_ctas(n_seqs, H, D, dtype, rows, max_kv) * kAtWarps;
     return plan_bytes(n_seqs, workers) + workers * 2 * pass_rows(dtype, rows) * (D + 4) * 4;
 }
 
@@ -747,7 +752,7 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
     AtArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
     a.group = p.group, a.causal = p.causal, a.layer = layer, a.max_q = (int32_t)p.max_q, a.window = p.window;
-    const int64_t ctas = share_ctas(c.n_seqs, c.H, p.dtype, rows, p.max_kv);
+    const int64_t ctas = share_ctas(c.n_seqs, c.H, c.D, p.dtype, rows, p.max_kv);
     a.workers = (int)ctas * kAtWarps;
     a.c_log2 = fabsf(p.scale) * kLog2e;
     a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
