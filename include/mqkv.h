@@ -56,7 +56,7 @@ typedef struct {
 typedef struct {
     int32_t *page_table;    /* [n_seqs][max_pages]; entries past a sequence's last page are not read */
     int32_t *kv_len;        /* [n_seqs] */
-    int32_t n_seqs;
+    int32_t n_seqs;         /* below 2^24 */
     int32_t max_pages;
 } mqkv_seqs;
 

@@ -48,6 +48,7 @@ int check_seqs(const char *fn, const mqkv_seqs *s) {
     if (s == nullptr) return set_error(MQ_ERR_ARG, "%s: NULL sequences", fn);
     if (s->n_seqs < 0 || s->max_pages < 0)
         return set_error(MQ_ERR_ARG, "%s: negative n_seqs=%d or max_pages=%d", fn, s->n_seqs, s->max_pages);
+    if (s->n_seqs >= 1 << 24) return set_error(MQ_ERR_SHAPE, "%s: n_seqs=%d must be below 2^24", fn, s->n_seqs);
     if (s->n_seqs == 0) return MQ_OK;
     if (s->max_pages == 0) return set_error(MQ_ERR_SHAPE, "%s: max_pages=0", fn);
     if (s->page_table == nullptr || s->kv_len == nullptr)

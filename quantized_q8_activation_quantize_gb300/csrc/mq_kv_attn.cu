@@ -35,7 +35,6 @@ struct AtArgs {
     int32_t max_q;
     int64_t window;
     float c_log2, sign;         // |scale| * log2(e), the sign of scale (it goes into q: score factors are not negative)
-    uint32_t *total;            // units of the call, for the join
     uint32_t *prefix;           // [n_seqs + 1][2]: places and units before each sequence
     struct AtJoin *join;        // [workers]
     float *part;                // [worker][2][R rows][D + 4]: o, m, l
@@ -110,8 +109,8 @@ struct AtSeq {
     __device__ __forceinline__ uint2 size(int H) const { return make_uint2((uint32_t)(tiles * H) * (nb + kAtExtra), (uint32_t)(tiles * H) * nb); }
 };
 
-// places and units before each sequence into prefix[0 .. n_seqs], by one CTA of THREADS threads.  (Their sums stay below 2^32: the host
-// has checked it for max_kv, and a table row holds no more tokens than its pages.)
+// places and units before each sequence into prefix[0 .. n_seqs], by one CTA of THREADS threads.  (Their sums stay below 2^32: the
+// host has checked it for whole table rows.)
 template <int THREADS>
 __device__ __forceinline__ void at_plan(const AtArgs &a, int R, uint2 *prefix, uint2 *s_warp, unsigned int *err, bool tell) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -153,7 +152,6 @@ __global__ void __launch_bounds__(1024) kv_attn_plan_kernel(AtArgs a, int R, uns
     grid_dep_wait();
     uint2 *prefix = reinterpret_cast<uint2 *>(a.prefix);
     at_plan<1024>(a, R, prefix, s_warp, err, true);
-    if (threadIdx.x == 0) *a.total = prefix[a.c.n_seqs].x;
 }
 
 // the last sequence that begins at or before unit u (one with units)
@@ -195,9 +193,6 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         uint2 *mine = reinterpret_cast<uint2 *>(sm + C::OFF_PLAN);
         at_plan<kAtThreads>(a, C::R, mine, reinterpret_cast<uint2 *>(sm + C::OFF_BAR + kAtWarps * RING * 8), err, blockIdx.x == 0);
         prefix = mine;
-        if (blockIdx.x == 0) {                                // for the join
-            if (threadIdx.x == 0) *a.total = mine[a.c.n_seqs].x;
-        }
     }
     __syncthreads();
     const uint32_t total = prefix[a.c.n_seqs].x, workers = min((uint32_t)a.workers, total), worker = blockIdx.x * kAtWarps + warp;
@@ -704,7 +699,7 @@ int64_t share_ctas(int32_t n_seqs, int32_t H, int D, int dtype, int64_t rows, in
     const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = at_ctas_per_sm(D, pass_tiles(dtype, rows)) * sm_count();
     return (units + kAtWarps - 1) / kAtWarps < most ? (units + kAtWarps - 1) / kAtWarps : most;
 }
-size_t plan_bytes(int32_t n_seqs, size_t workers) { return (256 + (((size_t)n_seqs + 4) & ~size_t(3)) * 8 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
+size_t plan_bytes(int32_t n_seqs, size_t workers) { return ((((size_t)n_seqs + 4) & ~size_t(3)) * 8 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
 
 template <typename T, int D, int MT>
 int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t ctas, unsigned int *err, cudaStream_t s) {
@@ -746,6 +741,9 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
                         const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
     const int64_t rows = p.max_q * p.group;
     if (use_tiles(rows)) return kv_launch_prefill(c, r, p, err, s);
+    const int64_t passes = (rows + pass_rows(p.dtype, rows) - 1) / pass_rows(p.dtype, rows);
+    if ((double)c.n_seqs * c.H * passes * ((double)c.max_pages * (c.T / kKB) + kAtExtra + 1) >= 4294967296.0)
+        return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences of up to %d pages have too many blocks for one call", c.n_seqs, c.max_pages);
     CUtensorMap tm;
     int rc = kv_tensor_map(&tm, cache, lay);
     if (rc != MQ_OK) return rc;
@@ -756,8 +754,7 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
     a.workers = (int)ctas * kAtWarps;
     a.c_log2 = fabsf(p.scale) * kLog2e;
     a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
-    a.total = static_cast<uint32_t *>(ws);
-    a.prefix = a.total + 64;
+    a.prefix = static_cast<uint32_t *>(ws);
     a.join = reinterpret_cast<AtJoin *>(a.prefix + 2 * ((c.n_seqs + 4) & ~3));
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes(c.n_seqs, (size_t)a.workers));
     const int tiles = pass_tiles(p.dtype, rows);

@@ -905,6 +905,8 @@ int prefill_t(PfArgs &a, unsigned int *err, cudaStream_t s) {
     if (rc != MQ_OK) return rc;
     a.tiles = (int)((a.max_q * a.group + C::ROWS - 1) / C::ROWS);
     const int64_t grid = (int64_t)a.c.H * a.c.n_seqs * a.tiles;
+    if (grid > INT_MAX)
+        return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences x %d KV heads x %d row tiles exceed the grid", a.c.n_seqs, a.c.H, a.tiles);
     return cuda_error(launch_pdl(fn, dim3((unsigned)grid), dim3(kPfThreads), C::SMEM, s, a, err), "mqkv_attention (tiles) launch");
 }
 

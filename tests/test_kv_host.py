@@ -58,7 +58,7 @@ def seqs(**kw):
 BAD_CACHES = [(dict(pool=None), B.MQ_ERR_ARG), (dict(pool=POOL + 128), B.MQ_ERR_ALIGN), (dict(n_pages=0), B.MQ_ERR_SHAPE),
               (dict(n_pages=1 << 31), B.MQ_ERR_SHAPE), (dict(head_dim=96), B.MQ_ERR_SHAPE), (dict(page_tokens=48), B.MQ_ERR_SHAPE),
               (dict(n_layers=0), B.MQ_ERR_SHAPE), (dict(refs=REFS + 2), B.MQ_ERR_ALIGN)]
-BAD_SEQS = [(dict(page_table=None), B.MQ_ERR_ARG), (dict(kv_len=None), B.MQ_ERR_ARG), (dict(n_seqs=-1), B.MQ_ERR_ARG),
+BAD_SEQS = [(dict(page_table=None), B.MQ_ERR_ARG), (dict(kv_len=None), B.MQ_ERR_ARG), (dict(n_seqs=-1), B.MQ_ERR_ARG), (dict(n_seqs=1 << 24), B.MQ_ERR_SHAPE),
             (dict(max_pages=0), B.MQ_ERR_SHAPE), (dict(max_pages=-2), B.MQ_ERR_ARG), (dict(page_table=TABLE + 1), B.MQ_ERR_ALIGN)]
 
 
