@@ -279,6 +279,18 @@ def test_prefill(dtype, heads, kv_heads, dim, page):
     check_attention(s, new, heads, dtype, window=100, seed=2)
 
 
+@pytest.mark.parametrize("n,dtype", [(257, "f32"), (1500, "f16")])
+def test_many_sequences(n, dtype):
+    # more than the plan's shared memory holds, and more than one round of its scan; most of them short, some empty
+    r = np.random.default_rng(n)
+    lens = [int(x) for x in r.choice([0, 1, 3, 17, 33, 70], n)]
+    lens[5] = 900
+    s = Setup(lens, 1, 64, 32, layers=1, seed=n)
+    check_attention(s, [1] * n, 2, dtype, layer=0)
+    new = [int(x) for x in r.integers(0, 3, n)]
+    check_attention(s, new, 2, dtype, layer=0)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_long_and_peaked(dtype):
     # long enough to be split many ways; scores far apart, so that one token carries a row
@@ -557,3 +569,18 @@ def test_steps_in_a_captured_graph():
                 want, mass, vmax = U.attention(x[2][b:b + 1].astype(np.float64), kk, vv, i + 1)
                 assert (np.abs(got[b:b + 1] - want) <= U.attention_tolerance(want, mass, vmax, i + 1, "f32")).all()
     status()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,prompt", [(4, 2, 64, 70), (14, 2, 128, 200)])
+def test_example_runs_the_operators_together(heads, kv_heads, dim, prompt):
+    from examples import kv_decode
+    tokens = 6
+    got = kv_decode.run(layers=2, hidden=512, heads=heads, kv_heads=kv_heads, dim=dim, prompt=prompt, tokens=tokens, page=32,
+                        say=lambda *a: None)
+    # `tokens` decode steps alone, one as three, one more of the first; the second has ended
+    assert got["len"] == [prompt + tokens + 2, 0, prompt + tokens + 1]
+    # attention's f32 rounding may move a Q8 code of the o projection's input by one: 1 / 127 of a block's largest value, of which a
+    # state sums `heads * dim` with random signs
+    assert got["spread"] < 2e-2
+    assert got["same_after_compact"] and np.isfinite(got["state"].cpu().numpy()).all()
+    assert got["shared"] == (prompt + tokens) // 32
