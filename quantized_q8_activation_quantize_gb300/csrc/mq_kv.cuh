@@ -176,7 +176,7 @@ struct KvAttn {
     void *out;
     int64_t qt, qh, ot, oh;
     int32_t n_q_heads, group, dtype, causal;
-    int64_t max_q, max_kv, window;
+    int64_t n_tokens, max_q, max_kv, window;
     float scale;
 };
 int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int layer, const KvView &c, const KvRows &r,

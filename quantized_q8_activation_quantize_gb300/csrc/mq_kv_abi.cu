@@ -267,7 +267,7 @@ int mqkv_attention(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer
     unsigned int *err = nullptr;
     KV_TRY(kv_state(&err));
     const KvAttn a{q, out, q_token_stride, q_head_stride, out_token_stride, out_head_stride, n_q_heads, n_q_heads / cache->n_kv_heads,
-                   dtype, causal != 0, max_q, max_kv, window, scale};
+                   dtype, causal != 0, n_tokens, max_q, max_kv, window, scale};
     return kv_launch_attention(*cache, lay, layer, view_of(*cache, *seqs, lay, layer), rows_of(cu, n_tokens, seqs->n_seqs), a, workspace,
                                err, reinterpret_cast<cudaStream_t>(stream));
 }

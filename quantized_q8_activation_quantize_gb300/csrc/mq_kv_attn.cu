@@ -22,7 +22,9 @@ namespace mq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
-constexpr uint32_t kAtExtra = 3;               // what the beginning and end of a row pass cost, in blocks
+// what the beginning and end of a row pass cost, in blocks: 0 took 56.5 us for 48 ragged sequences (47 for 24 windows of 20 rows), 2 50.4
+// (43.7), 4 50.2 (45.6), 8 49.0 (45.9)
+constexpr uint32_t kAtExtra = 3;
 constexpr int kAtSmemSeqs = 256;                // sequences whose plan fits the CTA's shared memory beside two CTAs' rings
 
 struct AtArgs {
@@ -63,6 +65,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// CTAs per SM: as many as the registers leave room for without spills (three with them took 76 us where two take 49)
 constexpr int at_ctas_per_sm(int D, int MT) { return D == 64 && MT == 1 ? 3 : 2; }
 
 // MT: 16-row MMA tiles that share the codes
@@ -70,8 +73,6 @@ template <typename T, int D, int MT>
 struct AtCfg {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int RT = TWO ? 8 : 16, R = RT * MT;      // rows of an MMA tile, of a pass
-    // CTAs per SM: as many as the registers leave room for without spills (three with them took 76 us where two take 49)
-    static constexpr int CPS = at_ctas_per_sm(D, MT);
     static constexpr int RING = MT == 1 || D == 64 ? 3 : 2;   // blocks in flight per warp
     static constexpr int BLK = kKB * D, SLOT = 2 * BLK;       // bytes of one 32-token block of K or V
     static constexpr bool QS = MT > 1 && D == 128;            // q fragments in shared memory: the registers hold 2 x 64 sums
@@ -688,11 +689,16 @@ int kv_tensor_map(CUtensorMap *tm, const mqkv_cache &c, const mqkv_layout &lay) 
     return MQ_OK;
 }
 
-// rows per KV head from which the tcgen05 tiles of mq_kv_prefill.cu are taken
-bool use_tiles(int64_t rows) { return rows > 64; }
-// MMA tiles per pass: two where the rows do not fit one
+// MMA tiles per pass: two where the rows do not fit one, so that the codes are widened once for both.  (Two for up to 8 f32 or 16 16-bit
+// rows, half of them empty: 38 us for 29, and 39 for 29, for 7 rows on 48 sequences of 2048 tokens; one, the codes read twice, for 14 f32
+// rows on 4 sequences of 32768: 49 for 47, for 28 16-bit rows 54 for 54 there and 46 for 48 on the 48.)
 int pass_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
 int pass_rows(int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(dtype, rows); }
+// More than two such passes over the cache (32 f32 rows per KV head, 64 16-bit ones): the tcgen05 tiles of mq_kv_prefill.cu.  Passes / tiles in
+// us, D = 128, 4 KV heads: f32, 28 rows 73/72, 42 rows 102/73, 56 rows 129/74 on 4 sequences of 32768 tokens; 63/64, 84/66, 105/67 on 48 of
+// 2048; 194/259, 283/259, 368/260 on 48 of 100 to 16384 (the passes share work evenly, row tiles are as long as their sequence).
+// bf16, 56 rows 81/60, 72/55, 206/205; 84 rows 110/60, 95/57, 300/205.
+bool use_tiles(int dtype, int64_t rows) { return rows > 2 * pass_rows(dtype, rows); }
 // CTAs: as many as are resident, or as there are units for their warps at most
 int64_t share_ctas(int32_t n_seqs, int32_t H, int D, int dtype, int64_t rows, int64_t max_kv) {
     const int64_t passes = (rows + pass_rows(dtype, rows) - 1) / pass_rows(dtype, rows), blocks = (max_kv + kKB - 1) / kKB;
@@ -714,7 +720,8 @@ int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t ctas, unsigned int *e
     rc = cuda_error(launch_pdl(kv_attn_kernel<T, D, MT>, dim3((unsigned)ctas), dim3(kAtThreads), smem, s, tm, a, err), "mqkv_attention launch");
     if (rc != MQ_OK) return rc;
     const unsigned rows = (unsigned)(a.max_q * a.group < C::R ? a.max_q * a.group : C::R);
-    // many partials to a pass: from 16 on
+    // Many partials to a pass, from 16 workers a pass on: 14.8 us with them, 34 without, for one sequence of 4096 tokens (128 workers a pass),
+    // 17.6 and 24 for 8 (38); 30.6 and 29.0 for 48 of 2048 (6).
     if (a.workers >= 16 * (int64_t)a.c.n_seqs * a.c.H)
         return cuda_error(launch_pdl(kv_attn_join_kernel<T, D, false>, dim3((unsigned)(a.workers + 7) / 8, rows), dim3(256), 0, s, a, (int)C::R),
                           "mqkv_attention join launch");
@@ -732,7 +739,7 @@ int attn_d(const CUtensorMap &tm, const AtArgs &a, int tiles, int64_t ctas, unsi
 size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t n_q_heads, int64_t n_tokens, int64_t max_q,
                        int64_t max_kv) {
     const int64_t rows = max_q * (n_q_heads / H);
-    if (use_tiles(rows)) return 256;
+    if (use_tiles(dtype, rows)) return kv_prefill_ws(n_seqs, H, D, dtype, n_q_heads / H, n_tokens, max_q);
     const size_t workers = (size_t)share_ctas(n_seqs, H, D, dtype, rows, max_kv) * kAtWarps;
     return plan_bytes(n_seqs, workers) + workers * 2 * pass_rows(dtype, rows) * (D + 4) * 4;
 }
@@ -740,7 +747,7 @@ size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t 
 int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int layer, const KvView &c, const KvRows &r,
                         const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
     const int64_t rows = p.max_q * p.group;
-    if (use_tiles(rows)) return kv_launch_prefill(c, r, p, err, s);
+    if (use_tiles(p.dtype, rows)) return kv_launch_prefill(c, r, p, ws, err, s);
     const int64_t passes = (rows + pass_rows(p.dtype, rows) - 1) / pass_rows(p.dtype, rows);
     if ((double)c.n_seqs * c.H * passes * ((double)c.max_pages * (c.T / kKB) + kAtExtra + 1) >= 4294967296.0)
         return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences of up to %d pages have too many blocks for one call", c.n_seqs, c.max_pages);

@@ -8,7 +8,8 @@
 namespace mq {
 
 // the tiled kernel for many rows (mq_kv_prefill.cu)
-int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err, cudaStream_t s);
+int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s);
+size_t kv_prefill_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int group, int64_t n_tokens, int64_t max_q);
 
 constexpr float kLog2e = 1.44269504088896341f;
 // the softmax weights enter the tensor cores as exp2(s - m + kPShift) times the V scale over the running largest V

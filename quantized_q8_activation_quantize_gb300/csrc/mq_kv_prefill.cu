@@ -16,10 +16,17 @@
 // instead of at every tile.  (V as f16(code * f16(256 dv / g)) took the factor off the weights and 3% off the time, but its two
 // roundings showed in f16 outputs.)
 //
+// Many rows of long sequences are 636 jobs of 40 to 64 tiles in the largest case measured: 436 us, 1056 TFLOP/s (of 1864 that cuBLAS
+// reaches); what is left is the chain MMA - commit - softmax - arrival - MMA of each tile and a CTA's beginning and end (8 tiles' time).
+//
 // f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
 // The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
 // each tile's P V goes to a fresh accumulator and is added to the row's sum in registers, rounding to nearest, under the
-// products of the next tiles: one row tile per CTA, S and O double-buffered, warps 0-3 and 4-7 the softmax of the tiles in turn.
+// products of the next tiles: one row tile per CTA, S and O double-buffered, warps 0-3 and 4-7 the softmax of the tiles in turn.  A prompt
+// of 3314 tokens, 28 query heads on 4 of 128: 179 us (157 GFLOP in two parts: 880 TFLOP/s); the softmax's issue slots bound it.
+//
+// q is staged by the softmax warps while the others look up and widen the first tiles: with all warps and before everything else, a CTA's
+// beginning took 5 us more (the prompt 187 us, the 16-bit chunks 478).
 #include <cuda.h>
 
 #include <climits>
@@ -34,6 +41,8 @@ constexpr int kPfThreads = 512;
 constexpr int kPfN = 128;                      // tokens of a tile
 constexpr int kPfSlots = 5;                    // f16 operand tiles in flight at most
 constexpr int kPfInfo = 4;                     // tiles that the lookup runs ahead
+// What a wave of pieces costs beside its tiles, the join, and each piece for the join, in tiles of 128 tokens (0.9 to 1.5 us each)
+constexpr double kPfPieceSteps = 8, kPfJoinSteps = 4, kPfPartSteps = 0.5;
 
 struct PfArgs {
     KvView c;
@@ -42,6 +51,8 @@ struct PfArgs {
     void *out;
     int64_t qt, qh, ot, oh;
     int32_t group, causal, tiles;
+    int32_t cut, pieces;        // the last `cut` row tiles (in the grid's order) are done in `pieces` pieces
+    float *part;                // [piece][row][D + 4]: o, m, l
     int64_t max_q, window;
     float c_log2;               // |scale| * log2(e)
     float sign;                 // of scale: folded into q, so that the score factors are not negative
@@ -66,7 +77,7 @@ struct PfCfg {
     static constexpr int OFF_RS = OFF_OP + SLOTS * OPT;     // row scales [ROWS]; f32 rows: then factors and maxima [4][128]
     static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 2 * 512 * 4 : 0);
     static constexpr int OFF_BAR = OFF_INFO + kPfInfo * (int)sizeof(PfInfo);
-    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 2;
+    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 3;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1008;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA exceeds the per-CTA limit");
@@ -148,11 +159,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 }
 
 struct PfBars {
-    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full;
+    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full, *q_full;
     __device__ __forceinline__ explicit PfBars(uint64_t *b) {
         op_full = b, op_empty = op_full + kPfSlots, info_full = op_empty + kPfSlots, info_empty = info_full + kPfInfo;
         s_full = info_empty + kPfInfo, p_full = s_full + 2, o_done = p_full + 2, o_free = o_done + 2, m_full = o_free + 2, drain = m_full + 2;
-        l_full = drain + 1;
+        l_full = drain + 1, q_full = l_full + 1;
     }
     // info_readers: warps that read a tile's lookup
     __device__ __forceinline__ void init(int info_readers) {
@@ -161,105 +172,171 @@ struct PfBars {
         for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 4), mbar_init(o_done + i, 1), mbar_init(o_free + i, 8), mbar_init(m_full + i, 4);
         mbar_init(drain, 1);
         mbar_init(l_full, 8);
+        mbar_init(q_full, 8);
         mbar_init_fence();
     }
 };
 
+// how a row tile of nj tiles of tokens is cut: `each` per piece, the last ones may have nothing
+__device__ __forceinline__ int pf_each(int nj, int pieces) { return (nj + pieces - 1) / pieces; }
+
 // the rows of a CTA and what they see; false if there are none
 struct PfTile {
-    int64_t lo, first, len, r0;      // row 0's token row, its position; the sequence's tokens; the first row
+    int64_t lo, first, len;          // the sequence's first new token: its row, its position; the sequence's tokens
+    int i0, g0;                      // row 0's new token and the head in the group
     int64_t base, b_lo, b_hi;        // first tile's first token; blocks that are read
     int64_t all_lo, all_hi;          // positions that every row sees
     int b, h, nrow, nj;
+    int slot;                        // of the piece's partial; -1: the rows are done here
     bool bad;
-    __device__ __forceinline__ bool init(const PfArgs &a, int per, unsigned int *err) {
-        // KV head fastest, then the sequence, the latest (longest) row tiles first
-        int64_t u = blockIdx.x;
-        h = (int)(u % a.c.H);
-        u /= a.c.H;
-        b = (int)(u % a.c.n_seqs);
-        const int tile = a.tiles - 1 - (int)(u / a.c.n_seqs);
+    __device__ __forceinline__ int token(int r, int G) const { return i0 + (int)((uint32_t)(g0 + r) / (uint32_t)G); }
+    __device__ __forceinline__ int head(int r, int G) const { return h * G + (int)((uint32_t)(g0 + r) % (uint32_t)G); }
+    // the row tile `job`, or piece `piece` of it: KV head fastest, then the sequence, the latest (longest) row tiles first
+    __device__ __forceinline__ bool init(const PfArgs &a, int per, uint32_t job, int piece, unsigned int *err) {
+        const uint32_t of = job / a.c.H, up = of / a.c.n_seqs;
+        h = (int)(job - of * a.c.H), b = (int)(of - up * a.c.n_seqs);
+        const int tile = a.tiles - 1 - (int)up;
         int64_t hi;
         a.r.of(b, lo, hi);
         int64_t n = hi - lo;
         if (n > a.max_q) {
-            if (threadIdx.x == 0) kv_error(err, KV_ERR_ROWS);
+            if (threadIdx.x == 0 && err != nullptr) kv_error(err, KV_ERR_ROWS);
             n = a.max_q;
         }
         len = a.c.len[b], first = len - (hi - lo);
         const int G = a.group;
         const int64_t rows = n * G;
-        r0 = (int64_t)tile * per;
+        const int64_t r0 = (int64_t)tile * per;
         if (r0 >= rows) return false;
+        i0 = (int)(r0 / G), g0 = (int)(r0 - (int64_t)i0 * G);
         bad = len < 0 || (len > 0 && ((len - 1) >> a.c.tshift) >= a.c.max_pages);
-        if (bad && threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
+        if (bad && threadIdx.x == 0 && err != nullptr) kv_error(err, KV_ERR_LEN);
         nrow = (int)min((int64_t)per, rows - r0);
         // the ends of what the rows see do not fall from row to row (rows that see nothing come first)
         int64_t t_lo = 0, t_hi = 0;
         all_lo = all_hi = 0;
         if (!bad) {
             int64_t x0, y0, x1, y1;
-            row_range(first + r0 / G, len, a.causal, a.window, x0, y0);
-            row_range(first + (r0 + nrow - 1) / G, len, a.causal, a.window, x1, y1);
+            row_range(first + token(0, G), len, a.causal, a.window, x0, y0);
+            row_range(first + token(nrow - 1, G), len, a.causal, a.window, x1, y1);
             t_lo = x0, t_hi = max(y0, y1);
             if (y0 > x0) all_lo = x1, all_hi = y0;
         }
         b_lo = t_lo / kKB, b_hi = (t_hi + kKB - 1) / kKB;
         nj = (int)((b_hi - b_lo + 3) / 4);
+        slot = -1;
+        if (piece >= 0) {
+            const int each = pf_each(nj, a.pieces), j0 = piece * each;
+            if (piece > 0 && j0 >= nj) return false;
+            if (each < nj) slot = 0;
+            b_lo += 4 * (int64_t)j0;
+            nj = min(each, nj - j0);
+            b_hi = min(b_hi, b_lo + 4 * (int64_t)nj);
+        }
         base = b_lo * kKB;
         return true;
     }
 };
 
-// q of the rows as f16 parts in the K-major swizzled layout, a warp per row; rows that are not there are zeros
+// a CTA's work: whole row tiles first, then the pieces of the others
+__device__ __forceinline__ bool pf_work(PfTile &w, const PfArgs &a, int per, unsigned int *err) {
+    const uint32_t whole = (uint32_t)(a.tiles * a.c.n_seqs * a.c.H - a.cut);
+    const bool cut = blockIdx.x >= whole;
+    const uint32_t v = blockIdx.x - whole, up = cut ? v / (uint32_t)a.pieces : 0;
+    if (!w.init(a, per, cut ? whole + up : blockIdx.x, cut ? (int)(v - up * a.pieces) : -1, err)) return false;
+    if (w.slot >= 0) w.slot = (int)v;
+    return true;
+}
+
+// the bits of the largest magnitude, as f32 (an infinity's or more if there is one or a NaN)
+template <int N>
+__device__ __forceinline__ uint32_t pf_amax(const Raw4<float> (&x)[N]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float4 w = x[e].w;
+        m = max(max(m, __float_as_uint(w.x) & 0x7fffffffu), max(__float_as_uint(w.y) & 0x7fffffffu, __float_as_uint(w.z) & 0x7fffffffu));
+        m = max(m, __float_as_uint(w.w) & 0x7fffffffu);
+    }
+    return m;
+}
+template <typename T, int N>
+__device__ __forceinline__ uint32_t pf_amax(const Raw4<T> (&x)[N]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m = __vmaxu2(m, __vmaxu2(x[e].w.x & 0x7fff7fffu, x[e].w.y & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    return m << 16;
+}
+
+// q of the rows as f16 parts in the K-major swizzled layout, by warps 0-7: 16 bytes a lane, eight loads in flight; rows that are not
+// there are zeros
 template <typename T, int D>
 __device__ __forceinline__ void pf_stage_q(const PfArgs &a, const PfTile &w, uint8_t *sm, float *s_rs, int count) {
     constexpr bool TWO = sizeof(T) == 4;
     using C = PfCfg<D, TWO>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
-#pragma unroll 2
-    for (int r = warp; r < count; r += kPfThreads / 32) {
-        float x[D / 32];
+    constexpr int N = TWO ? 1 : 2, LPR = D / (4 * N), RPW = 32 / LPR, FLY = 8;       // fours of elements per lane, lanes per row, rows per load
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group, col = (lane % LPR) * 4 * N;
+#pragma unroll 1
+    for (int r0 = warp * RPW + lane / LPR; r0 < count; r0 += 8 * RPW * FLY) {
+        Raw4<T> x[FLY][N];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-        if (r < w.nrow) {
-            const int64_t rr = w.r0 + r, i = rr / G;
-            const T *p = static_cast<const T *>(a.q) + (w.lo + i) * a.qt + (int64_t)(w.h * G + (int)(rr - i * G)) * a.qh + lane * (D / 32);
-            if constexpr (D == 128) {
-                load4(p, x);
+        for (int z = 0; z < FLY; ++z) {
+            const int r = r0 + 8 * RPW * z;
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[z][e] = Raw4<T>{};
+            if (r < w.nrow) {
+                const T *p = static_cast<const T *>(a.q) + (w.lo + w.token(r, G)) * a.qt + (int64_t)w.head(r, G) * a.qh + col;
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[z][e] = *reinterpret_cast<const Raw4<T> *>(p + 4 * e);
+            }
+        }
+#pragma unroll
+        for (int z = 0; z < FLY; ++z) {
+            const int r = r0 + 8 * RPW * z;
+            uint32_t amax = pf_amax(x[z]);
+            if constexpr (LPR == 32) {
+                amax = __reduce_max_sync(0xffffffffu, amax);
             } else {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[e] = static_cast<float>(p[e]);
+                for (int o = LPR / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            }
+            const bool fin = amax < 0x7f800000u;
+            const int ex = fin ? row_exponent(__uint_as_float(amax)) : 0;
+            const float down = fin ? pow2i(-ex) * a.sign : __int_as_float(0x7fc00000);   // a row with a NaN or an infinity becomes NaN
+            uint32_t hi[2 * N], lo[2 * N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float y[4];
+                unpack4(x[z][e], y);
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const float y0 = fin ? y[k] * down : down, y1 = fin ? y[k + 1] * down : down;
+                    hi[2 * e + (k >> 1)] = pack_f16(y0, y1);
+                    const float2 f = unpack_f16(hi[2 * e + (k >> 1)]);
+                    lo[2 * e + (k >> 1)] = pack_f16(y0 - f.x, y1 - f.y);
+                }
+            }
+            // 16-byte unit (col / 8) % 8 of row r % 128 in the 64-column half col / 64
+            uint8_t *dst = sm + C::OFF_Q + (r >> 7) * C::QT + (col >> 6) * 16384 + (r & 127) * 128 + ((((col >> 3) & 7) ^ (r & 7)) << 4) + (col & 7) * 2;
+            if (r < count) {
+                if constexpr (TWO) {
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(dst + C::TILES * C::QT) = make_uint2(lo[0], lo[1]);
+                } else {
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                }
+                if (lane % LPR == 0) s_rs[r] = pow2i(ex) * a.c_log2;
             }
         }
-        float amax = 0.0f;
-        bool fin = true;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            amax = fmaxf(amax, fabsf(x[e]));
-            fin = fin && fabsf(x[e]) <= 3.402823466e38f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        fin = __all_sync(0xffffffffu, fin);
-        const int ex = fin ? row_exponent(amax) : 0;
-        const float down = fin ? pow2i(-ex) * a.sign : __int_as_float(0x7fc00000);   // a row with a NaN or an infinity becomes NaN
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) x[e] = fin ? x[e] * down : down;
-        const int t = r >> 7, rt = r & 127, col = lane * (D / 32);
-        // 16-byte unit (col / 8) % 8 of row rt in the 64-column half col / 64
-        uint8_t *dst = sm + C::OFF_Q + t * C::QT + (col >> 6) * 16384 + rt * 128 + ((((col >> 3) & 7) ^ (rt & 7)) << 4) + (col & 7) * 2;
-#pragma unroll
-        for (int e = 0; e < D / 32; e += 2) {
-            const uint32_t p0 = pack_f16(x[e], x[e + 1]);
-            *reinterpret_cast<uint32_t *>(dst + 2 * e) = p0;
-            if constexpr (TWO) {
-                const float2 f = unpack_f16(p0);
-                *reinterpret_cast<uint32_t *>(dst + C::TILES * C::QT + 2 * e) = pack_f16(x[e] - f.x, x[e + 1] - f.y);
-            }
-        }
-        if (lane == 0) s_rs[r] = pow2i(ex) * a.c_log2;
     }
+}
+// ... then the tensor core and the other softmax warps have it
+__device__ __forceinline__ void pf_q_staged(const PfBars &bar, int lane) {
+    fence_proxy_async_smem();
+    warp_arrive(bar.q_full, lane);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
 // warp 12: pages and scales of the tiles, 32 blocks at a time, one a lane
@@ -566,15 +643,15 @@ __device__ __forceinline__ void pf_tile_weights_f32(uint32_t ts, float rs, const
     grid_dep_launch();                                                                                                        \
     grid_dep_wait();                                                                                                          \
     PfTile w;                                                                                                                 \
-    if (!w.init(a, C::ROWS, err)) return;                                                                                     \
+    if (!pf_work(w, a, C::ROWS, err)) return;                                                                                 \
     const int nt = w.nrow > 128 ? 2 : 1, nj = w.nj;                                                                           \
     if (threadIdx.x == 0) {                                                                                                   \
         *abort_flag = 0;                                                                                                      \
+        abort_flag[1] = w.slot;                                                                                               \
         const_cast<PfBars &>(bar).init(INFO_READERS);                                                                         \
     }                                                                                                                         \
     if (warp == 13) tmem_alloc(tmem_holder, 512);                                                                             \
-    pf_stage_q<T, D>(a, w, sm, s_rs, nt * 128);                                                                               \
-    fence_proxy_async_smem();                                                                                                 \
+    tc_fence_before();                                                                                                        \
     __syncthreads();                                                                                                          \
     tc_fence_after();                                                                                                         \
     const uint32_t tmem = *tmem_holder
@@ -584,7 +661,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsigned int *err) {
     PF_PROLOGUE(T, D, 4 * nt + 4);
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 12) {
             pf_lookup<false>(a, w, info, bar, err, abort_flag);
         } else if (warp == 13) {
@@ -594,7 +671,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             auto next = [&]() {
                 if (++slot == C::SLOTS) slot = 0, ph ^= 1;
             };
-            bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
+            bool ok = nj > 0 && warp_wait2(bar.q_full, bar.op_full, 0, err, abort_flag);
             if (ok) {
                 tc_fence_after();
                 mma.scores(s0, 0, 0);
@@ -635,16 +712,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                 }
                 if (more) mma_commit_warp(bar.op_empty + sk);
             }
-            if (*abort_flag) {                                 // products in flight end before the TMEM is freed
-                mma_commit_warp(bar.drain);
-                mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
-            }
+            // products and arrivals in flight end before the TMEM and the barriers go
+            mma_commit_warp(bar.drain);
+            mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
         }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         pf_widen<D, false>(a, w, sm + C::OFF_OP, info, bar, err, abort_flag);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        pf_stage_q<T, D>(a, w, sm, s_rs, nt * 128);
+        pf_q_staged(bar, lane);
         const int t = warp >> 2, r = threadIdx.x;
         if (t < nt) {
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -652,7 +730,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             int v0 = 0, v1 = 0;                                 // what the row sees, from the first tile's start
             if (r < w.nrow && !w.bad) {
                 int64_t x, y;
-                row_range(w.first + (w.r0 + r) / a.group, w.len, a.causal, a.window, x, y);
+                row_range(w.first + w.token(r, a.group), w.len, a.causal, a.window, x, y);
                 v0 = (int)max(x - w.base, (int64_t)0), v1 = (int)max(y - w.base, (int64_t)0);
             }
             const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
@@ -709,10 +787,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             float l, l1;
             f2_unpack(l2, l, l1);
             l += l1;
-            const float inv = l == 0.0f ? 0.0f : info[(nj + kPfInfo - 1) % kPfInfo].g / l;
-            const int64_t i = (w.r0 + r) / a.group;
-            const int gq = (int)(w.r0 + r - i * a.group);
-            T *dst = static_cast<T *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh;
+            const int piece = abort_flag[1];
+            const float gl = info[(nj + kPfInfo - 1) % kPfInfo].g, inv = piece >= 0 ? gl : l == 0.0f ? 0.0f : gl / l;
+            float *pd = a.part + ((int64_t)piece * C::ROWS + r) * (D + 4);
+            if (piece >= 0 && r < w.nrow) *reinterpret_cast<float2 *>(pd + D) = make_float2(m, l);
+            T *dst = static_cast<T *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh;
 #pragma unroll 1
             for (int e = 0; e < D / 32; ++e) {
                 uint32_t x[32];
@@ -726,7 +805,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                         float y[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) y[z] = nj > 0 && l != 0.0f ? __uint_as_float(x[k + z]) * inv : 0.0f;
-                        store4(dst + 32 * e + k, y);
+                        if (piece >= 0) store4(pd + 32 * e + k, y);
+                        else store4(dst + 32 * e + k, y);
                     }
                 }
             }
@@ -757,7 +837,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
             auto next = [&]() {
                 if (++slot == C::SLOTS) slot = 0, ph ^= 1;
             };
-            bool ok = nj > 0 && warp_wait(bar.op_full, 0, err, abort_flag);
+            bool ok = nj > 0 && warp_wait2(bar.q_full, bar.op_full, 0, err, abort_flag);
             if (ok) {
                 tc_fence_after();
                 mma.scores(s0, 0, 0);
@@ -784,23 +864,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
                 mma_commit_warp(bar.op_empty + slot);
                 next();
             }
-            if (*abort_flag) {                                 // products in flight end before the TMEM is freed
-                mma_commit_warp(bar.drain);
-                mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
-            }
+            // products and arrivals in flight end before the TMEM and the barriers go
+            mma_commit_warp(bar.drain);
+            mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         pf_widen<D, true>(a, w, sm + C::OFF_OP, info, bar, err, abort_flag);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        pf_stage_q<float, D>(a, w, sm, s_rs, 128);
+        pf_q_staged(bar, lane);
         // Two warpgroups take the tiles' softmax in turn, and each sums half of the columns of every tile's P V.
         const int a2 = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, ts = tmem + C::COL_S + lanes, to = tmem + C::COL_O + a2 * (D / 2) + lanes;
         int v0 = 0, v1 = 0;                                    // what the row sees, from the first tile's start
         if (r < w.nrow && !w.bad) {
             int64_t x, y;
-            row_range(w.first + (w.r0 + r) / a.group, w.len, a.causal, a.window, x, y);
+            row_range(w.first + w.token(r, a.group), w.len, a.causal, a.window, x, y);
             v0 = (int)max(x - w.base, (int64_t)0), v1 = (int)max(y - w.base, (int64_t)0);
         }
         const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
@@ -862,20 +943,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
         float l, l1;
         f2_unpack(l2, l, l1);
         l += l1;
+        float last_m = -INFINITY;
         if (nj > 0) {
-            const float last = s_m[((nj - 1) & 3) * 128 + r];
-            l *= exp2_approx(m - (last == -INFINITY ? 0.0f : last));
+            last_m = s_m[((nj - 1) & 3) * 128 + r];
+            l *= exp2_approx(m - (last_m == -INFINITY ? 0.0f : last_m));
         }
         s_m[((nj + 1 - a2) & 3) * 128 + r] = l;                 // two of the places that tiles nj - 1 and nj - 2 did not use
         if (a2 == ((nj - 1) & 1)) s_rs[r] = g;
         warp_arrive(bar.l_full, lane);
         warp_wait(bar.l_full, 0, err, abort_flag);
         l = s_m[((nj + 1) & 3) * 128 + r] + s_m[(nj & 3) * 128 + r];
-        const float inv = l == 0.0f ? 0.0f : s_rs[r] / l;
+        const int piece = abort_flag[1];
+        const float inv = piece >= 0 ? s_rs[r] : l == 0.0f ? 0.0f : s_rs[r] / l;
         if (r < w.nrow) {
-            const int64_t i = (w.r0 + r) / a.group;
-            const int gq = (int)(w.r0 + r - i * a.group);
-            float *dst = static_cast<float *>(a.out) + (w.lo + i) * a.ot + (int64_t)(w.h * a.group + gq) * a.oh + a2 * (D / 2);
+            float *dst = static_cast<float *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh + a2 * (D / 2);
+            if (piece >= 0) {
+                float *pd = a.part + ((int64_t)piece * C::ROWS + r) * (D + 4);
+                if (a2 == 0) *reinterpret_cast<float2 *>(pd + D) = make_float2(last_m, l);
+                dst = pd + a2 * (D / 2);
+            }
 #pragma unroll
             for (int k = 0; k < D / 2; k += 4) {
                 float y[4];
@@ -894,37 +980,141 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
     }
 }
 
+// Joins the pieces of the row tiles that were cut: a CTA per row tile and 8 rows, a warp per row.  Lane p has piece p's maximum and sum.
+constexpr int kPfMostPieces = 32, kPfJoinRows = 8;
 template <typename T, int D>
-int prefill_t(PfArgs &a, unsigned int *err, cudaStream_t s) {
+__global__ void __launch_bounds__(256) kv_tiles_join_kernel(PfArgs a) {
+    constexpr int V = D / 32, ROWS = PfCfg<D, sizeof(T) == 4>::ROWS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_launch();
+    grid_dep_wait();
+    PfTile w;
+    if (!w.init(a, ROWS, (uint32_t)(a.tiles * a.c.n_seqs * a.c.H - a.cut) + blockIdx.x, -1, nullptr)) return;
+    const int each = pf_each(w.nj, a.pieces), r = blockIdx.y * kPfJoinRows + warp;
+    if (each >= w.nj || r >= w.nrow) return;                   // done in one piece; no such row
+    const int n = (w.nj + each - 1) / each;
+    const int64_t step = (int64_t)ROWS * (D + 4);
+    const float *src = a.part + (int64_t)blockIdx.x * a.pieces * step + (int64_t)r * (D + 4);
+    const float2 ml = lane < n ? *reinterpret_cast<const float2 *>(src + lane * step + D) : make_float2(-INFINITY, 0.0f);
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = exp2_approx(ml.x - (m == -INFINITY ? 0.0f : m));
+    float l = ml.y * f, acc[V];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+        const float fp = __shfl_sync(0xffffffffu, f, p);
+        float y[V];
+        if constexpr (V == 4) load4(src + p * step + V * lane, y);
+        else *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(src + p * step + V * lane);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += fp * y[e];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *dst = static_cast<T *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= inv;
+    if constexpr (V == 4) {
+        store4(dst, acc);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) dst[e] = T(acc[e]);
+    }
+}
+
+// Which row tiles are cut.  A CTA takes a row tile, and a wave one per SM: what does not fill a wave leaves SMs idle for as long as a
+// row tile takes, so the last row tiles (the shortest) are cut along the tokens, all of them where there are not enough for a wave.
+// Whole / cut in us, 4 KV heads of 128: f32, 112 rows on a sequence of 4096 tokens 66 / 22, on 4 of 32768 493 / 76, on 48 of 2048 (192 row
+// tiles) 83 / 71; bf16, 511 rows on 4 of 32768 428 / 128, 1400 on 8 of 4096 132 / 108.  The lengths are the device's, so max_kv stands for
+// all: ragged sequences gain less (256 us for 48 of 100 to 16384 tokens, half of it the longest one's).
+struct PfCut {
+    int64_t tiles, cut;         // row tiles of the longest sequence; those (of all sequences and heads) that do not fill a wave
+    int most;                   // pieces at most: three waves of partials are room enough
+};
+PfCut pf_cut(int32_t n_seqs, int32_t H, int rows, int group, int64_t n_tokens, int64_t max_q) {
+    if (max_q > n_tokens) max_q = n_tokens;
+    const int64_t sms = sm_count(), tiles = (max_q * group + rows - 1) / rows;
+    if ((double)n_seqs * tiles * H > INT_MAX) return {tiles, 0, 1};                  // (refused by the call)
+    int64_t jobs = n_seqs * tiles;
+    if (n_tokens < n_seqs * max_q) {                           // of ragged sequences about
+        const int64_t about = (n_tokens * group + (int64_t)n_seqs * (rows / 2)) / rows;
+        jobs = about < n_seqs ? n_seqs : about < jobs ? about : jobs;
+    }
+    PfCut x = {tiles, jobs * H % sms, 1};
+    // (where there are not enough for a wave, those that the estimate has missed too)
+    if (jobs * H < sms) x.cut = n_seqs * tiles * H < sms ? n_seqs * tiles * H : sms;
+    if (x.cut > 0) x.most = (int)(3 * sms / x.cut < kPfMostPieces ? 3 * sms / x.cut : kPfMostPieces);
+    return x;
+}
+int pf_rows(int dtype) { return dtype == MQKV_F32 ? PfCfg<128, true>::ROWS : PfCfg<128, false>::ROWS; }
+// Pieces: what takes the fewest tile steps one after another (within 10% of the best number of pieces nearly everywhere it was tried:
+// 1 to 48 sequences, 112 to 1400 rows, 2048 to 32768 tokens).
+int pf_pieces(const PfCut &x, const PfArgs &a, int rows, int64_t max_kv) {
+    const int64_t last = x.cut / ((int64_t)a.c.n_seqs * a.c.H) + 1;                  // row tiles of a sequence up to the longest that is cut
+    int64_t seen = a.causal && last < x.tiles ? max_kv - a.max_q + last * rows / a.group : max_kv;
+    seen = seen < 0 ? 0 : seen > max_kv ? max_kv : seen;
+    if (a.window > 0 && a.window + rows / a.group < seen) seen = a.window + rows / a.group;
+    const double steps = (double)seen / kPfN;
+    int best = 1;
+    double least = steps + kPfPieceSteps;
+    for (int s = 2; s <= x.most && s <= steps; ++s) {
+        const double t = (double)((x.cut * s + sm_count() - 1) / sm_count()) * (steps / s + kPfPieceSteps) + kPfJoinSteps + s * kPfPartSteps;
+        if (t < least) least = t, best = s;
+    }
+    return best;
+}
+constexpr size_t pf_part_bytes(int rows, int D) { return (size_t)rows * (D + 4) * 4; }
+
+template <typename T, int D>
+int prefill_t(PfArgs &a, int64_t n_tokens, int64_t max_kv, void *ws, unsigned int *err, cudaStream_t s) {
     using C = PfCfg<D, sizeof(T) == 4>;
     const int slot = kAttrSlotKv + 8 + 2 * (sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 1 : 2) + (D == 128);
     void (*fn)(PfArgs, unsigned int *);
     if constexpr (sizeof(T) == 4) fn = kv_tiles_f32_kernel<D>;
     else fn = kv_tiles_kernel<T, D>;
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), C::SMEM, slot);
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), C::SMEM, slot);
     if (rc != MQ_OK) return rc;
-    a.tiles = (int)((a.max_q * a.group + C::ROWS - 1) / C::ROWS);
-    const int64_t grid = (int64_t)a.c.H * a.c.n_seqs * a.tiles;
+    const PfCut x = pf_cut(a.c.n_seqs, a.c.H, C::ROWS, a.group, n_tokens, a.max_q);
+    a.pieces = pf_pieces(x, a, C::ROWS, max_kv);
+    a.cut = a.pieces > 1 ? (int)x.cut : 0;
+    a.part = static_cast<float *>(ws);
+    const double grid = (double)a.c.H * a.c.n_seqs * x.tiles + (double)a.cut * (a.pieces - 1);
     if (grid > INT_MAX)
-        return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences x %d KV heads x %d row tiles exceed the grid", a.c.n_seqs, a.c.H, a.tiles);
-    return cuda_error(launch_pdl(fn, dim3((unsigned)grid), dim3(kPfThreads), C::SMEM, s, a, err), "mqkv_attention (tiles) launch");
+        return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences x %d KV heads x %lld row tiles exceed the grid", a.c.n_seqs, a.c.H, (long long)x.tiles);
+    a.tiles = (int)x.tiles;
+    rc = cuda_error(launch_pdl(fn, dim3((unsigned)grid), dim3(kPfThreads), C::SMEM, s, a, err), "mqkv_attention (tiles) launch");
+    if (rc != MQ_OK || a.cut == 0) return rc;
+    const int64_t most = a.max_q * a.group, rows = most < C::ROWS ? most : C::ROWS;
+    return cuda_error(launch_pdl(kv_tiles_join_kernel<T, D>, dim3((unsigned)a.cut, (unsigned)((rows + kPfJoinRows - 1) / kPfJoinRows)), dim3(256), 0,
+                                 s, a),
+                      "mqkv_attention (tiles) join launch");
 }
 
 }  // namespace
 
-int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, unsigned int *err, cudaStream_t s) {
+size_t kv_prefill_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int group, int64_t n_tokens, int64_t max_q) {
+    const PfCut x = pf_cut(n_seqs, H, pf_rows(dtype), group, n_tokens, max_q);
+    return x.most > 1 ? (size_t)x.cut * x.most * pf_part_bytes(pf_rows(dtype), D) : 256;
+}
+
+int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
     PfArgs a;
     a.c = c, a.r = r, a.q = p.q, a.out = p.out, a.qt = p.qt, a.qh = p.qh, a.ot = p.ot, a.oh = p.oh;
     a.group = p.group, a.causal = p.causal, a.max_q = p.max_q, a.window = p.window;
     a.c_log2 = fabsf(p.scale) * kLog2e;
     a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
+    auto go = [&](auto launch) { return launch(a, p.n_tokens, p.max_kv, ws, err, s); };
     if (c.D == 128)
-        return p.dtype == MQKV_F32   ? prefill_t<float, 128>(a, err, s)
-               : p.dtype == MQKV_F16 ? prefill_t<__half, 128>(a, err, s)
-                                     : prefill_t<__nv_bfloat16, 128>(a, err, s);
-    return p.dtype == MQKV_F32   ? prefill_t<float, 64>(a, err, s)
-           : p.dtype == MQKV_F16 ? prefill_t<__half, 64>(a, err, s)
-                                 : prefill_t<__nv_bfloat16, 64>(a, err, s);
+        return p.dtype == MQKV_F32   ? go(prefill_t<float, 128>)
+               : p.dtype == MQKV_F16 ? go(prefill_t<__half, 128>)
+                                     : go(prefill_t<__nv_bfloat16, 128>);
+    return p.dtype == MQKV_F32   ? go(prefill_t<float, 64>)
+           : p.dtype == MQKV_F16 ? go(prefill_t<__half, 64>)
+                                 : go(prefill_t<__nv_bfloat16, 64>);
 }
 
 }  // namespace mq

@@ -279,6 +279,24 @@ def test_prefill(dtype, heads, kv_heads, dim, page):
     check_attention(s, new, heads, dtype, window=100, seed=2)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(window=700), dict(window=3), dict(causal=False), dict(scale=0.0), dict(qscale=6.0), dict(max_kv=100000)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()) or "causal")
+def test_few_row_tiles(dtype, dim, kw):
+    # too few row tiles for every SM: they are cut along the tokens, into more pieces than the short sequences have tiles for
+    s = Setup([4100, 0, 37, 2500, 1], 2, dim, 64, seed=dim)
+    check_attention(s, [40, 3, 37, 12, 0], 8, dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype,lens,new,heads,kv_heads", [("f32", [1500] * 40, [20] * 40, 16, 4), ("f16", [1500] * 40, [20] * 40, 16, 4),
+                                                           ("f32", [2000], [640], 32, 8), ("bf16", [1500, 3000], [640, 645], 32, 8)])
+def test_last_row_tiles_cut(dtype, lens, new, heads, kv_heads):
+    # a wave of whole row tiles and more, the rest cut: some of many sequences, and the first of several per sequence
+    s = Setup(lens, kv_heads, 64, 64, layers=1, seed=len(lens))
+    check_attention(s, new, heads, dtype, layer=0)
+
+
 @pytest.mark.parametrize("n,dtype", [(257, "f32"), (1500, "f16")])
 def test_many_sequences(n, dtype):
     # more than the plan's shared memory holds, and more than one round of its scan; most of them short, some empty
