@@ -17,13 +17,15 @@
 // roundings showed in f16 outputs.)
 //
 // Many rows of long sequences are 636 jobs of 40 to 64 tiles in the largest case measured: 436 us, 1056 TFLOP/s (of 1864 that cuBLAS
-// reaches); what is left is the chain MMA - commit - softmax - arrival - MMA of each tile and a CTA's beginning and end (8 tiles' time).
+// reaches; tensor pipe 50%, issue 49%); what is left is the chain MMA - commit - softmax - arrival - MMA of each tile and a CTA's beginning
+// and end (8 tiles' time).
 //
 // f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
 // The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
 // each tile's P V goes to a fresh accumulator and is added to the row's sum in registers, rounding to nearest, under the
 // products of the next tiles: one row tile per CTA, S and O double-buffered, warps 0-3 and 4-7 the softmax of the tiles in turn.  A prompt
-// of 3314 tokens, 28 query heads on 4 of 128: 179 us (157 GFLOP in two parts: 880 TFLOP/s); the softmax's issue slots bound it.
+// of 3314 tokens, 28 query heads on 4 of 128: 179 us (157 GFLOP in two parts: 880 TFLOP/s); the tiles' chain bounds it
+// (tensor pipe 40%, issue 49%).
 //
 // q is staged by the softmax warps while the others look up and widen the first tiles: with all warps and before everything else, a CTA's
 // beginning took 5 us more (the prompt 187 us, the 16-bit chunks 478).
