@@ -160,6 +160,19 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// A wait looks at a phase's parity only, so a barrier must not complete a phase while a warp that waits for the one before it has not
+// looked.  Why none does (tests/test_kv_tiles_model.py walks the waits and arrivals of both kernels through schedules):
+//   op_full, op_empty    the ring: a place is filled after its products were committed, which came after both fillers' arrivals
+//   info_full, info_empty  the lookup's ring: refilled after every reader has arrived
+//   s_full[b]            the next scores of a buffer are issued after p_full of its last ones, to which every reader of s_full arrives
+//   p_full[b]            only the MMA warp waits; the next weights need scores that it issues after that wait
+//   o_done[b]            f32 rows: the next products wait for o_free, to which all eight warps arrive.  16-bit rows: they wait for p_full of
+//                        the same row tile, to which its four warps arrive
+//   o_free[b]            only the MMA warp waits; the warps' next arrivals need products that it issues after that wait
+//   m_full[b]            the warpgroup that arrives waits, before its next arrival, for the other one's, sent after that one's wait; the wait after the
+//                        last tile is for an arrival that has no successor
+//   q_full, l_full, drain  one phase
+// (The sums of f32 rows may not wait for p_full: its owner can arrive for tile j + 2 before the other warpgroup looks for tile j.)
 struct PfBars {
     uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full, *q_full;
     __device__ __forceinline__ explicit PfBars(uint64_t *b) {
@@ -897,7 +910,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
             const int at = j & 1;
             if (j >= 2) {                                      // half of tile j - 2's products
                 const uint32_t ph = ((j >> 1) - 1) & 1;
-                if (!warp_wait2(bar.p_full + at, bar.o_done + at, ph, err, abort_flag)) break;     // the factors, the products
+                // the products, and after the last tile of the other warpgroup its factors: those of its earlier tiles came with the maxima
+                // that this one waited for in its own tile j - 1
+                if (!warp_wait(bar.o_done + at, ph, err, abort_flag)) break;
+                if (j == nj + 1 && at != a2 && !warp_wait(bar.m_full + at, ph, err, abort_flag)) break;
                 const float f = s_f[((j - 2) & 3) * 128 + r];
                 const uint64_t ff = f2_pack(f, f);
                 tc_fence_after();
