@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "mq_kv_attn.cuh"
+#include "mq_kv_join.h"
 
 namespace mq {
 namespace {
@@ -40,12 +41,6 @@ struct AtArgs {
     uint32_t *prefix;           // [n_seqs + 1][2]: places and units before each sequence
     struct AtJoin *join;        // [workers]
     float *part;                // [worker][2][R rows][D + 4]: o, m, l
-};
-
-// a row pass that began with a worker and ends with another: its partials are number 1 of workers first .. last - 1 and number 0 of the last
-struct AtJoin {
-    int32_t nrow, last, h, r0;      // nrow 0: none
-    int64_t tok;
 };
 
 // equal shares of the places: the first rem of them have one more
@@ -199,10 +194,8 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
     }
     __syncthreads();
     const uint32_t total = prefix[a.c.n_seqs].x, workers = min((uint32_t)a.workers, total), worker = blockIdx.x * kAtWarps + warp;
-    if (worker >= workers) {                                  // every share has a place at least
-        if (lane == 0) a.join[worker].nrow = 0;
-        return;
-    }
+    if (lane == 0) a.join[worker].nrow = 0;                   // until there is one: the join must not follow what an earlier call has left
+    if (worker >= workers) return;                            // every share has a place at least
     const AtShare shares(total, workers);
     const int H = a.c.H, G = a.group;
     // the first unit at or after a place
@@ -222,10 +215,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
     uint32_t edge = lane < 2 ? unit_at(shares.begin(worker + lane)) : 0;
     const uint32_t u0 = __shfl_sync(0xffffffffu, edge, 0);
     const int mine = (int)(__shfl_sync(0xffffffffu, edge, 1) - u0);
-    if (mine == 0) {
-        if (lane == 0) a.join[worker].nrow = 0;
-        return;
-    }
+    if (mine == 0) return;
 
     // 32 of the warp's units at a time, one a lane: page, scales, where in the page and which head
     int pg = -1, at = 0;
@@ -401,7 +391,13 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
 #pragma unroll 1
       for (; k < stop; ++k) {
         const int li = k & 31;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar + slot, phase, err, KV_ERR_WAIT, nullptr))) return;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar + slot, phase, err, KV_ERR_WAIT, nullptr))) {
+            for (int i = 0; i < RING && k + i < mine; ++i) {  // the copies in flight end (again with a limit) before their memory goes
+                mbar_wait(bar + slot, phase, err, KV_ERR_WAIT, nullptr);
+                if (++slot == RING) slot = 0, phase ^= 1;
+            }
+            return;
+        }
         const uint8_t *sk = ring + slot * C::SLOT, *sv = sk + C::BLK;
         // scores of 32 tokens: four n-tiles of 8
         float s[MT][4][4];
@@ -594,7 +590,10 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
     const int row = blockIdx.y, lane = threadIdx.x & 31, warp = FEW ? 0 : threadIdx.x >> 5;
     const int mine = FEW ? blockIdx.x * 4 + (threadIdx.x >> 5) : lane < 8 ? blockIdx.x * 8 + lane : a.workers;
     AtJoin w = {0, 0, 0, 0, 0};
-    if (mine < a.workers && (!FEW || lane == 0)) w = a.join[mine];
+    if (mine < a.workers && (!FEW || lane == 0)) {
+        w = a.join[mine];
+        if (!at_join_holds(w, mine, a.workers, R, a.c.H, a.group, a.r.n_tokens)) w.nrow = 0;
+    }
     for (uint32_t todo = __ballot_sync(0xffffffffu, row < w.nrow); todo != 0; todo &= todo - 1) {
         const int from = __ffs(todo) - 1, first = __shfl_sync(0xffffffffu, mine, from);
         const int last = __shfl_sync(0xffffffffu, w.last, from), n = last - first + 1;
