@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(TIN) == 4 ? 2 : 3) kv_a
     } else {
         b = kv_find_seq(rows, c.n_seqs, u, 2, shift);
         u0 = (rows.begin(b) >> shift) + 2 * (int64_t)b;
+        if (u < u0) return;                                                     // (cu does not begin at 0: rows of no sequence)
     }
     int64_t lo, hi;
     rows.of(b, lo, hi);

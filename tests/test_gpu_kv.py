@@ -131,6 +131,25 @@ def test_append_token_by_token_and_strided():
     s.check_pool()
 
 
+@pytest.mark.parametrize("before,after", [(300, 0), (130, 400), (1000, 7)])
+def test_append_where_cu_does_not_begin_at_0(before, after):
+    # rows before cu[0] and past cu[n] are no sequence's: nothing is read or written for them
+    new = [3, 40, 0, 200]
+    s = Setup([40, 45, 33, 210], 2, 64, 32, seed=12)
+    r = np.random.default_rng(6)
+    x = r.standard_normal((2, before + sum(new) + after, 2, 64)).astype(np.float32)
+    xt = dev(x)
+    kv.mqkv_append(s.cache, s.seqs, 1, xt[0], xt[1], i32(before + np.concatenate([[0], np.cumsum(new)])))
+    status()
+    at = before
+    for b, n in enumerate(new):
+        for half in range(2):
+            if n:
+                s.m.append(1, half, s.rows[b], s.lens[b], x[half, at:at + n])
+        at += n
+    s.check_pool()
+
+
 def test_append_of_values_that_cannot_be_a_scale():
     s = Setup([70, 33, 40, 20], 1, 64, 64, seed=4)
     x = np.random.default_rng(5).standard_normal((70 + 1 + 8 + 20, 1, 64)).astype(np.float32)
