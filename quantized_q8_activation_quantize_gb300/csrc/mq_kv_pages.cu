@@ -32,25 +32,26 @@ struct Ws {
 };
 
 // exclusive prefix sum over the block's values; *total gets the sum.  Two barriers, reusable at once.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int *total) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *s_warp, T *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    int w = s_warp[lane];                       // 32 warps: one sum a lane
-    int z = w;
+    T w = s_warp[lane];                         // 32 warps: one sum a lane
+    T z = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, z, o);
+        const T y = __shfl_up_sync(0xffffffffu, z, o);
         if (lane >= o) z += y;
     }
-    const int before = __shfl_sync(0xffffffffu, z - w, warp);
+    const T before = __shfl_sync(0xffffffffu, z - w, warp);
     *total = __shfl_sync(0xffffffffu, z, 31);
     return before + x - v;
 }
@@ -83,30 +84,31 @@ __device__ bool find_free(const int32_t *refs, int n_pages, int need, int32_t *l
 
 __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(KvPages p, const int32_t *add, Ws ws, unsigned int *err) {
     __shared__ int s_warp[32];
+    __shared__ int64_t s_need[32];
     grid_dep_launch();
     grid_dep_wait();
     const int T = 1 << p.tshift;
-    int need = 0;
+    int64_t need = 0;                           // of all sequences: may pass 32 bits, and is refused below
     bool bad = false;
     for (int base = 0; base < p.n_seqs; base += kPlanThreads) {
         const int b = base + threadIdx.x;
-        int k = 0;
+        int64_t k = 0;
         if (b < p.n_seqs) {
             const int64_t len = p.len[b], a = add != nullptr ? add[b] : 1;
             const int64_t have = (len + T - 1) >> p.tshift, want = (len + a + T - 1) >> p.tshift;
             if (len < 0 || a < 0 || want > p.max_pages || len + a > INT32_MAX) bad = true;
-            else k = (int)(want - have);
+            else k = want - have;
         }
-        int total;
-        const int at = need + block_scan(k, s_warp, &total);
-        if (b < p.n_seqs) ws.prefix[b] = at;
+        int64_t total;
+        const int64_t at = need + block_scan(k, s_need, &total);
+        if (b < p.n_seqs) ws.prefix[b] = (int)at;
         need += total;
     }
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) kv_error(err, KV_ERR_LEN);
         return;
     }
-    if (!find_free(p.refs, p.n_pages, need, ws.list, s_warp)) {
+    if (need > p.n_pages || !find_free(p.refs, p.n_pages, (int)need, ws.list, s_warp)) {
         if (threadIdx.x == 0) kv_error(err, KV_ERR_FULL);
         return;
     }
@@ -269,10 +271,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(KvPages p, Ws 
         const bool in = base + threadIdx.x < p.n_pages, used = in && p.refs[i] > 0;
         const bool hole = in && !used && i < n_live, mover = used && i >= n_live;
         int total;
-        int at = holes + block_scan(hole, s_warp, &total);
+        int at = holes + block_scan((int)hole, s_warp, &total);
         if (hole) ws.dst[at] = i;
         holes += total;
-        at = movers + block_scan(mover, s_warp, &total);
+        at = movers + block_scan((int)mover, s_warp, &total);
         if (mover) ws.src[at] = i;
         movers += total;
         if (in) ws.list[i] = i;                   // where page i goes

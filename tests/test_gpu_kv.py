@@ -537,6 +537,20 @@ def test_extend_defaults_and_refusals():
     s.check()
 
 
+@pytest.mark.parametrize("n_seqs,max_pages", [(65536, 32768), (65536, 65536), (65537, 65536)])
+def test_extend_by_more_pages_than_32_bits_count(n_seqs, max_pages):
+    import torch
+    # the pages that all sequences ask for are 2^31, 2^32 and 2^32 + 2^16: refused, and nothing changes
+    pool, refs = kv.alloc_pool(70000, 1, 1, 64, 32)
+    table = torch.empty((n_seqs, max_pages), dtype=torch.int32, device="cuda")
+    table[:, :2] = -1
+    length = torch.zeros(n_seqs, dtype=torch.int32, device="cuda")
+    c, s = kv.cache(pool, refs, 1, 1, 64, 32), kv.sequences(table, length)
+    kv.mqkv_extend(c, s, torch.full((n_seqs,), 32 * max_pages, dtype=torch.int32, device="cuda"), kv.alloc_pages_workspace(c, s))
+    status("free pages")
+    assert not length.any() and not refs.any() and (table[:, :2] == -1).all()
+
+
 def test_fork_and_release_refusals():
     s = PageSetup(12, 5, 3)
     s.p.extend([40, 10, 0, 0, 0])
