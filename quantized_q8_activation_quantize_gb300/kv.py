@@ -132,6 +132,13 @@ def _i32(name, t, n=None):
     return t.data_ptr()
 
 
+def _ws(t):
+    """(pointer, bytes) of a workspace: contiguous CUDA memory of any type."""
+    if not t.is_cuda or not t.is_contiguous():
+        _bad("the workspace is not a contiguous CUDA tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 # ----------------------------------------------------------------------- descriptions, memory ---
 
 def mqkv_page_layout(n_layers: int, n_kv_heads: int, head_dim: int, page_tokens: int) -> dict:
@@ -231,13 +238,12 @@ def mqkv_attention(cache, seqs, layer: int, q, out, cu, max_q: int, max_kv: int,
     return _check((_L or lib()).mqkv_attention(cache, seqs, layer, _dtype(dtype), *_rows("q", q, n, heads, D),
                                                *_rows("out", out, n, heads, D), heads, _i32("cu", cu, seqs.n_seqs + 1), n, max_q,
                                                max_kv, causal, window, D ** -0.5 if scale is None else scale,
-                                               workspace.data_ptr(), workspace.numel(), _on(stream, q)))
+                                               *_ws(workspace), _on(stream, q)))
 
 
 def mqkv_extend(cache, seqs, add, workspace, stream=None):
     """kv_len += add (int32 [n_seqs]; None: 1), with pages for the new tokens."""
-    return _check((_L or lib()).mqkv_extend(cache, seqs, _i32("add", add, seqs.n_seqs), workspace.data_ptr(), workspace.numel(),
-                                            _on(stream, workspace)))
+    return _check((_L or lib()).mqkv_extend(cache, seqs, _i32("add", add, seqs.n_seqs), *_ws(workspace), _on(stream, workspace)))
 
 
 def mqkv_release(cache, seqs, ids, stream=None):
@@ -246,12 +252,12 @@ def mqkv_release(cache, seqs, ids, stream=None):
 
 def mqkv_fork(cache, seqs, parent, child, workspace, stream=None):
     n = parent.numel()
-    return _check((_L or lib()).mqkv_fork(cache, seqs, _i32("parent", parent), _i32("child", child, n), n, workspace.data_ptr(),
-                                          workspace.numel(), _on(stream, workspace)))
+    return _check((_L or lib()).mqkv_fork(cache, seqs, _i32("parent", parent), _i32("child", child, n), n, *_ws(workspace),
+                                          _on(stream, workspace)))
 
 
 def mqkv_compact(cache, seqs, workspace, stream=None):
-    return _check((_L or lib()).mqkv_compact(cache, seqs, workspace.data_ptr(), workspace.numel(), _on(stream, workspace)))
+    return _check((_L or lib()).mqkv_compact(cache, seqs, *_ws(workspace), _on(stream, workspace)))
 
 
 def mqkv_copy_pages(cache, src, dst, stream=None):

@@ -182,6 +182,39 @@ def test_binding_refuses_wrong_tensors(L):
         kv.mqkv_append(c, s, 0, torch.zeros((7, 4, 128), dtype=torch.float64), torch.zeros((7, 4, 128), dtype=torch.float64))
 
 
+def test_binding_refuses_a_workspace_that_is_not_the_device_s(L, monkeypatch):
+    import torch
+
+    class OnDevice:                                          # a tensor of a device, as far as the binding looks
+        is_cuda, dtype = True, torch.int32
+
+        def __init__(self, shape, stride, size=4, contiguous=True):
+            self.shape, self.size, self.contiguous, self.strides = shape, size, contiguous, stride
+
+        numel = lambda self: int(np.prod(self.shape))        # noqa: E731
+        element_size = lambda self: self.size                # noqa: E731
+        is_contiguous = lambda self: self.contiguous         # noqa: E731
+        data_ptr = lambda self: WS                           # noqa: E731
+        get_device = lambda self: 0                          # noqa: E731
+        stride = lambda self: self.strides                   # noqa: E731
+    c, s = cache(), seqs()
+    monkeypatch.setattr(kv, "_on", lambda stream, t: None)
+    ids = OnDevice((1,), (1,))
+    q, out = OnDevice((3, 8, 128), (1024, 128, 1)), OnDevice((3, 8, 128), (1024, 128, 1))
+    q.dtype = out.dtype = torch.float32
+    calls = [lambda ws: kv.mqkv_extend(c, s, None, ws), lambda ws: kv.mqkv_fork(c, s, ids, ids, ws), lambda ws: kv.mqkv_compact(c, s, ws),
+             lambda ws: kv.mqkv_attention(c, s, 0, q, out, None, 1, 9, ws)]
+    for f in calls:
+        for ws in (torch.empty(1 << 20, dtype=torch.uint8), OnDevice((1 << 20, 2), (4, 1), contiguous=False)):
+            with pytest.raises(B.MQError, match="workspace is not a contiguous CUDA tensor"):
+                f(ws)
+    # its size counts in bytes
+    need = L.mqkv_pages_workspace_bytes(c, s)
+    assert kv._ws(OnDevice((need // 4,), (1,))) == (WS, need)
+    with pytest.raises(B.MQError, match="bytes, .* needed"):
+        kv.mqkv_extend(c, s, None, OnDevice((need // 4 - 1,), (1,)))
+
+
 # ------------------------------------------------------------- the model itself is pinned ---
 
 def test_model_append_closed_forms():
