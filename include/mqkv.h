@@ -25,8 +25,10 @@
  * stream, host checks before any launch, mq_last_error() names the values, no fallback).  The two
  * descriptions mqkv_cache and mqkv_seqs are host structs, read during the call only.  What only the
  * device can see (lengths, table entries, page counts) is checked there: a bad value is never followed,
- * it sets a bit that mqkv_device_status() reports, and the affected sequence is left out (its outputs
- * are zeros where the call has outputs).
+ * it sets a bit that mqkv_device_status() reports, and what it concerns is left out.  A bad length: the
+ * sequence (its outputs are zeros where the call has outputs).  A bad table entry: mqkv_append skips the
+ * blocks that lie in it, mqkv_read gives zeros for the tokens in it, and mqkv_attention gives zeros for all
+ * rows of a sequence of which any row would read it.
  */
 #ifndef MQKV_H
 #define MQKV_H

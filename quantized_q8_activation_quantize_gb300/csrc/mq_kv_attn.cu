@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 if (pg < 0 || pg >= a.c.n_pages) {
                     kv_error(err, KV_ERR_PAGE);
                     pg = -1;
+                    dk = -INFINITY;                           // no scale: the passes over the block are lost
                 } else {
                     const float *sc = reinterpret_cast<const float *>(a.c.pool + pg * a.c.page_bytes + a.c.off_s);
                     dk = sc[h * spp + sb];
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
     float rs[MT][RT], m[MT][RT], l[MT][RT];
     float o[MT][NT][4];
     float gmax = 0.0f;                                        // the largest V scale so far
+    bool lost = false;                                        // a block of this share's part of the pass has no page
 
     // the row pass of unit u: its rows' q and ranges; how many units of it are left
     auto begin = [&](uint32_t u, bool &fresh) -> uint32_t {
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         row_range(q.first + (r0 + nrow - 1) / G, q.len, a.causal, a.window, x1, y1);
         all_lo = (int)x1, all_hi = y0 > x0 ? (int)y0 : 0;
         gmax = 0.0f;
+        lost = false;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
 #pragma unroll
@@ -351,14 +354,22 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         if constexpr (C::QS) __syncwarp();
         return left;
     };
-    // the rows' sums leave: divided where the pass is whole, else as partial `which` of this worker
+    // the rows' sums leave: divided where the pass is whole, else as partial `which` of this worker.  Of a lost pass zeros leave, with a sum of
+    // weights below zero for the join
     auto end = [&](bool whole, int which) {
+        if (lost) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
+        }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int e = 0; e < RT; ++e) {
                 l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 1);
                 l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 2);
+                if (lost) l[t][e] = whole ? 0.0f : -1.0f;
                 const int rr = t * C::RT + g + 8 * e;
                 if (rr < nrow) {
                     const float f = whole ? (l[t][e] == 0.0f ? 0.0f : gmax / l[t][e]) : gmax;
@@ -429,6 +440,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
             }
         }
         const float dkb = __shfl_sync(0xffffffffu, dk0, li), dvb = __shfl_sync(0xffffffffu, dv0, li);
+        lost = lost || dkb == -INFINITY;
         const int t0 = (int)(blk + (k - k0)) * kKB;
         const bool inner = t0 >= all_lo && t0 <= all_hi - kKB;
         // the V scale reference moves to twice a scale that exceeds it
@@ -600,12 +612,14 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
         const float *base = a.part + row * (int64_t)(D + 4);
         auto part = [&](int c) { return base + (2 * (int64_t)c + (c < last)) * R * (D + 4); };
         float mm = -INFINITY, ll = 0.0f, acc[V];
+        bool lost = false;
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.0f;
         // 32 of this warp's partials at a time: a lane has the maximum and the sum of one
         for (int p0 = warp; p0 < n; p0 += 32 * JW) {
             const int p = p0 + JW * lane;
             const float2 ml = p < n ? *reinterpret_cast<const float2 *>(part(first + p) + D) : make_float2(-INFINITY, 0.0f);
+            lost = lost || __any_sync(0xffffffffu, ml.y < 0.0f);
             float mn = fmaxf(ml.x, mm);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -631,7 +645,7 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
         }
         float sum = ll;
         if constexpr (!FEW) {
-            if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = ll;
+            if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = lost ? -1.0f : ll;
             if (warp > 0) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) s_o[warp - 1][V * lane + e] = acc[e];
@@ -646,6 +660,7 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
 #pragma unroll
                 for (int x = 0; x < JW; ++x) {
                     const float f = exp2_approx(s_ml[x][0] - mb);
+                    lost = lost || s_ml[x][1] < 0.0f;
                     sum += s_ml[x][1] * f;
 #pragma unroll
                     for (int e = 0; e < V; ++e) acc[e] = x == 0 ? acc[e] * f : acc[e] + s_o[x - 1][V * lane + e] * f;
@@ -659,7 +674,7 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
             const int i = (r0 + row) / a.group;
             T *dst = static_cast<T *>(a.out) + (tok + i) * a.ot + (int64_t)(h * a.group + (r0 + row - i * a.group)) * a.oh + V * lane;
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] *= inv;
+            for (int e = 0; e < V; ++e) acc[e] = lost ? 0.0f : acc[e] * inv;
             if constexpr (V == 4) {
                 store4(dst, acc);
             } else {

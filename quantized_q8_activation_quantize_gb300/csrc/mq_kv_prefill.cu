@@ -79,7 +79,7 @@ struct PfCfg {
     static constexpr int OFF_RS = OFF_OP + SLOTS * OPT;     // row scales [ROWS]; f32 rows: then factors and maxima [4][128]
     static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 2 * 512 * 4 : 0);
     static constexpr int OFF_BAR = OFF_INFO + kPfInfo * (int)sizeof(PfInfo);
-    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 3;
+    static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 4;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1008;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA exceeds the per-CTA limit");
@@ -171,14 +171,14 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 //   o_free[b]            only the MMA warp waits; the warps' next arrivals need products that it issues after that wait
 //   m_full[b]            the warpgroup that arrives waits, before its next arrival, for the other one's, sent after that one's wait; the wait after the
 //                        last tile is for an arrival that has no successor
-//   q_full, l_full, drain  one phase
+//   q_full, l_full, pages, drain  one phase
 // (The sums of f32 rows may not wait for p_full: its owner can arrive for tile j + 2 before the other warpgroup looks for tile j.)
 struct PfBars {
-    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full, *q_full;
+    uint64_t *op_full, *op_empty, *info_full, *info_empty, *s_full, *p_full, *o_done, *o_free, *m_full, *drain, *l_full, *q_full, *pages;
     __device__ __forceinline__ explicit PfBars(uint64_t *b) {
         op_full = b, op_empty = op_full + kPfSlots, info_full = op_empty + kPfSlots, info_empty = info_full + kPfInfo;
         s_full = info_empty + kPfInfo, p_full = s_full + 2, o_done = p_full + 2, o_free = o_done + 2, m_full = o_free + 2, drain = m_full + 2;
-        l_full = drain + 1, q_full = l_full + 1;
+        l_full = drain + 1, q_full = l_full + 1, pages = q_full + 1;
     }
     // info_readers: warps that read a tile's lookup
     __device__ __forceinline__ void init(int info_readers) {
@@ -188,6 +188,7 @@ struct PfBars {
         mbar_init(drain, 1);
         mbar_init(l_full, 8);
         mbar_init(q_full, 8);
+        mbar_init(pages, 1);
         mbar_init_fence();
     }
 };
@@ -352,6 +353,31 @@ __device__ __forceinline__ void pf_q_staged(const PfBars &bar, int lane) {
     fence_proxy_async_smem();
     warp_arrive(bar.q_full, lane);
     asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// warp 14: whether every page that rows of the CTA's sequence read is there.  If one is not, all of the sequence's rows are zeros, those
+// too that do not see it: every CTA looks at all of them (a pool of pages of 32 tokens: 4 bytes for the 8 KB that a head of 128 reads).
+__device__ __forceinline__ void pf_check_pages(const PfArgs &a, const PfTile &w, const PfBars &bar, unsigned int *err, volatile int *lost) {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    if (!w.bad) {
+        int64_t lo, hi, x0, y0, x1, y1;
+        a.r.of(w.b, lo, hi);
+        row_range(w.first, w.len, a.causal, a.window, x0, y0);
+        row_range(w.first + min(hi - lo, a.max_q) - 1, w.len, a.causal, a.window, x1, y1);
+        const int32_t *table = a.c.table + (int64_t)w.b * a.c.max_pages;
+        const int64_t end = (max(y0, y1) + a.c.T - 1) >> a.c.tshift;
+#pragma unroll 4
+        for (int64_t p = (x0 >> a.c.tshift) + lane; p < end; p += 32) {
+            const int page = table[p];
+            bad = bad || page < 0 || page >= a.c.n_pages;
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) {
+        kv_error(err, KV_ERR_PAGE);
+        *lost = 1;
+    }
+    warp_arrive(bar.pages, lane);
 }
 
 // warp 12: pages and scales of the tiles, 32 blocks at a time, one a lane
@@ -663,6 +689,7 @@ __device__ __forceinline__ void pf_tile_weights_f32(uint32_t ts, float rs, const
     if (threadIdx.x == 0) {                                                                                                   \
         *abort_flag = 0;                                                                                                      \
         abort_flag[1] = w.slot;                                                                                               \
+        abort_flag[2] = 0;                                                                                                    \
         const_cast<PfBars &>(bar).init(INFO_READERS);                                                                         \
     }                                                                                                                         \
     if (warp == 13) tmem_alloc(tmem_holder, 512);                                                                             \
@@ -730,6 +757,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             // products and arrivals in flight end before the TMEM and the barriers go
             mma_commit_warp(bar.drain);
             mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
+        } else if (warp == 14) {
+            pf_check_pages(a, w, bar, err, abort_flag + 2);
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -798,11 +827,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             }
             // ---------------------------------------------------------------- the rows' outputs
             if (nj > 0 && ok) ok = warp_wait(bar.o_done + t, (nj - 1) & 1, err, abort_flag);
+            warp_wait(bar.pages, 0, err, abort_flag);
             tc_fence_after();
             float l, l1;
             f2_unpack(l2, l, l1);
             l += l1;
             const int piece = abort_flag[1];
+            const bool lost = abort_flag[2] != 0;              // zeros leave, with a sum of weights below zero for the join
+            if (lost) l = piece >= 0 ? -1.0f : 0.0f;
             const float gl = info[(nj + kPfInfo - 1) % kPfInfo].g, inv = piece >= 0 ? gl : l == 0.0f ? 0.0f : gl / l;
             float *pd = a.part + ((int64_t)piece * C::ROWS + r) * (D + 4);
             if (piece >= 0 && r < w.nrow) *reinterpret_cast<float2 *>(pd + D) = make_float2(m, l);
@@ -819,7 +851,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                     for (int k = 0; k < 32; k += 4) {
                         float y[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) y[z] = nj > 0 && l != 0.0f ? __uint_as_float(x[k + z]) * inv : 0.0f;
+                        for (int z = 0; z < 4; ++z) y[z] = nj > 0 && l != 0.0f && !lost ? __uint_as_float(x[k + z]) * inv : 0.0f;
                         if (piece >= 0) store4(pd + 32 * e + k, y);
                         else store4(dst + 32 * e + k, y);
                     }
@@ -882,6 +914,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
             // products and arrivals in flight end before the TMEM and the barriers go
             mma_commit_warp(bar.drain);
             mbar_wait(bar.drain, 0, err, KV_ERR_WAIT, nullptr);
+        } else if (warp == 14) {
+            pf_check_pages(a, w, bar, err, abort_flag + 2);
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -970,8 +1004,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
         if (a2 == ((nj - 1) & 1)) s_rs[r] = g;
         warp_arrive(bar.l_full, lane);
         warp_wait(bar.l_full, 0, err, abort_flag);
+        warp_wait(bar.pages, 0, err, abort_flag);
         l = s_m[((nj + 1) & 3) * 128 + r] + s_m[(nj & 3) * 128 + r];
         const int piece = abort_flag[1];
+        const bool lost = abort_flag[2] != 0;                  // zeros leave, with a sum of weights below zero for the join
+        if (lost) l = piece >= 0 ? -1.0f : 0.0f;
         const float inv = piece >= 0 ? s_rs[r] : l == 0.0f ? 0.0f : s_rs[r] / l;
         if (r < w.nrow) {
             float *dst = static_cast<float *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh + a2 * (D / 2);
@@ -986,7 +1023,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
                 f2_unpack(acc[k / 2], y[0], y[1]);
                 f2_unpack(acc[k / 2 + 1], y[2], y[3]);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) y[z] *= inv;
+                for (int z = 0; z < 4; ++z) y[z] = lost ? 0.0f : y[z] * inv;
                 store4(dst + k, y);
             }
         }
@@ -1033,9 +1070,10 @@ __global__ void __launch_bounds__(256) kv_tiles_join_kernel(PfArgs a) {
         for (int e = 0; e < V; ++e) acc[e] += fp * y[e];
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const bool lost = __any_sync(0xffffffffu, ml.y < 0.0f);    // a page was not there
     T *dst = static_cast<T *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh + V * lane;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] *= inv;
+    for (int e = 0; e < V; ++e) acc[e] = lost ? 0.0f : acc[e] * inv;
     if constexpr (V == 4) {
         store4(dst, acc);
     } else {

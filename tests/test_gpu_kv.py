@@ -329,6 +329,43 @@ def test_many_sequences(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,new,heads", [([700, 90, 1500], [1, 1, 2], 4), ([70] * 90, [1] * 90, 8), ([20011, 300], [1, 1], 4),
+                                            ([4100, 37, 2500], [40, 37, 12], 8), ([700] * 45, [70] * 45, 8)],
+                         ids=["passes", "short", "joined", "cut", "whole"])
+def test_rows_of_a_bad_page_entry_are_zero(dtype, lens, new, heads):
+    import torch
+    s = Setup(lens, 2, 64, 32, seed=21)
+    q = torch.randn((sum(new), heads, 64), device="cuda").to(ttype(dtype))
+    q[0, 1, 3] = float("nan")                                # zeros for a row that would be NaN, too
+    at = np.concatenate([[0], np.cumsum(new)])
+    ws = kv.alloc_attention_workspace(s.cache, s.seqs, heads, len(q), max(new), max(lens), q.dtype)
+    good, out = torch.full_like(q, 9.0), torch.full_like(q, 9.0)
+    kv.mqkv_attention(s.cache, s.seqs, 1, q, good, i32(at), max(new), max(lens), ws)
+    status()
+    entries = s.table.clone()
+    # the last page (causal rows before it do not see it), one in the middle, the first one; of the first sequence and of others
+    for b, page, entry in ((0, (lens[0] - 1) // 32, -1), (len(lens) - 1, lens[-1] // 64, len(s.refs)), (len(lens) // 2, 0, 2 ** 31 - 1)):
+        s.table.copy_(entries)
+        s.table[b, page] = entry
+        out.fill_(9.0)
+        kv.mqkv_attention(s.cache, s.seqs, 1, q, out, i32(at), max(new), max(lens), ws)
+        status("page table")
+        assert (out[at[b]:at[b + 1]] == 0).all()
+        rest = torch.cat([torch.arange(0, at[b]), torch.arange(at[b + 1], at[-1])]).cuda()
+        assert torch.equal(out[rest].nan_to_num(7.0), good[rest].nan_to_num(7.0))
+    # an entry that no row's window reaches is not looked at
+    far = [b for b, n in enumerate(lens) if n - new[b] > 200]
+    if far:
+        s.table.copy_(entries)
+        kv.mqkv_attention(s.cache, s.seqs, 1, q, good, i32(at), max(new), max(lens), ws, window=100)
+        status()
+        s.table[far[0], 0] = -1
+        kv.mqkv_attention(s.cache, s.seqs, 1, q, out, i32(at), max(new), max(lens), ws, window=100)
+        status()
+        assert torch.equal(out.nan_to_num(7.0), good.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_long_and_peaked(dtype):
     # long enough to be split many ways; scores far apart, so that one token carries a row
     s = Setup([20011, 4099], 1, 128, 128, seed=7)

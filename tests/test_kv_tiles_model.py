@@ -116,6 +116,11 @@ def widen(r, me, wi, nj, slots):
         yield ("arrive", f"op_full{n % slots}")
 
 
+def check_pages(r, me):
+    r.write(me, "lost", 0)
+    yield ("arrive", "pages")
+
+
 class Issue:
     def __init__(self, r, slots):
         self.r, self.slots, self.n = r, slots, 0
@@ -189,20 +194,22 @@ def f32_softmax(r, me, w, nj, sums_wait):
     r.write(me, f"m{(nj + 1 - a2) & 3},{row}", f"sum{a2}")
     yield ("arrive", "l_full")
     yield ("wait", "l_full", 0)
+    yield ("wait", "pages", 0)
+    r.read(me, "lost", 0)
     for g in range(2):
         r.read(me, f"m{(nj + 1 - g) & 3},{row}", f"sum{g}")
 
 
 def f32_actors(r, nj, sums_wait):
     slots = 4
-    a = {"lookup": lookup(r, "lookup", nj), "mma": f32_mma(r, nj, slots), "tc": tensor_core(r)}
+    a = {"lookup": lookup(r, "lookup", nj), "mma": f32_mma(r, nj, slots), "tc": tensor_core(r), "check": check_pages(r, "check")}
     a.update({f"widen{i}": widen(r, f"widen{i}", i, nj, slots) for i in range(4)})
     a.update({f"soft{w}": f32_softmax(r, f"soft{w}", w, nj, sums_wait) for w in range(8)})
     return a
 
 
 def f32_bars():
-    b = {"q_full": 8, "drain": 1, "l_full": 8}
+    b = {"q_full": 8, "drain": 1, "l_full": 8, "pages": 1}
     b.update({f"op_full{i}": 2 for i in range(4)}, **{f"op_empty{i}": 1 for i in range(4)})
     b.update({f"info_full{i}": 1 for i in range(INFO)}, **{f"info_empty{i}": 8 for i in range(INFO)})
     for i in range(2):
@@ -259,18 +266,20 @@ def half_softmax(r, me, w, nj, nt, rescale):
     if nj:
         yield ("wait", f"o_done{t}", nj - 1)
         assert r.mem[f"O{t}"] == nj - 1
+    yield ("wait", "pages", 0)
+    r.read(me, "lost", 0)
 
 
 def half_actors(r, nj, nt, rescale):
     slots = 5
-    a = {"lookup": lookup(r, "lookup", nj), "mma": half_mma(r, nj, nt, slots), "tc": tensor_core(r)}
+    a = {"lookup": lookup(r, "lookup", nj), "mma": half_mma(r, nj, nt, slots), "tc": tensor_core(r), "check": check_pages(r, "check")}
     a.update({f"widen{i}": widen(r, f"widen{i}", i, nj, slots) for i in range(4)})
     a.update({f"soft{w}": half_softmax(r, f"soft{w}", w, nj, nt, rescale) for w in range(8)})
     return a
 
 
 def half_bars(nt):
-    b = {"q_full": 8, "drain": 1}
+    b = {"q_full": 8, "drain": 1, "pages": 1}
     b.update({f"op_full{i}": 2 for i in range(5)}, **{f"op_empty{i}": 1 for i in range(5)})
     b.update({f"info_full{i}": 1 for i in range(INFO)}, **{f"info_empty{i}": 4 * nt + 4 for i in range(INFO)})
     for i in range(2):
@@ -278,7 +287,7 @@ def half_bars(nt):
     return b
 
 
-NAMES = ["lookup", "mma", "tc"] + [f"widen{i}" for i in range(4)] + [f"soft{w}" for w in range(8)]
+NAMES = ["lookup", "mma", "tc", "check"] + [f"widen{i}" for i in range(4)] + [f"soft{w}" for w in range(8)]
 
 
 def schedules(seed):
