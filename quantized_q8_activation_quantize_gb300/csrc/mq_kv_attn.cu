@@ -54,6 +54,18 @@ struct AtShare {
     }
 };
 
+// sum += a b, rounded to nearest.  The tensor core cuts its f32 sums toward zero, always the same way, and a share has no longest length: with
+// the products added up there, f32 rows over 430 blocks of values of one sign were off by 6.9e-5 and over 1725 by 2.0e-4 (now 3.6e-7 and
+// 8.2e-7); two additions more per MMA cost 1 to 3% of the time.
+__device__ __forceinline__ void mma16816_add(float (&sum)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    float d[4];
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    f2_unpack(f2_add(f2_pack(sum[0], sum[1]), f2_pack(d[0], d[1])), sum[0], sum[1]);
+    f2_unpack(f2_add(f2_pack(sum[2], sum[3]), f2_pack(d[2], d[3])), sum[2], sum[3]);
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -68,12 +80,10 @@ template <typename T, int D, int MT>
 struct AtCfg {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int RT = TWO ? 8 : 16, R = RT * MT;      // rows of an MMA tile, of a pass
-    static constexpr int RING = MT == 1 || D == 64 ? 3 : 2;   // blocks in flight per warp
+    static constexpr int RING = 3;                            // blocks in flight per warp
     static constexpr int BLK = kKB * D, SLOT = 2 * BLK;       // bytes of one 32-token block of K or V
-    static constexpr bool QS = MT > 1 && D == 128;            // q fragments in shared memory: the registers hold 2 x 64 sums
     static constexpr int LD = D + 4;                          // floats of a row of sums
-    static constexpr int OFF_Q = kAtWarps * RING * SLOT;
-    static constexpr int OFF_BAR = OFF_Q + (QS ? kAtWarps * MT * (D / 16) * 512 : 0);
+    static constexpr int OFF_BAR = kAtWarps * RING * SLOT;
     static constexpr int OFF_PLAN = OFF_BAR + kAtWarps * RING * 8 + 64;
     static constexpr int SMEM = OFF_PLAN + 1008;              // then the plan
 };
@@ -264,8 +274,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
     uint32_t last = 0;                                        // the pass's last place
     int all_lo = 0, all_hi = 0;                               // what every row of the pass sees
     int v_lo[MT][RT], v_hi[MT][RT];
-    uint32_t qa[C::QS ? 1 : MT][KS][4];
-    uint32_t *qs = reinterpret_cast<uint32_t *>(sm + C::OFF_Q) + warp * MT * KS * 128 + lane * 4;
+    uint32_t qa[MT][KS][4];
     float rs[MT][RT], m[MT][RT], l[MT][RT];
     float o[MT][NT][4];
     float gmax = 0.0f;                                        // the largest V scale so far
@@ -342,16 +351,12 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                     }
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
-                        if (TWO || (z & 1) == e) {
-                            if constexpr (C::QS) qs[(t * KS + ks) * 128 + z] = w[z];
-                            else qa[t][ks][z] = w[z];
-                        }
+                        if (TWO || (z & 1) == e) qa[t][ks][z] = w[z];
                 }
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
         }
-        if constexpr (C::QS) __syncwarp();
         return left;
     };
     // the rows' sums leave: divided where the pass is whole, else as partial `which` of this worker.  Of a lost pass zeros leave, with a sum of
@@ -427,15 +432,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                     uint32_t x, y;
                     codes_f16(ww[z], x, y);
 #pragma unroll
-                    for (int k = 0; k < MT; ++k) {
-                        if constexpr (C::QS) {
-                            const uint4 f = *reinterpret_cast<const uint4 *>(qs + (k * KS + 4 * hh + z) * 128);
-                            const uint32_t ff[4] = {f.x, f.y, f.z, f.w};
-                            mma16816(s[k][t], ff, x, y);
-                        } else {
-                            mma16816(s[k][t], qa[k][4 * hh + z], x, y);
-                        }
-                    }
+                    for (int k = 0; k < MT; ++k) mma16816(s[k][t], qa[k][4 * hh + z], x, y);
                 }
             }
         }
@@ -561,15 +558,15 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 codes_f16(y0, q0, q1);
 #pragma unroll
                 for (int x = 0; x < MT; ++x) {
-                    mma16816(o[x][4 * k + 0], pa[x], p0, q0);
-                    mma16816(o[x][4 * k + 1], pa[x], p1, q1);
+                    mma16816_add(o[x][4 * k + 0], pa[x], p0, q0);
+                    mma16816_add(o[x][4 * k + 1], pa[x], p1, q1);
                 }
                 codes_f16(x1, p0, p1);
                 codes_f16(y1, q0, q1);
 #pragma unroll
                 for (int x = 0; x < MT; ++x) {
-                    mma16816(o[x][4 * k + 2], pa[x], p0, q0);
-                    mma16816(o[x][4 * k + 3], pa[x], p1, q1);
+                    mma16816_add(o[x][4 * k + 2], pa[x], p0, q0);
+                    mma16816_add(o[x][4 * k + 3], pa[x], p1, q1);
                 }
             }
         }
@@ -705,20 +702,21 @@ int kv_tensor_map(CUtensorMap *tm, const mqkv_cache &c, const mqkv_layout &lay) 
     return MQ_OK;
 }
 
-// MMA tiles per pass: two where the rows do not fit one, so that the codes are widened once for both.  (Two for up to 8 f32 or 16 16-bit
-// rows, half of them empty: 38 us for 29, and 39 for 29, for 7 rows on 48 sequences of 2048 tokens; one, the codes read twice, for 14 f32
-// rows on 4 sequences of 32768: 49 for 47, for 28 16-bit rows 54 for 54 there and 46 for 48 on the 48.)
-int pass_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
-int pass_rows(int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(dtype, rows); }
-// More than two such passes over the cache (32 f32 rows per KV head, 64 16-bit ones): the tcgen05 tiles of mq_kv_prefill.cu.  Passes / tiles in
+// MMA tiles per pass of 64-wide heads: two where the rows do not fit one, so that the codes are widened once for both (one: 34 us for 31 for 14
+// f32 rows, 55 for 47 for 28, on 4 sequences of 32768 tokens, 40 for 38 and 67 for 57 on 48 of 100 to 16384; 28 16-bit rows 38 for 38, 56 for 47).
+// Of 128-wide heads one: the sums of two leave no registers for the additions that keep them exact (spills: 55 us for 51 for 14 f32 rows, 85 for 86
+// for 28, on 4 of 32768; 66 for 54 for 28 16-bit rows).
+int pass_tiles(int D, int dtype, int64_t rows) { return D == 64 && rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
+int pass_rows(int D, int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(D, dtype, rows); }
+// Beyond 32 f32 rows per KV head, 64 16-bit ones: the tcgen05 tiles of mq_kv_prefill.cu.  Passes / tiles in
 // us, D = 128, 4 KV heads: f32, 28 rows 73/72, 42 rows 102/73, 56 rows 129/74 on 4 sequences of 32768 tokens; 63/64, 84/66, 105/67 on 48 of
 // 2048; 194/259, 283/259, 368/260 on 48 of 100 to 16384 (the passes share work evenly, row tiles are as long as their sequence).
 // bf16, 56 rows 81/60, 72/55, 206/205; 84 rows 110/60, 95/57, 300/205.
-bool use_tiles(int dtype, int64_t rows) { return rows > 2 * pass_rows(dtype, rows); }
+bool use_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 32 : 64); }
 // CTAs: as many as are resident, or as there are units for their warps at most
 int64_t share_ctas(int32_t n_seqs, int32_t H, int D, int dtype, int64_t rows, int64_t max_kv) {
-    const int64_t passes = (rows + pass_rows(dtype, rows) - 1) / pass_rows(dtype, rows), blocks = (max_kv + kKB - 1) / kKB;
-    const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = at_ctas_per_sm(D, pass_tiles(dtype, rows)) * sm_count();
+    const int64_t passes = (rows + pass_rows(D, dtype, rows) - 1) / pass_rows(D, dtype, rows), blocks = (max_kv + kKB - 1) / kKB;
+    const int64_t units = passes * H * (blocks > 0 ? blocks : 1) * n_seqs, most = at_ctas_per_sm(D, pass_tiles(D, dtype, rows)) * sm_count();
     return (units + kAtWarps - 1) / kAtWarps < most ? (units + kAtWarps - 1) / kAtWarps : most;
 }
 size_t plan_bytes(int32_t n_seqs, size_t workers) { return ((((size_t)n_seqs + 4) & ~size_t(3)) * 8 + workers * sizeof(AtJoin) + 255) & ~size_t(255); }
@@ -746,7 +744,7 @@ int attn_t(const CUtensorMap &tm, const AtArgs &a, int64_t ctas, unsigned int *e
 }
 template <typename T>
 int attn_d(const CUtensorMap &tm, const AtArgs &a, int tiles, int64_t ctas, unsigned int *err, cudaStream_t s) {
-    if (a.c.D == 128) return tiles == 1 ? attn_t<T, 128, 1>(tm, a, ctas, err, s) : attn_t<T, 128, 2>(tm, a, ctas, err, s);
+    if (a.c.D == 128) return attn_t<T, 128, 1>(tm, a, ctas, err, s);
     return tiles == 1 ? attn_t<T, 64, 1>(tm, a, ctas, err, s) : attn_t<T, 64, 2>(tm, a, ctas, err, s);
 }
 
@@ -757,14 +755,14 @@ size_t kv_attention_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int32_t 
     const int64_t rows = max_q * (n_q_heads / H);
     if (use_tiles(dtype, rows)) return kv_prefill_ws(n_seqs, H, D, dtype, n_q_heads / H, n_tokens, max_q);
     const size_t workers = (size_t)share_ctas(n_seqs, H, D, dtype, rows, max_kv) * kAtWarps;
-    return plan_bytes(n_seqs, workers) + workers * 2 * pass_rows(dtype, rows) * (D + 4) * 4;
+    return plan_bytes(n_seqs, workers) + workers * 2 * pass_rows(D, dtype, rows) * (D + 4) * 4;
 }
 
 int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int layer, const KvView &c, const KvRows &r,
                         const KvAttn &p, void *ws, unsigned int *err, cudaStream_t s) {
     const int64_t rows = p.max_q * p.group;
     if (use_tiles(p.dtype, rows)) return kv_launch_prefill(c, r, p, ws, err, s);
-    const int64_t passes = (rows + pass_rows(p.dtype, rows) - 1) / pass_rows(p.dtype, rows);
+    const int64_t passes = (rows + pass_rows(c.D, p.dtype, rows) - 1) / pass_rows(c.D, p.dtype, rows);
     if ((double)c.n_seqs * c.H * passes * ((double)c.max_pages * (c.T / kKB) + kAtExtra + 1) >= 4294967296.0)
         return set_error(MQ_ERR_SHAPE, "mqkv_attention: %d sequences of up to %d pages have too many blocks for one call", c.n_seqs, c.max_pages);
     CUtensorMap tm;
@@ -780,7 +778,7 @@ int kv_launch_attention(const mqkv_cache &cache, const mqkv_layout &lay, int lay
     a.prefix = static_cast<uint32_t *>(ws);
     a.join = reinterpret_cast<AtJoin *>(a.prefix + 2 * ((c.n_seqs + 4) & ~3));
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes(c.n_seqs, (size_t)a.workers));
-    const int tiles = pass_tiles(p.dtype, rows);
+    const int tiles = pass_tiles(c.D, p.dtype, rows);
     return p.dtype == MQKV_F32   ? attn_d<float>(tm, a, tiles, ctas, err, s)
            : p.dtype == MQKV_F16 ? attn_d<__half>(tm, a, tiles, ctas, err, s)
                                  : attn_d<__nv_bfloat16>(tm, a, tiles, ctas, err, s);

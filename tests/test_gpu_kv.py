@@ -373,6 +373,24 @@ def test_long_and_peaked(dtype):
     check_attention(s, [2, 1], 7, dtype, qscale=6.0)
 
 
+@pytest.mark.parametrize("heads,dim", [(4, 128), (12, 128), (4, 64), (12, 64)])
+def test_sums_over_long_shares(heads, dim):
+    # four workers for 65536 tokens of values of one sign: sums that are cut instead of rounded drift (they did by 4e-5 of the result).
+    # Of the terms of attention_tolerance the sums' is replaced: 1024 additions a worker (two per 32 tokens), each within 2^-24 of the sum and of
+    # either sign, so four times their root in all; the rest as there.
+    n = 65536
+    s = Setup([n], 1, dim, 256, layers=1, seed=dim)
+    s.m.codes[:, :, 1] = np.abs(s.m.codes[:, :, 1])
+    s.pool.copy_(dev(s.m.bytes(fill=0xFF)))
+    q = np.random.default_rng(1).standard_normal((1, heads, dim)) * 0.1
+    got, q = run_attention(s, q, [1], "f32", layer=0, max_kv=1)
+    k, v = (s.m.values(0, half, s.rows[0], np.arange(n)) for half in range(2))
+    out, mass, vmax = U.attention(q, k, v, n)
+    tol = (2 * (2 * (2.0 ** -21 + 2.0 ** -22) * mass + 2.0 ** -21) + 4 * 1024 ** 0.5 * 2.0 ** -24) * vmax
+    off = np.abs(got - out).max(-1)
+    assert (off <= tol).all(), (off / vmax, tol / vmax)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("new", [1, 200])
 def test_scales_of_many_sizes(dtype, new):
