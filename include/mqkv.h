@@ -113,10 +113,13 @@ MQ_API int mqkv_read(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t lay
  *   scale      factor of the scores (1 / sqrt(head_dim) as a rule); finite
  *   workspace  mqkv_attention_workspace_bytes(...) bytes, 256-byte aligned, not shared by calls in flight
  *
- * A row that sees nothing (its sequence has no cached token, or every position is masked) is zero.  A row whose q holds a NaN or an infinity is NaN (if it sees
- * anything).  f32 rows keep f32 accuracy: q and the softmax weights enter the tensor cores as two f16
- * parts each.  16-bit rows enter as one f16 part (q of bf16 exactly, scaled by a power of two per row)
- * and the softmax weights are rounded to f16.
+ * A row that sees nothing (its sequence has no cached token, or every position is masked) is zero.  A row
+ * whose q holds a NaN or an infinity is NaN (if it sees anything).  f32 rows keep f32 accuracy: q and the
+ * softmax weights enter the tensor cores as two f16 parts each.  16-bit rows enter as one f16 part (q of
+ * bf16 exactly, scaled by a power of two per row) and the softmax weights are rounded to f16.  The weights
+ * are held relative to the row's largest product of weight and V scale, so a row's error is a fraction of
+ * the values that it weighs itself: large values of other tokens, masked or of no weight, take nothing
+ * from it, except within a block of 32 tokens, which share their scale.
  */
 MQ_API int mqkv_attention(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int32_t dtype, const void *q,
                           int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,

@@ -5,7 +5,7 @@
 // codes k, v and block scales dk, dv (one per 32 tokens), s_ij = c dk_j (q_i . k_j), c = scale log2(e); the softmax runs
 // in one pass over blocks of 32 tokens with a running maximum m and sum l per row, and
 //     o_i = sum_j 2^(s_ij - m_i) dv_j v_j / l_i.
-// dv enters the weights, p' = 2^(s - m) dv / g with g the largest dv so far, so both products run on exact integers.
+// dv enters the weights (mq_kv_attn.cuh: relative to the row's own largest product of weight and dv), so both products run on exact integers.
 //
 // Tensor cores.  Decode needs 2 D flops per cached byte and row; the CUDA cores cannot give that at HBM rate for the 7
 // rows of a 28:4 head layout (47 TFMA/s of 37), the warp-level m16n8k16 can with 16 rows of which 7 are used (37% of its
@@ -40,7 +40,7 @@ struct AtArgs {
     float c_log2, sign;         // |scale| * log2(e), the sign of scale (it goes into q: score factors are not negative)
     uint32_t *prefix;           // [n_seqs + 1][2]: places and units before each sequence
     struct AtJoin *join;        // [workers]
-    float *part;                // [worker][2][R rows][D + 4]: o, m, l
+    float *part;                // [worker][2][R rows][D + 4]: the mean, m, l
 };
 
 // equal shares of the places: the first rem of them have one more
@@ -275,9 +275,8 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
     int all_lo = 0, all_hi = 0;                               // what every row of the pass sees
     int v_lo[MT][RT], v_hi[MT][RT];
     uint32_t qa[MT][KS][4];
-    float rs[MT][RT], m[MT][RT], l[MT][RT];
+    float rs[MT][RT], m[MT][RT], ra[MT][RT], l[MT][RT];       // q's scale, the references m and A, the sum of weights
     float o[MT][NT][4];
-    float gmax = 0.0f;                                        // the largest V scale so far
     bool lost = false;                                        // a block of this share's part of the pass has no page
 
     // the row pass of unit u: its rows' q and ranges; how many units of it are left
@@ -299,7 +298,6 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         row_range(q.first + r0 / G, q.len, a.causal, a.window, x0, y0);
         row_range(q.first + (r0 + nrow - 1) / G, q.len, a.causal, a.window, x1, y1);
         all_lo = (int)x1, all_hi = y0 > x0 ? (int)y0 : 0;
-        gmax = 0.0f;
         lost = false;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
             for (int e = 0; e < RT; ++e) {
                 const int rr = t * C::RT + g + 8 * e;
                 v_lo[t][e] = v_hi[t][e] = 0;
-                m[t][e] = -INFINITY, l[t][e] = 0.0f;
+                m[t][e] = ra[t][e] = -INFINITY, l[t][e] = 0.0f;
                 float x[D / 4];
                 if (rr < nrow) {
                     const int i = (r0 + rr) / G;
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         }
         return left;
     };
-    // the rows' sums leave: divided where the pass is whole, else as partial `which` of this worker.  Of a lost pass zeros leave, with a sum of
+    // the rows' means leave: into the output where the pass is whole, else as partial `which` of this worker.  Of a lost pass zeros leave, with a sum of
     // weights below zero for the join
     auto end = [&](bool whole, int which) {
         if (lost) {
@@ -377,7 +375,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 if (lost) l[t][e] = whole ? 0.0f : -1.0f;
                 const int rr = t * C::RT + g + 8 * e;
                 if (rr < nrow) {
-                    const float f = whole ? (l[t][e] == 0.0f ? 0.0f : gmax / l[t][e]) : gmax;
+                    const float f = l[t][e] == 0.0f ? 0.0f : 1.0f / l[t][e] * ref_factor(ra[t][e], m[t][e]);
                     const int i = (r0 + rr) / G;
                     float *part = a.part + ((int64_t)(2 * worker + which) * C::R + rr) * (D + 4);
                     T *dst = static_cast<T *>(a.out) + (tok + i) * a.ot + (int64_t)(h * G + (r0 + rr - i * G)) * a.oh + cc * (D / 4);
@@ -440,14 +438,8 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
         lost = lost || dkb == -INFINITY;
         const int t0 = (int)(blk + (k - k0)) * kKB;
         const bool inner = t0 >= all_lo && t0 <= all_hi - kKB;
-        // the V scale reference moves to twice a scale that exceeds it
-        float gold = 1.0f;
-        if (dvb > gmax) {
-            gold = gmax / (2.0f * dvb);
-            gmax = 2.0f * dvb;
-        }
-        const float pv = gmax > 0.0f ? dvb / gmax : 0.0f;
-        bool grow = gold != 1.0f;
+        const float lgv = log2_approx(dvb);
+        bool grow = false;
         float mx[MT][RT], kk[MT][RT];
 #pragma unroll
         for (int x = 0; x < MT; ++x)
@@ -474,7 +466,7 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 y = max3(y, s[x][1][f + 1], s[x][2][f]);
                 y = max3(y, s[x][2][f + 1], s[x][3][f]);
                 mx[x][e] = fmaxf(y, s[x][3][f + 1]) * kk[x][e];
-                grow = grow || mx[x][e] > m[x][e] + kTau || (m[x][e] == -INFINITY && mx[x][e] > m[x][e]);
+                grow = grow || mx[x][e] > m[x][e] + kTau || mx[x][e] + lgv > ra[x][e] + kTau || (m[x][e] == -INFINITY && mx[x][e] > m[x][e]);
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -484,11 +476,13 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 for (int e = 0; e < RT; ++e) {
                     float y = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], 1));
                     y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                    float ref = fmaxf(ra[x][e], y + lgv);
                     y = fmaxf(y, m[x][e]);
-                    f[e] = y == -INFINITY ? 1.0f : exp2_approx(m[x][e] - y);
+                    ref = fmaxf(ref, y - kRefSpan);
+                    l[x][e] *= y == -INFINITY ? 1.0f : exp2_approx(m[x][e] - y);
                     m[x][e] = y;
-                    l[x][e] *= f[e];
-                    f[e] *= gold;
+                    f[e] = ref == -INFINITY ? 1.0f : exp2_approx(ra[x][e] - ref);
+                    ra[x][e] = ref;
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
@@ -497,11 +491,12 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                 }
             }
         }
-        const uint64_t pv2 = f2_pack(pv, pv);
 #pragma unroll
         for (int x = 0; x < MT; ++x)
 #pragma unroll
             for (int e = 0; e < RT; ++e) {
+                const float pv = v_factor(dvb, ref_factor(m[x][e], ra[x][e]));
+                const uint64_t pv2 = f2_pack(pv, pv);
                 const float off = kLazyShift - (m[x][e] == -INFINITY ? 0.0f : m[x][e]);
                 const uint64_t off2 = f2_pack(off, off), k2 = f2_pack(kk[x][e], kk[x][e]);
                 uint64_t sum = f2_pack(0.0f, 0.0f);
@@ -620,9 +615,9 @@ __global__ void __launch_bounds__(FEW ? 128 : 256) kv_attn_join_kernel(AtArgs a,
             float mn = fmaxf(ml.x, mm);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            const float mb = mn == -INFINITY ? 0.0f : mn, old = exp2_approx(mm - mb), f = exp2_approx(ml.x - mb);
+            const float mb = mn == -INFINITY ? 0.0f : mn, old = exp2_approx(mm - mb), f = ml.y * exp2_approx(ml.x - mb);   // of its mean
             mm = mn;
-            float x = ml.y * f;
+            float x = f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             ll = ll * old + x;

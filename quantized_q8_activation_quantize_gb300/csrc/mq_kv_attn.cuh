@@ -12,13 +12,16 @@ int kv_launch_prefill(const KvView &c, const KvRows &r, const KvAttn &p, void *w
 size_t kv_prefill_ws(int32_t n_seqs, int32_t H, int32_t D, int dtype, int group, int64_t n_tokens, int64_t max_q);
 
 constexpr float kLog2e = 1.44269504088896341f;
-// the softmax weights enter the tensor cores as exp2(s - m + kPShift) times the V scale over the running largest V
-// scale, at most 2^kPShift: the shift keeps small weights out of f16's subnormals
-constexpr float kPShift = 12.0f;
-
-// With a reference maximum that moves only when the maximum grows by more than kTau (the factor cancels in o / l), weights reach
-// 2^(kLazyShift + kTau) < 65504.
-constexpr float kTau = 8.0f, kLazyShift = 6.0f;
+// Every row has two references, both powers of two: m for its scores, of which l = sum 2^(s - m), and A for its weights times V scales, of which
+// o = sum 2^(s - A) dv v.  What enters the tensor cores, 2^(s - m + shift) times dv 2^(m - A), is at most 2^shift however the V scales of the
+// row's tokens differ, and what the row does not see or hardly weighs takes no bits from the rest.  (With the largest V scale of all blocks met, seen by
+// the row or not, as one reference for all rows, a block of 2^16 times the others' scale without weight put f32 rows of a long share 2e-4 off, one
+// of 2^28 0.4.)  The result is o 2^(A - m) / l.
+// kPShift keeps small weights out of f16's subnormals; where the references move only when the maximum grows by more than kTau, weights
+// reach 2^(kLazyShift + kTau) < 65504.
+constexpr float kPShift = 12.0f, kTau = 8.0f, kLazyShift = 6.0f;
+// A stays above m - kRefSpan, so that 2^(m - A) is finite (a row that has met scales of zero only)
+constexpr float kRefSpan = 120.0f;
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -31,6 +34,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^(x - y) of references, 0 where there is none yet (y is minus infinity)
+__device__ __forceinline__ float ref_factor(float x, float y) { return y == -INFINITY ? 0.0f : exp2_approx(x - y); }
+// what a weight relative to m is multiplied by to become one relative to A, for a V scale (finite: a weight of zero stays zero)
+__device__ __forceinline__ float v_factor(float dv, float m_over_a) { return fminf(dv * m_over_a, 3.402823466e38f); }
 
 // four codes of a word as two f16 pairs, exactly: byte b becomes the f16 1024 + b, minus 1152
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {

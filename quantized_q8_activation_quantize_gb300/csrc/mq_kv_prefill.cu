@@ -11,9 +11,8 @@
 //
 // 16-bit rows (kv_tiles_kernel): two row tiles (256 rows) share every K / V tile, warps 0-3 and 4-7 their softmax; the
 // tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), the softmax of one tile under the products of the other.  A row's
-// reference maximum moves only when the maximum grows by more than kTau (a factor that cancels in o / l), and the V
-// scale reference g only when a scale exceeds it, to twice that, so O in TMEM is rescaled a few times per row
-// instead of at every tile.  (V as f16(code * f16(256 dv / g)) took the factor off the weights and 3% off the time, but its two
+// references move only when the maximum grows by more than kTau (a factor that cancels in o / l), so O in TMEM is rescaled a
+// few times per row instead of at every tile.  (V as f16(code * f16(256 dv / g)) took the factor off the weights and 3% off the time, but its two
 // roundings showed in f16 outputs.)
 //
 // Many rows of long sequences are 636 jobs of 40 to 64 tiles in the largest case measured: 436 us, 1056 TFLOP/s (of 1864 that cuBLAS
@@ -54,7 +53,7 @@ struct PfArgs {
     int64_t qt, qh, ot, oh;
     int32_t group, causal, tiles;
     int32_t cut, pieces;        // the last `cut` row tiles (in the grid's order) are done in `pieces` pieces
-    float *part;                // [piece][row][D + 4]: o, m, l
+    float *part;                // [piece][row][D + 4]: the mean, m, l
     int64_t max_q, window;
     float c_log2;               // |scale| * log2(e)
     float sign;                 // of scale: folded into q, so that the score factors are not negative
@@ -62,10 +61,8 @@ struct PfArgs {
 
 // what the lookup leaves for a tile of four blocks
 struct PfInfo {
-    float dk[4], pv[4];         // K scales; V scales over g
+    float dk[4], dv[4], lv[4];  // K scales; V scales and their binary logarithms
     int page[4];                // -1: no such block (codes of zero)
-    float gf, g;                // factor of what was summed before, g from here on
-    float pad[2];
 };
 
 template <int D, bool TWO>
@@ -76,8 +73,8 @@ struct PfCfg {
     static constexpr int QT = 128 * D * 2;                     // one part of one row tile
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_OP = OFF_Q + PARTS * TILES * QT;
-    static constexpr int OFF_RS = OFF_OP + SLOTS * OPT;     // row scales [ROWS]; f32 rows: then factors and maxima [4][128]
-    static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 2 * 512 * 4 : 0);
+    static constexpr int OFF_RS = OFF_OP + SLOTS * OPT;     // row scales [ROWS]; f32 rows: then factors, references A [4][128] each, maxima and sums [2][2][128]
+    static constexpr int OFF_INFO = OFF_RS + ROWS * 4 + (TWO ? 3 * 512 * 4 : 0);
     static constexpr int OFF_BAR = OFF_INFO + kPfInfo * (int)sizeof(PfInfo);
     static constexpr int NBAR = 2 * kPfSlots + 2 * kPfInfo + 5 * 2 + 4;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -381,7 +378,6 @@ __device__ __forceinline__ void pf_check_pages(const PfArgs &a, const PfTile &w,
 }
 
 // warp 12: pages and scales of the tiles, 32 blocks at a time, one a lane
-template <bool TWO>
 __device__ __forceinline__ void pf_lookup(const PfArgs &a, const PfTile &w, PfInfo *info, const PfBars &bar, unsigned int *err, volatile int *abort) {
     const int lane = threadIdx.x & 31;
     int pg = -1, pg_n = -1;
@@ -402,30 +398,19 @@ __device__ __forceinline__ void pf_lookup(const PfArgs &a, const PfTile &w, PfIn
         }
     };
     fetch(w.b_lo + lane);
-    float g = 0.0f;
     for (int j = 0; j < w.nj; ++j) {
         if ((j & 7) == 0) {
             pg = pg_n, dk = dk_n, dv = dv_n;
             fetch(w.b_lo + 4 * (int64_t)(j + 8) + lane);
         }
-        const int l0 = 4 * (j & 7), e = lane - l0;
-        float dmax = dv;
-        dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 1));
-        dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 2));
-        dmax = __shfl_sync(0xffffffffu, dmax, l0);
-        const float to = TWO ? dmax : 2.0f * dmax;
-        float gf = 1.0f;
-        if (dmax > g) {
-            gf = g / to;
-            g = to;
-        }
+        const int e = lane - 4 * (j & 7);
         if (j >= kPfInfo && !warp_wait(bar.info_empty + j % kPfInfo, (j / kPfInfo - 1) & 1, err, abort)) break;
         PfInfo &o = info[j % kPfInfo];
         if (e >= 0 && e < 4) {
             o.dk[e] = dk;
-            o.pv[e] = g > 0.0f ? dv / g : 0.0f;
+            o.dv[e] = dv;
+            o.lv[e] = log2_approx(dv);
             o.page[e] = pg;
-            if (e == 0) o.gf = gf, o.g = g;
         }
         __threadfence_block();
         warp_arrive(bar.info_full + j % kPfInfo, lane);
@@ -596,13 +581,17 @@ __device__ __forceinline__ float pf_load_max32(uint32_t taddr) {
 }
 // The softmax reads a tile's scores twice from TMEM: once for the maximum, once, 64 or 32 at a time, for the weights.  Holding all 128
 // in registers left the compiler none to overlap the elements' chains with (3600 clocks a tile for f32 rows).
-__device__ __forceinline__ float pf_tile_max(uint32_t ts, const float (&kb)[4]) {
+// ... and `top`: the largest of a block's maximum times its V scale (binary logarithms)
+__device__ __forceinline__ float pf_tile_max(uint32_t ts, const float (&kb)[4], const float4 &lv, float &top) {
     float mx = -INFINITY;
+    top = -INFINITY;
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-        const float m0 = pf_load_max32(ts + 64 * e), m1 = pf_load_max32(ts + 64 * e + 32);
+        float m0 = pf_load_max32(ts + 64 * e), m1 = pf_load_max32(ts + 64 * e + 32);
         tmem_ld_wait();
-        mx = max3(mx, m0 * (e ? kb[2] : kb[0]), m1 * (e ? kb[3] : kb[1]));
+        m0 *= e ? kb[2] : kb[0], m1 *= e ? kb[3] : kb[1];
+        mx = max3(mx, m0, m1);
+        top = max3(top, m0 + (e ? lv.z : lv.x), m1 + (e ? lv.w : lv.y));
     }
     return mx;
 }
@@ -647,23 +636,26 @@ __device__ __forceinline__ void pf_tile_weights(uint32_t ts, const float (&kb)[4
 }
 // f32 rows, a block of 32 tokens at a time: its 16 columns of leading parts and 16 of the rest in the scores' place
 __device__ __forceinline__ float pf_score_factor(float rs, float dk) { return fmaxf(rs * dk, 0x1p-120f); }
-__device__ __forceinline__ float pf_tile_max_f32(uint32_t ts, float rs, const PfInfo &o) {
+__device__ __forceinline__ float pf_tile_max_f32(uint32_t ts, float rs, const PfInfo &o, float &top) {
     float mx = -INFINITY;
+    top = -INFINITY;
 #pragma unroll 1
     for (int e = 0; e < 4; e += 2) {
         uint32_t s[2][32];
         pf_load_scores(ts + 32 * e, s);
-        mx = max3(mx, pf_max32(s[0]) * pf_score_factor(rs, o.dk[e]), pf_max32(s[1]) * pf_score_factor(rs, o.dk[e + 1]));
+        const float m0 = pf_max32(s[0]) * pf_score_factor(rs, o.dk[e]), m1 = pf_max32(s[1]) * pf_score_factor(rs, o.dk[e + 1]);
+        mx = max3(mx, m0, m1);
+        top = max3(top, m0 + o.lv[e], m1 + o.lv[e + 1]);
     }
     return mx;
 }
-__device__ __forceinline__ void pf_tile_weights_f32(uint32_t ts, float rs, const PfInfo &o, float off, uint64_t &l2) {
+__device__ __forceinline__ void pf_tile_weights_f32(uint32_t ts, float rs, const PfInfo &o, float off, float m_over_a, uint64_t &l2) {
     const uint64_t off2 = f2_pack(off, off);
 #pragma unroll 1
     for (int e = 0; e < 4; ++e) {
         uint32_t s[32], w[16], v[16];
         tmem_ld32(ts + 32 * e, s);
-        const float kb = pf_score_factor(rs, o.dk[e]), pv = o.pv[e];
+        const float kb = pf_score_factor(rs, o.dk[e]), pv = v_factor(o.dv[e], m_over_a);
         tmem_ld_wait();
         pf_weights<true>(s, kb, off2, pv, l2, w, v);
         tmem_st16(ts + 32 * e, w);
@@ -705,7 +697,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 12) {
-            pf_lookup<false>(a, w, info, bar, err, abort_flag);
+            pf_lookup(a, w, info, bar, err, abort_flag);
         } else if (warp == 13) {
             const PfMma<D, false> mma(sm);
             const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
@@ -779,14 +771,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             }
             const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
             const float rs = s_rs[r];
-            float m = -INFINITY;
+            float m = -INFINITY, ra = -INFINITY;                // the references m and A
             uint64_t l2 = f2_pack(0.0f, 0.0f);
             bool ok = true;
             for (int j = 0; j < nj; ++j) {
                 if (!(ok = warp_wait(bar.info_full + j % kPfInfo, (j / kPfInfo) & 1, err, abort_flag))) break;      // under the products
                 const PfInfo &o = info[j % kPfInfo];
-                const float4 dk = *reinterpret_cast<const float4 *>(o.dk), pv = *reinterpret_cast<const float4 *>(o.pv);
-                const float gf = o.gf, pb[4] = {pv.x, pv.y, pv.z, pv.w};
+                const float4 dk = *reinterpret_cast<const float4 *>(o.dk), dv = *reinterpret_cast<const float4 *>(o.dv),
+                             lv = *reinterpret_cast<const float4 *>(o.lv);
                 // at least 2^-120, so that a masked score stays minus infinity under a scale of zero
                 const float kb[4] = {fmaxf(rs * dk.x, 0x1p-120f), fmaxf(rs * dk.y, 0x1p-120f), fmaxf(rs * dk.z, 0x1p-120f), fmaxf(rs * dk.w, 0x1p-120f)};
                 warp_arrive(bar.info_empty + j % kPfInfo, lane);
@@ -794,17 +786,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                 tc_fence_after();
                 const int t0 = j * kPfN;
                 if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) pf_mask(ts, v0 - t0, v1 - t0);
-                const float mx = pf_tile_max(ts, kb);
-                const bool grow = mx > m + kTau || (m == -INFINITY && mx > m);
-                if (__any_sync(0xffffffffu, grow || gf != 1.0f)) {
-                    const float mn = grow ? mx : m;
-                    const float f = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
-                    m = mn;
+                float top;
+                const float mx = pf_tile_max(ts, kb, lv, top);
+                if (__any_sync(0xffffffffu, mx > m + kTau || top > ra + kTau || (m == -INFINITY && mx > m))) {
+                    const float mn = fmaxf(m, mx), ref = max3(ra, top, mn - kRefSpan);
+                    const float f = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), fo = ref == -INFINITY ? 1.0f : exp2_approx(ra - ref);
+                    m = mn, ra = ref;
                     l2 = f2_mul(l2, f2_pack(f, f));
-                    if (j > 0) {
+                    if (j > 0 && __any_sync(0xffffffffu, fo != 1.0f)) {
                         if (!(ok = warp_wait(bar.o_done + t, (j - 1) & 1, err, abort_flag))) break;
                         tc_fence_after();
-                        const uint64_t ff = f2_pack(f * gf, f * gf);
+                        const uint64_t ff = f2_pack(fo, fo);
 #pragma unroll 1
                         for (int e = 0; e < D / 16; ++e) {
                             uint32_t x[16];
@@ -820,6 +812,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
                         }
                     }
                 }
+                const float over = ref_factor(m, ra);
+                const float pb[4] = {v_factor(dv.x, over), v_factor(dv.y, over), v_factor(dv.z, over), v_factor(dv.w, over)};
                 pf_tile_weights(ts, kb, pb, kLazyShift - (m == -INFINITY ? 0.0f : m), l2);
                 tmem_st_wait();
                 tc_fence_before();
@@ -835,7 +829,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
             const int piece = abort_flag[1];
             const bool lost = abort_flag[2] != 0;              // zeros leave, with a sum of weights below zero for the join
             if (lost) l = piece >= 0 ? -1.0f : 0.0f;
-            const float gl = info[(nj + kPfInfo - 1) % kPfInfo].g, inv = piece >= 0 ? gl : l == 0.0f ? 0.0f : gl / l;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l * ref_factor(ra, m);
             float *pd = a.part + ((int64_t)piece * C::ROWS + r) * (D + 4);
             if (piece >= 0 && r < w.nrow) *reinterpret_cast<float2 *>(pd + D) = make_float2(m, l);
             T *dst = static_cast<T *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh;
@@ -872,11 +866,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_kernel(PfArgs a, unsig
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, unsigned int *err) {
     PF_PROLOGUE(float, D, 4 + 4);
-    float *s_f = s_rs + 128, *s_m = s_f + 512;                 // [4 tiles][128] factors of what was summed before, maxima
+    float *s_f = s_rs + 128, *s_a = s_f + 512;                 // [4 tiles][128] factors of what was summed before, references A
+    float *s_l = s_a + 512;                                    // [warpgroup][2][128] maxima and sums of weights
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 12) {
-            pf_lookup<true>(a, w, info, bar, err, abort_flag);
+            pf_lookup(a, w, info, bar, err, abort_flag);
         } else if (warp == 13) {
             const PfMma<D, true> mma(sm);
             const uint32_t s0 = tmem + C::COL_S, o0 = tmem + C::COL_O;
@@ -935,7 +930,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
         }
         const int i_lo = (int)max(w.all_lo - w.base, (int64_t)INT_MIN), i_hi = (int)max(w.all_hi - w.base, (int64_t)INT_MIN);
         const float rs = s_rs[r];
-        float m = -INFINITY, g = 0.0f;                         // the maximum and V scale reference of this warpgroup's last tile
+        float m = -INFINITY;                                   // the maximum of this warpgroup's tiles: its sum's reference
         uint64_t l2 = f2_pack(0.0f, 0.0f);
         uint64_t acc[D / 4];
 #pragma unroll
@@ -967,54 +962,47 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_tiles_f32_kernel(PfArgs a, u
             if (!warp_wait2(bar.info_full + j % kPfInfo, bar.s_full + at, (j / kPfInfo) & 1, (j >> 1) & 1, err, abort_flag)) break;
             tc_fence_after();
             const PfInfo &o = info[j % kPfInfo];
-            const float gf = o.gf;
-            g = o.g;
             const int t0 = j * kPfN;
             if (!(t0 >= i_lo && t0 + kPfN <= i_hi)) pf_mask(ts + at * 128, v0 - t0, v1 - t0);
-            const float mx = pf_tile_max_f32(ts + at * 128, rs, o);
-            float before = -INFINITY;                          // the maximum after tile j - 1, from the other warpgroup
+            float top;
+            const float mx = pf_tile_max_f32(ts + at * 128, rs, o, top);
+            float before = -INFINITY;                          // A after tile j - 1, from the other warpgroup
             if (j > 0) {
                 if (!warp_wait(bar.m_full + (at ^ 1), ((j - 1) >> 1) & 1, err, abort_flag)) break;
-                before = s_m[((j - 1) & 3) * 128 + r];
+                before = s_a[((j - 1) & 3) * 128 + r];
             }
-            const float mn = fmaxf(before, mx), mb = mn == -INFINITY ? 0.0f : mn;
+            const float mn = fmaxf(m, mx), mb = mn == -INFINITY ? 0.0f : mn, ref = max3(before, top, mn - kRefSpan);
             // their places: the other warpgroup has published tile j - 1's, so it has summed tile j - 4 and is done with these
-            s_m[(j & 3) * 128 + r] = mn;
-            s_f[(j & 3) * 128 + r] = exp2_approx(before - mb) * gf;
+            s_a[(j & 3) * 128 + r] = ref;
+            s_f[(j & 3) * 128 + r] = ref_factor(before, ref);
             warp_arrive(bar.m_full + at, lane);
             const float f = exp2_approx(m - mb);
             m = mn;
             l2 = f2_mul(l2, f2_pack(f, f));
-            pf_tile_weights_f32(ts + at * 128, rs, o, kPShift - mb, l2);
+            pf_tile_weights_f32(ts + at * 128, rs, o, kPShift - mb, ref_factor(mn, ref), l2);
             warp_arrive(bar.info_empty + j % kPfInfo, lane);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(bar.p_full + at, lane);
         }
-        // both warpgroups' sums of weights, relative to the last tile's maximum; V's reference is the last tile's
+        // the sum of both warpgroups' weights, relative to the larger maximum; the last tile's A is what the outputs are relative to
         float l, l1;
         f2_unpack(l2, l, l1);
-        l += l1;
-        float last_m = -INFINITY;
-        if (nj > 0) {
-            last_m = s_m[((nj - 1) & 3) * 128 + r];
-            l *= exp2_approx(m - (last_m == -INFINITY ? 0.0f : last_m));
-        }
-        s_m[((nj + 1 - a2) & 3) * 128 + r] = l;                 // two of the places that tiles nj - 1 and nj - 2 did not use
-        if (a2 == ((nj - 1) & 1)) s_rs[r] = g;
+        s_l[a2 * 256 + r] = m, s_l[a2 * 256 + 128 + r] = l + l1;
         warp_arrive(bar.l_full, lane);
         warp_wait(bar.l_full, 0, err, abort_flag);
         warp_wait(bar.pages, 0, err, abort_flag);
-        l = s_m[((nj + 1) & 3) * 128 + r] + s_m[(nj & 3) * 128 + r];
+        const float m0 = s_l[r], m1 = s_l[256 + r], mm = fmaxf(m0, m1), mb = mm == -INFINITY ? 0.0f : mm;
+        l = s_l[128 + r] * exp2_approx(m0 - mb) + s_l[384 + r] * exp2_approx(m1 - mb);
         const int piece = abort_flag[1];
         const bool lost = abort_flag[2] != 0;                  // zeros leave, with a sum of weights below zero for the join
         if (lost) l = piece >= 0 ? -1.0f : 0.0f;
-        const float inv = piece >= 0 ? s_rs[r] : l == 0.0f ? 0.0f : s_rs[r] / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l * (nj > 0 ? ref_factor(s_a[((nj - 1) & 3) * 128 + r], mm) : 0.0f);
         if (r < w.nrow) {
             float *dst = static_cast<float *>(a.out) + (w.lo + w.token(r, a.group)) * a.ot + (int64_t)w.head(r, a.group) * a.oh + a2 * (D / 2);
             if (piece >= 0) {
                 float *pd = a.part + ((int64_t)piece * C::ROWS + r) * (D + 4);
-                if (a2 == 0) *reinterpret_cast<float2 *>(pd + D) = make_float2(last_m, l);
+                if (a2 == 0) *reinterpret_cast<float2 *>(pd + D) = make_float2(mm, l);
                 dst = pd + a2 * (D / 2);
             }
 #pragma unroll
@@ -1054,8 +1042,8 @@ __global__ void __launch_bounds__(256) kv_tiles_join_kernel(PfArgs a) {
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float f = exp2_approx(ml.x - (m == -INFINITY ? 0.0f : m));
-    float l = ml.y * f, acc[V];
+    const float f = ml.y * exp2_approx(ml.x - (m == -INFINITY ? 0.0f : m));   // of its mean
+    float l = f, acc[V];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll

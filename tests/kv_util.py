@@ -123,6 +123,31 @@ def attention_tolerance(out, mass, vmax, length, dtype):
     return (2 * weight + sums)[..., None] * vmax[..., None] + u * np.abs(out) + (2.0 ** -25 if dtype == "f16" else 1e-38)
 
 
+def attention_own(q, k, v, d, length, dtype, causal=True, window=0):
+    """attention() with a tolerance per element that knows only what the row sees and weighs: d [length, H] are the V scales.
+
+    A weight's error (attention_tolerance; 2^-20 for exp2 and the factors between the two references) counts with its own token's
+    w |v|, and in the sum of weights with the result; the sums with sum w |v|.  A weight times V scale below f16's subnormals is lost: 2^-30 of
+    the row's largest, times at most 127, for each token."""
+    n, Hq, D = q.shape
+    G, scale = Hq // k.shape[1], 1 / np.sqrt(D)
+    u = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    out, tol = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    for i in range(n):
+        p = length - n + i
+        hi, lo = min(p + 1, length) if causal else length, max(0, p - window + 1) if window else 0
+        for x in range(Hq if hi > lo else 0):
+            kk, vv, dd = k[lo:hi, x // G], v[lo:hi, x // G], d[lo:hi, x // G]
+            s = kk @ q[i, x] * scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            e = 2 * (2.0 ** -21 + 2.0 ** -22) * (np.abs(kk) @ np.abs(q[i, x])) * scale + 2.0 ** -20 + (0 if dtype == "f32" else 2.0 ** -11)
+            out[i, x] = w @ vv
+            tol[i, x] = ((w * e) @ np.abs(vv) + np.abs(out[i, x]) * (w @ e) + (length / 16 + 8) * 2.0 ** -23 * (w @ np.abs(vv)) +
+                         length * 2.0 ** -30 * 127 * (w * dd).max() + u * np.abs(out[i, x]) + (2.0 ** -25 if dtype == "f16" else 1e-38))
+    return out, tol
+
+
 # ----------------------------------------------------------------------------- pages ---
 
 class Pages:

@@ -407,6 +407,37 @@ def test_scales_of_many_sizes(dtype, new):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,max_kv", [(5, None), (5, 1), (130, None), (130, 1)])
+@pytest.mark.parametrize("kind,dim", [("later", 64), ("later", 128), ("window", 128), ("unweighted", 64), ("unweighted", 128)])
+def test_large_values_take_no_bits_from_rows_that_do_not_weigh_them(dtype, new, max_kv, kind, dim):
+    # a block of V up to 2^90 times the others': after a row, before its window, or where its weight vanishes; held to the row's own values.
+    # (max_kv = 1: few workers with long shares, row tiles in one piece)
+    n = 579
+    r = np.random.default_rng(31)
+    q = 1 + 0.2 * r.standard_normal((new, 4, dim))
+    for ratio in (2.0 ** 12, 2.0 ** 28, 2.0 ** 90):
+        s = Setup([n], 2, dim, 64, seed=32)
+        # (positions 576 .. 578, 0 .. 95, 320 .. 351)
+        for blk in {"later": [18], "window": [0, 1, 2], "unweighted": [10]}[kind]:
+            p, sb = s.rows[0][blk // 2], blk % 2
+            s.m.scales[p, :, 1, :, sb] *= np.float32(ratio)
+            if kind == "unweighted":
+                s.m.codes[p, :, 0, :, 32 * sb:32 * sb + 32] = -127
+                s.m.scales[p, :, 0, :, sb] = 0.2
+        s.pool.copy_(dev(s.m.bytes()))
+        kw = {"window": 200} if kind == "window" else {}
+        got, qq = run_attention(s, q, [new], dtype, max_kv=max_kv, **kw)
+        pos = np.arange(n)
+        k, v = (s.m.values(1, half, s.rows[0], pos) for half in range(2))
+        d = s.m.scales[s.rows[0][pos // 64], 1, 1, :, pos % 64 // 32].astype(np.float64)
+        out, tol = U.attention_own(qq, k, v, d, n, dtype, **kw)
+        fits = np.abs(out) < (6e4 if dtype == "f16" else 1e37)
+        assert fits[:new - 3].all()
+        off = np.abs(got - out)
+        assert (off <= tol)[fits].all(), (ratio, float((off / tol)[fits].max()), np.argwhere((off > tol) & fits)[:3])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_queries_of_extreme_sizes_and_not_numbers(dtype):
     s = Setup([100, 90, 0], 2, 128, 32, seed=13)
     new = [3, 2, 1]

@@ -189,15 +189,15 @@ def f32_softmax(r, me, w, nj, sums_wait):
         yield ("arrive", f"info_empty{j % INFO}")
         r.mem[f"S{at}"][row] = j
         yield ("arrive", f"p_full{at}")
-    if nj:
-        r.read(me, f"m{(nj - 1) & 3},{row}", nj - 1)
-    r.write(me, f"m{(nj + 1 - a2) & 3},{row}", f"sum{a2}")
+    r.write(me, f"l{a2},{row}", f"sum{a2}")
     yield ("arrive", "l_full")
     yield ("wait", "l_full", 0)
     yield ("wait", "pages", 0)
     r.read(me, "lost", 0)
     for g in range(2):
-        r.read(me, f"m{(nj + 1 - g) & 3},{row}", f"sum{g}")
+        r.read(me, f"l{g},{row}", f"sum{g}")
+    if nj:
+        r.read(me, f"m{(nj - 1) & 3},{row}", nj - 1)
 
 
 def f32_actors(r, nj, sums_wait):
