@@ -216,6 +216,9 @@ int mqkv_read(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int
                           k_head_stride, v, v_token_stride, v_head_stride, start, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// a window that reaches past every position (they lie within 2^31 of 0), with room for the sums that the kernels make of it
+static constexpr int64_t kFarWindow = (int64_t)1 << 40;
+
 static int check_attn_sizes(const char *fn, const mqkv_cache *cache, int32_t n_q_heads, int64_t max_q, int64_t max_kv) {
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || n_q_heads > 65536)
         return set_error(MQ_ERR_SHAPE, "%s: n_q_heads=%d must be a multiple of n_kv_heads=%d of at most 65536", fn, n_q_heads, cache->n_kv_heads);
@@ -248,6 +251,7 @@ int mqkv_attention(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer
     KV_TRY(check_attn_sizes(fn, cache, n_q_heads, max_q, max_kv));
     if (window < 0) return set_error(MQ_ERR_ARG, "%s: negative window=%lld", fn, (long long)window);
     if (!std::isfinite(scale)) return set_error(MQ_ERR_ARG, "%s: scale=%g not finite", fn, (double)scale);
+    window = window < kFarWindow ? window : kFarWindow;
     if (n_tokens == 0) return MQ_OK;
     if (max_q == 0) return set_error(MQ_ERR_ARG, "%s: max_q=0 for %lld tokens", fn, (long long)n_tokens);
     if (cu == nullptr && max_q < n_tokens / seqs->n_seqs)

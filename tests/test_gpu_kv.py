@@ -316,6 +316,16 @@ def test_last_row_tiles_cut(dtype, lens, new, heads, kv_heads):
     check_attention(s, new, heads, dtype, layer=0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 40 + 1, 2 ** 63 - 1])
+def test_windows_past_every_position(dtype, causal, window):
+    # rows at positions far below the first token among them: without causality they see all of it
+    for lens, new in (([2, 70], [7, 3]), ([10, 200], [200, 40])):
+        s = Setup(lens, 2, 64, 32, seed=23)
+        check_attention(s, new, 4, dtype, causal=causal, window=window)
+
+
 @pytest.mark.parametrize("n,dtype", [(257, "f32"), (1500, "f16")])
 def test_many_sequences(n, dtype):
     # more than the plan's shared memory holds, and more than one round of its scan; most of them short, some empty
