@@ -61,24 +61,21 @@ __device__ __forceinline__ float amax_of(const Raw4<T> (&r)[IT], bool &finite) {
 
 constexpr int kAppendThreads = 256, kAppendVecs = 2, kAppendWarps = 8 / kAppendVecs;    // vectors per CTA, warps per vector
 
-constexpr int kAppendShift = 7;
-
 // One CTA per (group of `blocks` consecutive blocks of 32 slots, two of the 2 H vectors (half, head)); four warps per vector, 8 slots
 // each, all of a lane's values in registers between the maximum and the codes, the next block's asked for before this one's
 // are worked on.  Unit u of the grid's x belongs to the last sequence b with U(b) <= u, U(b) = begin(b) / (32 blocks) + 2 b: a
 // sequence of n tokens touches at most that many groups more, so the units of the sequences never overlap and need no prefix sum.
-// Moves 5 (f32) or 3 bytes a value.  Four blocks per CTA: 40k bf16 tokens of 8 heads of 128 take 48 us with one, 39 with four (6.3 TB/s),
-// 10k 12.5 and 11; up to 4k tokens and for single ones it makes no difference (6 us).  The conversions' issue slots and HBM bound the
-// large ones alike, the launch the small ones.
+// Moves 5 (f32) or 3 bytes a value: 32k tokens of 8 heads of 128 in 63 us from f32 (5.2 TB/s), 46 from f16 (4.3), 58 from bf16 (3.4; its
+// kernel spills 88 bytes at three CTAs per SM).
 template <typename TIN, int D>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(TIN) == 4 ? 2 : 3) kv_append_kernel(KvView c, KvRows rows, const TIN *k, int64_t kt, int64_t kh,
+__global__ void __launch_bounds__(kAppendThreads, sizeof(TIN) == 4 ? 2 : 3) kv_append_kernel(KvView c, KvRows rows, int shift, const TIN *k, int64_t kt, int64_t kh,
                                                                       const TIN *v, int64_t vt, int64_t vh, unsigned int *err) {
     constexpr int LPR = D / 4, RPW = 32 / LPR, IT = kKB / kAppendWarps / RPW;   // lanes per row, rows per warp and step, steps
     __shared__ float s_amax[2][8];
     grid_dep_launch();
     grid_dep_wait();
     const int64_t u = blockIdx.x;
-    constexpr int shift = kAppendShift, blocks = 1 << (shift - 5);
+    const int blocks = 1 << (shift - 5);
     int b;
     int64_t u0;
     if (rows.cu == nullptr) {
@@ -270,12 +267,14 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows 
 template <typename T>
 int append_t(const KvView &c, const KvRows &r, const void *k, int64_t kt, int64_t kh, const void *v, int64_t vt, int64_t vh,
              unsigned int *err, cudaStream_t s) {
-    constexpr int shift = kAppendShift;
+    // Four blocks to a CTA where that leaves a few CTAs per SM, one where it would not.  One / four, from f32 and from bf16: 512 tokens of 4 heads
+    // of 128 3.4 / 7.2, 3.4 / 7.9 us, 3314 of them 5.8 / 8.6, 4.4 / 9.1; 10k of 8 heads 30 / 25, 23 / 24, 32k 86 / 63, 64 / 58 (two: 70, 59).
     const int gy = (2 * c.H + kAppendVecs - 1) / kAppendVecs;
+    const int shift = (r.n_tokens >> 7) * gy >= 4 * sm_count() ? 7 : 5;
     const int64_t units = r.cu == nullptr ? c.n_seqs * ((r.each >> shift) + 2) : (r.n_tokens >> shift) + 2 * (int64_t)c.n_seqs;
     const dim3 grid((unsigned)units, gy);
     auto fn = c.D == 128 ? kv_append_kernel<T, 128> : kv_append_kernel<T, 64>;
-    return cuda_error(launch_pdl(fn, grid, dim3(kAppendThreads), 0, s, c, r, static_cast<const T *>(k), kt, kh,
+    return cuda_error(launch_pdl(fn, grid, dim3(kAppendThreads), 0, s, c, r, shift, static_cast<const T *>(k), kt, kh,
                                  static_cast<const T *>(v), vt, vh, err),
                       "mqkv_append launch");
 }

@@ -102,6 +102,26 @@ def test_append_matches_the_model(dtype, dim, page, heads):
     s.check_pool()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("before", [0, 300])
+def test_append_of_many_tokens(dtype, before):
+    import torch
+    # enough for four blocks to a CTA; sequences that begin and end anywhere in them, one of none, one inside a block
+    new, had = [1700, 1, 0, 33, 128, 129, 2900, 500], [5, 40, 7, 31, 0, 96, 64, 1001]
+    s = Setup([a + n for a, n in zip(had, new)], 16, 64, 64, layers=1, seed=41)
+    x = np.random.default_rng(42).standard_normal((2, before + sum(new), 16, 64)).astype(np.float32)
+    xt = torch.from_numpy(x).to(ttype(dtype)).cuda()
+    kv.mqkv_append(s.cache, s.seqs, 0, xt[0], xt[1], i32(before + np.concatenate([[0], np.cumsum(new)])))
+    status()
+    x, at = xt.float().cpu().numpy(), before
+    for b, n in enumerate(new):
+        for half in range(2):
+            if n:
+                s.m.append(0, half, s.rows[b], s.lens[b], x[half, at:at + n])
+        at += n
+    s.check_pool()
+
+
 def test_append_token_by_token_and_strided():
     import torch
     # one projection's output [tokens, q heads + 2 * kv heads, dim]: k and v are strided views; no cu, one token each
