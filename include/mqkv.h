@@ -136,7 +136,8 @@ MQ_API size_t mqkv_attention_workspace_bytes(const mqkv_cache *cache, const mqkv
  *
  * refs and page_table are the allocator's whole state: a page with refs 0 is free.  Pages are taken lowest
  * first, in the order of the sequences (or forks).  These calls run on one stream in order; they must not run
- * beside one another on the same cache.  workspace: mqkv_pages_workspace_bytes(...), 256-byte aligned.
+ * beside one another on the same cache.  They alone give pages back: a length that is lowered by hand past its last
+ * page's beginning leaves pages that belong to no sequence.  workspace: mqkv_pages_workspace_bytes(...), 256-byte aligned.
  */
 MQ_API size_t mqkv_pages_workspace_bytes(const mqkv_cache *cache, const mqkv_seqs *seqs);
 
@@ -156,7 +157,8 @@ MQ_API int mqkv_fork(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32
                      int32_t n, void *workspace, size_t workspace_bytes, mq_stream_t stream);
 
 /* Moves live pages to the front of the pool: with L live pages, the k-th live page at or past L moves to the k-th
- * free page below L, and refs and table follow. */
+ * free page below L, and refs and table follow.  seqs has to be all sequences of the cache: the rows of others would
+ * go on naming the places that their pages have left. */
 MQ_API int mqkv_compact(const mqkv_cache *cache, const mqkv_seqs *seqs, void *workspace, size_t workspace_bytes,
                         mq_stream_t stream);
 

@@ -23,8 +23,8 @@ namespace mq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
-// what the beginning and end of a row pass cost, in blocks: 0 took 56.5 us for 48 ragged sequences (47 for 24 windows of 20 rows), 2 50.4
-// (43.7), 4 50.2 (45.6), 8 49.0 (45.9)
+// what the beginning and end of a row pass cost, in blocks: 0 took 53.0 us for 48 ragged sequences (41.3 and, of f32 rows, 51.0 for 24 windows of
+// 20 rows), 2 47.2 (39.4, 50.1), 3 46.7 (38.3, 49.8), 4 46.5 (38.4, 50.0), 8 46.7 (39.0, 51.7)
 constexpr uint32_t kAtExtra = 3;
 constexpr int kAtSmemSeqs = 256;                // sequences whose plan fits the CTA's shared memory beside two CTAs' rings
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// CTAs per SM: as many as the registers leave room for without spills (three with them took 76 us where two take 49)
+// CTAs per SM: as many as the registers leave room for without spills (of 128-wide heads three with them took 76 us where two took 49)
 constexpr int at_ctas_per_sm(int D, int MT) { return D == 64 && MT == 1 ? 3 : 2; }
 
 // MT: 16-row MMA tiles that share the codes
@@ -176,8 +176,8 @@ __device__ __forceinline__ int at_find(const uint2 *prefix, int n_seqs, uint32_t
 // own ring of K / V blocks; loads run ahead over the ends of row passes and no warp waits for another.  Where a row pass ends, or the share does, the sums leave: divided where the pass lies
 // in the share whole, else as a partial for the join kernel.  (Shares of whole CTAs, their warps joined in shared memory at the end of
 // each pass, left fewer partials but made every end of a pass cost 5 us: 77 us against 49 for a ragged batch of 48 sequences.)
-// With its join: 48 sequences of 100 to 16384 tokens, 28 f32 query heads on 4 of 128: 49 us, 198 MB at 4.1 TB/s (fixed latencies of the
-// 8 warps per SM bound it: issue 39%, DRAM 61%); two bf16 ones of 200k and 262k: 88 us, 5.4 TB/s.
+// With its join: 48 sequences of 100 to 16384 tokens, 28 f32 query heads on 4 of 128: 46 us, 198 MB at 4.3 TB/s (fixed latencies of the
+// 8 warps per SM bound it: issue 42%, DRAM 61%); two bf16 ones of 200k and 262k: 87 us, 5.5 TB/s.
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_kernel(const __grid_constant__ CUtensorMap tm, AtArgs a, unsigned int *err) {
     using C = AtCfg<T, D, MT>;
@@ -527,6 +527,8 @@ __global__ void __launch_bounds__(kAtThreads, at_ctas_per_sm(D, MT)) kv_attn_ker
                     y = unpack_f16(pa[x][2]);
                     pa[x][3] = pack_f16(sx[2 * t2 + 1][0] - y.x, sx[2 * t2 + 1][1] - y.y);
                 } else {
+                    // the weights of 16-bit rows in one f16 part, for half the MMAs: f16 rows of drafted tokens are 2.6e-4 off, with the
+                    // rounding of the outputs alone 2.1e-4; bf16 ones show nothing (1.7e-3)
                     pa[x][1] = pack_f16(sx[2 * t2][2], sx[2 * t2][3]);
                     pa[x][3] = pack_f16(sx[2 * t2 + 1][2], sx[2 * t2 + 1][3]);
                 }
@@ -703,10 +705,19 @@ int kv_tensor_map(CUtensorMap *tm, const mqkv_cache &c, const mqkv_layout &lay) 
 // for 28, on 4 of 32768; 66 for 54 for 28 16-bit rows).
 int pass_tiles(int D, int dtype, int64_t rows) { return D == 64 && rows > (dtype == MQKV_F32 ? 8 : 16) ? 2 : 1; }
 int pass_rows(int D, int dtype, int64_t rows) { return (dtype == MQKV_F32 ? 8 : 16) * pass_tiles(D, dtype, rows); }
-// Beyond 32 f32 rows per KV head, 64 16-bit ones: the tcgen05 tiles of mq_kv_prefill.cu.  Passes / tiles in
-// us, D = 128, 4 KV heads: f32, 28 rows 73/72, 42 rows 102/73, 56 rows 129/74 on 4 sequences of 32768 tokens; 63/64, 84/66, 105/67 on 48 of
-// 2048; 194/259, 283/259, 368/260 on 48 of 100 to 16384 (the passes share work evenly, row tiles are as long as their sequence).
-// bf16, 56 rows 81/60, 72/55, 206/205; 84 rows 110/60, 95/57, 300/205.
+// Beyond 32 f32 rows per KV head, 64 16-bit ones: the tcgen05 tiles of mq_kv_prefill.cu.  The passes share work evenly whatever the lengths, row
+// tiles are as long as their sequence, and the host does not know the lengths: on both sides of the rule one kind of batch would be up to 45% faster
+// with the other kernel.  Passes / tiles in us, 4 KV heads:
+//                          4 x 32768 tokens          48 x 2048             48 x 100 to 16384         1 x 4096
+//   D 128, f32,  28 rows         85 / 70               71 / 64                105 / 251               16 / 20
+//                42             123 / 72               97 / 66                149 / 252               16 / 20
+//          bf16, 42              73 / 61               62 / 55                 87 / 210               19 / 17
+//                56              91 / 61               77 / 56                111 / 211               18 / 18
+//                84             129 / 62              106 / 58                158 / 212               19 / 18
+//   D 64,  f32,  32              47 / 57               40 / 51                 57 / 195               17 / 17
+//                48              64 / 57               53 / 53                 77 / 195               18 / 17
+//          bf16, 48              56 / 50               50 / 47                 70 / 167               21 / 16
+//                64              57 / 50               51 / 47                 72 / 167               22 / 16
 bool use_tiles(int dtype, int64_t rows) { return rows > (dtype == MQKV_F32 ? 32 : 64); }
 // CTAs: as many as are resident, or as there are units for their warps at most
 int64_t share_ctas(int32_t n_seqs, int32_t H, int D, int dtype, int64_t rows, int64_t max_kv) {

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(KvPages p, const 
         __syncwarp();
     }
     __syncthreads();
-    // the copies; blocks[] turns from a length into the used blocks of the tail page
+    // the copies; list[] turns from a page into the used blocks of the tail page
     for (int base = 0; base < n; base += kPlanThreads) {
         const int i = base + threadIdx.x;
         int len = 0, at = -1, s = 0, d = 0;

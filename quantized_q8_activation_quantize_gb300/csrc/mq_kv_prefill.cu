@@ -5,8 +5,8 @@
 // S = Q K^T accumulates exact products; a tile's score is S times (row scale) (K scale of the token's block).
 //
 // Both kernels: 16 warps; 8-11 widen codes (global memory -> registers -> f16 operand tiles with the 128-byte swizzle, a
-// ring of five), 12 looks up pages and scales ahead of everyone, 13 issues the MMAs; a softmax thread owns a row and
-// holds its 128 scores in registers.  P replaces S in TMEM (f16, the A operand comes from TMEM); V is the MN-major B
+// ring of five, of four for f32 rows), 12 looks up pages and scales ahead of everyone, 13 issues the MMAs, 14 looks over the
+// sequence's table entries; a softmax thread owns a row and reads its scores from TMEM, 32 or 64 at a time.  P replaces S in TMEM (f16, the A operand comes from TMEM); V is the MN-major B
 // operand, so nothing is transposed.
 //
 // 16-bit rows (kv_tiles_kernel): two row tiles (256 rows) share every K / V tile, warps 0-3 and 4-7 their softmax; the
@@ -15,16 +15,21 @@
 // few times per row instead of at every tile.  (V as f16(code * f16(256 dv / g)) took the factor off the weights and 3% off the time, but its two
 // roundings showed in f16 outputs.)
 //
-// Many rows of long sequences are 636 jobs of 40 to 64 tiles in the largest case measured: 436 us, 1056 TFLOP/s (of 1864 that cuBLAS
-// reaches; tensor pipe 50%, issue 49%); what is left is the chain MMA - commit - softmax - arrival - MMA of each tile and a CTA's beginning
+// Their weights are one f16 part: the worst of 320 f16 rows over 2048, 8192 and 16384 tokens of either sign is 4.0e-4 to 4.3e-4 off, with the
+// rounding of the outputs alone 2.5e-4; of one sign 2.7e-4 for 2.7e-4.  O stays in TMEM over a row tile's whole length, where the tensor
+// core cuts its sums toward zero (f32 rows, below, do not let it): of one sign 3.2e-4 at 32768 tokens and 4.8e-4 at 65536, for 2.5e-4 and
+// 1.8e-4.  bf16 outputs show neither (2.0e-3 with and without).
+//
+// Many rows of long sequences are 636 jobs of 40 to 64 tiles in the largest case measured: 434 us, 1060 TFLOP/s (of 1864 that cuBLAS
+// reaches; issue 49%); what is left is the chain MMA - commit - softmax - arrival - MMA of each tile and a CTA's beginning
 // and end (8 tiles' time).
 //
 // f32 rows (kv_tiles_f32_kernel): q and the weights enter as two f16 parts each (twice the MMAs), V as its exact codes.
 // The tensor core's f32 accumulation truncates; over a long row of tiles that grew to 4e-6 of the result (3314 tokens), so
 // each tile's P V goes to a fresh accumulator and is added to the row's sum in registers, rounding to nearest, under the
 // products of the next tiles: one row tile per CTA, S and O double-buffered, warps 0-3 and 4-7 the softmax of the tiles in turn.  A prompt
-// of 3314 tokens, 28 query heads on 4 of 128: 179 us (157 GFLOP in two parts: 880 TFLOP/s); the tiles' chain bounds it
-// (tensor pipe 40%, issue 49%).
+// of 3314 tokens, 28 query heads on 4 of 128: 183 us (157 GFLOP in two parts: 858 TFLOP/s); the tiles' chain bounds it
+// (tensor pipe 36%, issue 48%).
 //
 // q is staged by the softmax warps while the others look up and widen the first tiles: with all warps and before everything else, a CTA's
 // beginning took 5 us more (the prompt 187 us, the 16-bit chunks 478).
