@@ -167,7 +167,7 @@ MQ_API int mqkv_compact(const mqkv_cache *cache, const mqkv_seqs *seqs, void *wo
 MQ_API int mqkv_copy_pages(const mqkv_cache *cache, const int32_t *src, const int32_t *dst, int32_t n,
                            mq_stream_t stream);
 
-/* Synchronizes stream, then reads and clears this device's cache error word: MQ_OK, MQ_ERR_DEVICE_TIMEOUT (a
+/* Synchronizes stream, then reads and clears this device's cache error word (one for all streams): MQ_OK, MQ_ERR_DEVICE_TIMEOUT (a
  * bounded wait ran out: the outputs of that call are undefined) or MQKV_ERR_STATE (text in mq_last_error()). */
 MQ_API int mqkv_device_status(mq_stream_t stream);
 

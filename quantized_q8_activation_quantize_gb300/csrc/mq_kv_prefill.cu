@@ -6,8 +6,8 @@
 //
 // Both kernels: 16 warps; 8-11 widen codes (global memory -> registers -> f16 operand tiles with the 128-byte swizzle, a
 // ring of five, of four for f32 rows), 12 looks up pages and scales ahead of everyone, 13 issues the MMAs, 14 looks over the
-// sequence's table entries; a softmax thread owns a row and reads its scores from TMEM, 32 or 64 at a time.  P replaces S in TMEM (f16, the A operand comes from TMEM); V is the MN-major B
-// operand, so nothing is transposed.
+// sequence's table entries; a softmax thread owns a row and reads its scores from TMEM, 32 or 64 at a time.  P replaces S in
+// TMEM (f16, the A operand comes from TMEM); V is the MN-major B operand, so nothing is transposed.
 //
 // 16-bit rows (kv_tiles_kernel): two row tiles (256 rows) share every K / V tile, warps 0-3 and 4-7 their softmax; the
 // tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), the softmax of one tile under the products of the other.  A row's

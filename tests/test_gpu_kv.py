@@ -346,6 +346,24 @@ def test_windows_past_every_position(dtype, causal, window):
         check_attention(s, new, 4, dtype, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,new,heads", [(128, 6, 14), (64, 20, 16), (128, 70, 4)])
+def test_tiles_of_many_sequences_again_and_again(dtype, dim, new, heads):
+    import torch
+    # every SM with several row tiles after one another, whole ones and pieces: all waits end, and the results are the same each time
+    s = Setup([1800 + 16 * b for b in range(48)], 2, dim, 64, layers=1, seed=dim)
+    q = torch.randn((48 * new, heads, dim), device="cuda").to(ttype(dtype))
+    ws = kv.alloc_attention_workspace(s.cache, s.seqs, heads, len(q), new, max(s.lens), q.dtype)
+    out, first = torch.empty_like(q), None
+    for i in range(40):
+        out.fill_(9.0)
+        kv.mqkv_attention(s.cache, s.seqs, 0, q, out, None, new, max(s.lens), ws)
+        first = out.clone() if i == 0 else first
+        assert torch.equal(out, first), i
+    status()
+    assert torch.isfinite(first).all()
+
+
 @pytest.mark.parametrize("n,dtype", [(257, "f32"), (1500, "f16")])
 def test_many_sequences(n, dtype):
     # more than the plan's shared memory holds, and more than one round of its scan; most of them short, some empty
