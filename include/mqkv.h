@@ -33,7 +33,7 @@
 #ifndef MQKV_H
 #define MQKV_H
 
-#include "mq.h"
+#include "mqd.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -89,6 +89,24 @@ MQ_API int mqkv_page_layout(int32_t n_layers, int32_t n_kv_heads, int32_t head_d
 MQ_API int mqkv_append(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int32_t dtype, const void *k,
                        int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
                        int64_t v_head_stride, const int32_t *cu, int64_t n_tokens, mq_stream_t stream);
+
+/*
+ * mqkv_append_rope -- mqkv_append of keys turned by their positions (mqd_rope), with the queries turned beside it: what a layer does
+ * between its projections and mqkv_attention, in one launch.
+ *
+ *   plan       rot_dim at most head_dim
+ *   pos        int32 [n_tokens], the position of every row; NULL: the cached ones (kv_len[b] - n_b + i)
+ *   q, q_out   [n_tokens][n_q_heads][head_dim] of dtype, as x and out of mqd_rope (q_out may be q itself); n_q_heads = 0: no queries
+ *   k, v, cu   as in mqkv_append; q_out may lie in one buffer with k and v (one projection's output) where their heads do not meet
+ *
+ * Keys are turned in f32 and quantized as they come out, without a rounding to dtype; q_out holds what mqd_rope gives.  Rows of q that
+ * belong to no sequence are left as they were; those of a sequence with a bad length are zeros.
+ */
+MQ_API int mqkv_append_rope(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int32_t dtype, const mqd_rope_plan *plan,
+                            const int32_t *pos, const void *q, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
+                            int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t n_q_heads, const void *k,
+                            int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                            int64_t v_head_stride, const int32_t *cu, int64_t n_tokens, mq_stream_t stream);
 
 /*
  * mqkv_read -- the values q * d of tokens of every sequence, dense, rounded once to dtype.
@@ -155,6 +173,14 @@ MQ_API int mqkv_release(const mqkv_cache *cache, const mqkv_seqs *seqs, const in
  * a bad id or a child that is not empty is left out. */
 MQ_API int mqkv_fork(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *parent, const int32_t *child,
                      int32_t n, void *workspace, size_t workspace_bytes, mq_stream_t stream);
+
+/* Every row becomes what another (or the same) one was: row b continues sequence parent[b] (int32 [n_seqs]; -1: it becomes empty), all
+ * at once, so that parent is any map of the rows (a step of beam search: mqd_beam_select's next_row).  Rows that continue the same sequence share its full
+ * pages; of a partly filled last page the lowest such row keeps the page and the others get copies of its used blocks.  Pages that nobody continues are
+ * free, and are taken for the copies at once.  All or nothing: with too few free pages, a bad entry of parent, a bad length or table entry no
+ * row changes (MQKV_ERR_STATE).  At most 32768 sequences. */
+MQ_API int mqkv_reorder(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *parent, void *workspace, size_t workspace_bytes,
+                        mq_stream_t stream);
 
 /* Moves live pages to the front of the pool: with L live pages, the k-th live page at or past L moves to the k-th
  * free page below L, and refs and table follow.  seqs has to be all sequences of the cache: the rows of others would

@@ -62,7 +62,7 @@ int set_error(int code, const char *fmt, ...) {
 
 namespace {
 int g_sm_count[kMaxDevices] = {0};
-constexpr int kAttrSlots = kAttrSlotKv + 32;       // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM; cache
+constexpr int kAttrSlots = kAttrSlotReorder + 1;    // GEMM below 16; GEMV 16 + 16 per format; fused GEMM; small-M GEMM; cache
 bool g_attr_done[kMaxDevices][kAttrSlots] = {};
 }  // namespace
 
@@ -160,7 +160,7 @@ int device_state(unsigned int **err) {
     return MQ_OK;
 }
 
-static int plane_from(void *base, int64_t M, int64_t K, Plane *p) {
+int plane_from(void *base, int64_t M, int64_t K, Plane *p) {
     mq_plane_layout L;
     int rc = mq_q8_plane_layout(M, K, &L);
     if (rc != MQ_OK) return rc;
@@ -173,7 +173,7 @@ static int plane_from(void *base, int64_t M, int64_t K, Plane *p) {
     return MQ_OK;
 }
 
-static int check_k(int64_t K) {
+int check_k(int64_t K) {
     if (K <= 0 || K % kQK != 0 || K >= kMaxDim)
         return set_error(MQ_ERR_SHAPE, "K=%lld must be a positive multiple of 256 below 2^31", (long long)K);
     return MQ_OK;

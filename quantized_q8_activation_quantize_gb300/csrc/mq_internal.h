@@ -45,6 +45,10 @@ struct Dump {
 
 int set_error(int code, const char *fmt, ...);
 
+// MQ_OK for a K that the planes allow (a positive multiple of 256 below 2^31); the sections of a plane at `base`
+int check_k(int64_t K);
+int plane_from(void *base, int64_t M, int64_t K, Plane *p);
+
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // whether the byte ranges [a, a + na) and [b, b + nb) share a byte
@@ -120,5 +124,6 @@ void *tensor_map_encoder();
 constexpr int kAttrSlotSmall = kAttrSlotSwiglu + 8;
 // attribute slots of the cache's attention: 2 * dtype + (head_dim == 128), 8 per kernel
 constexpr int kAttrSlotKv = kAttrSlotSmall + 16;
+constexpr int kAttrSlotReorder = kAttrSlotKv + 32;
 
 }  // namespace mq

@@ -168,6 +168,16 @@ __device__ __forceinline__ void kv_error(unsigned int *err, unsigned int bit) { 
 // launchers (arguments already validated)
 int kv_launch_append(const KvView &c, const KvRows &r, int dtype, const void *k, int64_t kt, int64_t kh, const void *v,
                      int64_t vt, int64_t vh, unsigned int *err, cudaStream_t s);
+// the queries beside a turned append (mq_kv_rope.cu); x: nullptr where there are none
+struct KvRopeRows {
+    const void *x;
+    void *out;
+    int64_t xt, xh, ot, oh;
+    int32_t heads;
+};
+struct RopePlan;
+int kv_launch_append_rope(const KvView &c, const KvRows &r, int dtype, const RopePlan &plan, const int32_t *pos, const KvRopeRows &q, const void *k,
+                          int64_t kt, int64_t kh, const void *v, int64_t vt, int64_t vh, unsigned int *err, cudaStream_t s);
 int kv_launch_read(const KvView &c, const KvRows &r, int dtype, void *k, int64_t kt, int64_t kh, void *v, int64_t vt,
                    int64_t vh, const int32_t *start, unsigned int *err, cudaStream_t s);
 
@@ -195,6 +205,7 @@ int kv_launch_extend(const KvPages &p, const int32_t *add, void *ws, unsigned in
 int kv_launch_release(const KvPages &p, const int32_t *ids, int n, unsigned int *err, cudaStream_t s);
 int kv_launch_fork(const KvPages &p, const int32_t *parent, const int32_t *child, int n, void *ws, unsigned int *err,
                    cudaStream_t s);
+int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigned int *err, cudaStream_t s);
 int kv_launch_compact(const KvPages &p, void *ws, unsigned int *err, cudaStream_t s);
 int kv_launch_copy(const KvPages &p, const int32_t *src, const int32_t *dst, int n, unsigned int *err, cudaStream_t s);
 

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "mq_kv.cuh"
+#include "mqd.cuh"
 
 namespace mq {
 namespace {
@@ -96,6 +97,17 @@ bool rows_apart(int64_t n, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
     return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (n - 1) * ts + dim);
 }
 
+// whether the values of two [n][width] tensors of the given token strides are surely apart: their spans are, or both have one stride and their rows'
+// places in it do not meet
+bool values_apart(const void *a, size_t na, int64_t as, int64_t aw, const void *b, size_t nb, int64_t bs, int64_t bw, int64_t n, int32_t dtype) {
+    if (!overlaps(a, na, b, nb)) return true;
+    if (n <= 1 || as != bs || as <= 0) return false;
+    const int64_t size = type_bytes(dtype), s = as * size;
+    int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % s;
+    if (d < 0) d += s;
+    return aw * size <= d && d + bw * size <= s;
+}
+
 KvView view_of(const mqkv_cache &c, const mqkv_seqs &s, const mqkv_layout &lay, int32_t layer) {
     KvView v;
     v.pool = static_cast<uint8_t *>(c.pool) + (size_t)layer * lay.layer_bytes;
@@ -179,6 +191,50 @@ int mqkv_append(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, i
     KV_TRY(kv_state(&err));
     return kv_launch_append(view_of(*cache, *seqs, lay, layer), rows_of(cu, n_tokens, seqs->n_seqs), dtype, k, k_token_stride,
                             k_head_stride, v, v_token_stride, v_head_stride, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mqkv_append_rope(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int32_t dtype, const mqd_rope_plan *plan, const int32_t *pos,
+                     const void *q, int64_t q_token_stride, int64_t q_head_stride, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                     int32_t n_q_heads, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                     int64_t v_head_stride, const int32_t *cu, int64_t n_tokens, mq_stream_t stream) {
+    const char *fn = "mqkv_append_rope";
+    mqkv_layout lay;
+    KV_TRY(check_cache(fn, cache, &lay, false));
+    KV_TRY(check_seqs(fn, seqs));
+    KV_TRY(check_rows(fn, cache, seqs, layer, dtype, cu, n_tokens));
+    const int64_t H = cache->n_kv_heads, D = cache->head_dim;
+    RopePlan rope;
+    KV_TRY(rope_plan_of(fn, plan, (int32_t)D, &rope));
+    if (!aligned(pos, 4)) return set_error(MQ_ERR_ALIGN, "%s: pos %p not 4-byte aligned", fn, (const void *)pos);
+    if (n_q_heads < 0 || n_q_heads > 65536) return set_error(MQ_ERR_SHAPE, "%s: n_q_heads=%d not in 0 .. 65536", fn, n_q_heads);
+    if (n_tokens == 0) return MQ_OK;
+    KV_TRY(check_tensor(fn, "k", k, k_token_stride, k_head_stride, dtype));
+    KV_TRY(check_tensor(fn, "v", v, v_token_stride, v_head_stride, dtype));
+    const size_t pool = lay.page_bytes * (size_t)cache->n_pages, kb = span(n_tokens, H, D, k_token_stride, k_head_stride, dtype),
+                 vb = span(n_tokens, H, D, v_token_stride, v_head_stride, dtype);
+    size_t qb = 0, ob = 0;
+    if (n_q_heads > 0) {
+        KV_TRY(check_rope_heads(fn, "q", q, q_token_stride, q_head_stride, dtype));
+        KV_TRY(check_rope_heads(fn, "q_out", q_out, q_out_token_stride, q_out_head_stride, dtype));
+        KV_TRY(check_rope_out(fn, q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, n_tokens, n_q_heads, D, dtype));
+        qb = span(n_tokens, n_q_heads, D, q_token_stride, q_head_stride, dtype);
+        ob = span(n_tokens, n_q_heads, D, q_out_token_stride, q_out_head_stride, dtype);
+    }
+    if (overlaps(cache->pool, pool, k, kb) || overlaps(cache->pool, pool, v, vb) || overlaps(cache->pool, pool, q, qb) || overlaps(cache->pool, pool, q_out, ob))
+        return set_error(MQ_ERR_ARG, "%s: the pool %p overlaps q %p, q_out %p, k %p or v %p", fn, cache->pool, q, q_out, k, v);
+    // q_out may lie in one buffer with k and v (a projection's output) where their values do not meet
+    const int64_t ow = (n_q_heads - 1) * q_out_head_stride + D;
+    if (!values_apart(q_out, ob, q_out_token_stride, ow, k, kb, k_token_stride, (H - 1) * k_head_stride + D, n_tokens, dtype) ||
+        !values_apart(q_out, ob, q_out_token_stride, ow, v, vb, v_token_stride, (H - 1) * v_head_stride + D, n_tokens, dtype))
+        return set_error(MQ_ERR_ARG, "%s: q_out %p overlaps k %p or v %p", fn, q_out, k, v);
+    if (overlaps(q_out, ob, pos, pos ? (size_t)n_tokens * 4 : 0) || overlaps(q_out, ob, plan->turns, (size_t)plan->rot_dim * 4) ||
+        overlaps(q_out, ob, cu, cu ? ((size_t)seqs->n_seqs + 1) * 4 : 0))
+        return set_error(MQ_ERR_ARG, "%s: q_out %p overlaps pos %p, cu %p or the turns %p", fn, q_out, (const void *)pos, (const void *)cu, (const void *)plan->turns);
+    unsigned int *err = nullptr;
+    KV_TRY(kv_state(&err));
+    const KvRopeRows rows{n_q_heads > 0 ? q : nullptr, q_out, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, n_q_heads};
+    return kv_launch_append_rope(view_of(*cache, *seqs, lay, layer), rows_of(cu, n_tokens, seqs->n_seqs), dtype, rope, pos, rows, k, k_token_stride, k_head_stride, v,
+                                 v_token_stride, v_head_stride, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int mqkv_read(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t layer, int32_t dtype, void *k, int64_t k_token_stride,
@@ -326,6 +382,21 @@ int mqkv_fork(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *par
     unsigned int *err = nullptr;
     KV_TRY(kv_state(&err));
     return kv_launch_fork(pages_of(*cache, seqs, lay), parent, child, n, workspace, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mqkv_reorder(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *parent, void *workspace, size_t workspace_bytes, mq_stream_t stream) {
+    const char *fn = "mqkv_reorder";
+    mqkv_layout lay;
+    KV_TRY(check_cache(fn, cache, &lay, true));
+    KV_TRY(check_seqs(fn, seqs));
+    if (seqs->n_seqs > 32768) return set_error(MQ_ERR_SHAPE, "%s: n_seqs=%d above 32768", fn, seqs->n_seqs);
+    if (seqs->n_seqs == 0) return MQ_OK;
+    if (parent == nullptr) return set_error(MQ_ERR_ARG, "%s: NULL parent", fn);
+    if (!aligned(parent, 4)) return set_error(MQ_ERR_ALIGN, "%s: parent %p not 4-byte aligned", fn, (const void *)parent);
+    KV_TRY(check_ws(fn, workspace, workspace_bytes, mqkv_pages_workspace_bytes(cache, seqs)));
+    unsigned int *err = nullptr;
+    KV_TRY(kv_state(&err));
+    return kv_launch_reorder(pages_of(*cache, seqs, lay), parent, workspace, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int mqkv_compact(const mqkv_cache *cache, const mqkv_seqs *seqs, void *workspace, size_t workspace_bytes, mq_stream_t stream) {

@@ -305,6 +305,165 @@ __device__ __forceinline__ void remap_row(const KvPages &p, const Ws &ws, int b,
     }
 }
 
+// ---------------------------------------------------------------- reorder ---
+// Row b becomes what row parent[b] was.  One cluster of blocks does the bookkeeping (its barriers order the phases: checks, reference counts, pages
+// for the copies, the table), a second kernel copies the used blocks of the last pages that two rows would share.
+constexpr int kReorderCluster = 8, kReorderCells = 32768;      // cells of the table that a block holds at a time
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// the int at `p` of this block's shared memory, in block `rank` of the cluster
+__device__ __forceinline__ int cluster_peer(const int *p, int rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// what row b holds now and shall hold: pages (of its own, of its parent), tokens
+struct ReorderRow {
+    int parent, held, now, len;
+};
+__device__ __forceinline__ ReorderRow reorder_row(const KvPages &p, const int32_t *parent, int b) {
+    const int T = 1 << p.tshift;
+    ReorderRow r;
+    r.parent = parent[b];
+    r.len = r.parent >= 0 ? p.len[r.parent] : 0;
+    r.held = (int)(((int64_t)p.len[b] + T - 1) >> p.tshift);
+    r.now = (int)(((int64_t)r.len + T - 1) >> p.tshift);
+    return r;
+}
+
+// the reference counts' change for row b by one warp (sign -1: taken back): pages that both the row and its parent hold in the same place stay
+__device__ __forceinline__ void reorder_refs(const KvPages &p, const ReorderRow &r, int b, bool copies, int sign) {
+    if (r.parent == b && !copies) return;
+    const int32_t *own = p.table + (int64_t)b * p.max_pages, *from = p.table + (int64_t)(r.parent >= 0 ? r.parent : 0) * p.max_pages;
+    const int shared = r.now - copies;                         // the last page of a row that copies is its own
+    for (int s = threadIdx.x & 31; s < max(r.held, shared); s += 32) {
+        const int a = s < r.held ? own[s] : -1, c = s < shared ? from[s] : -1;
+        if (a == c) continue;
+        if (a >= 0) atomicAdd(&p.refs[a], -sign);
+        if (c >= 0) atomicAdd(&p.refs[c], sign);
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_reorder_kernel(KvPages p, const int32_t *parent, Ws ws, int cols, unsigned int *err) {
+    extern __shared__ int32_t s_cells[];                       // [n_seqs][cols]
+    __shared__ int s_warp[32], s_bad, s_most;
+    grid_dep_launch();
+    grid_dep_wait();
+    const int T = 1 << p.tshift, n = p.n_seqs, rank = cluster_rank(), ranks = gridDim.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kPlanThreads / 32;
+    int32_t *first = ws.dst;                                   // the lowest row that continues each row
+    if (threadIdx.x == 0) s_bad = 0, s_most = 0;
+    for (int b = rank * kPlanThreads + threadIdx.x; b < n; b += ranks * kPlanThreads) first[b] = INT32_MAX;
+    cluster_sync();
+    // checks, a warp per row
+    unsigned bad = 0;
+    int most = 0;
+    for (int b = rank * warps + warp; b < n; b += ranks * warps) {
+        const int a = parent[b];
+        const int64_t held = ((int64_t)p.len[b] + T - 1) >> p.tshift;
+        if (a < -1 || a >= n) bad |= KV_ERR_SEQ;
+        else if (a >= 0 && lane == 0) atomicMin(&first[a], b);
+        if (p.len[b] < 0 || held > p.max_pages) {
+            bad |= KV_ERR_LEN;
+            continue;
+        }
+        most = max(most, (int)held);
+        for (int s = lane; s < held; s += 32) {
+            const int page = p.table[(int64_t)b * p.max_pages + s];
+            if (page < 0 || page >= p.n_pages) bad |= KV_ERR_PAGE;
+        }
+    }
+    if (bad) atomicOr(&s_bad, (int)bad);
+    if (lane == 0) atomicMax(&s_most, most);
+    cluster_sync();
+    bad = 0, most = 0;
+    for (int i = 0; i < ranks; ++i) bad |= (unsigned)cluster_peer(&s_bad, i), most = max(most, cluster_peer(&s_most, i));
+    if (bad) {                                                 // nothing has changed
+        if (rank == 0 && threadIdx.x == 0) {
+            kv_error(err, bad);
+            ws.plan->n = 0;
+        }
+        cluster_sync();                                        // (no block ends while another reads its shared memory)
+        return;
+    }
+    for (int b = rank * warps + warp; b < n; b += ranks * warps) {
+        const ReorderRow r = reorder_row(p, parent, b);
+        reorder_refs(p, r, b, r.parent >= 0 && (r.len & (T - 1)) != 0 && first[r.parent] != b, 1);
+    }
+    cluster_sync();
+    if (rank == 0) {
+        int need = 0;
+        for (int base = 0; base < n; base += kPlanThreads) {
+            const int b = base + threadIdx.x;
+            int k = 0, len = 0;
+            if (b < n) {
+                const ReorderRow r = reorder_row(p, parent, b);
+                len = r.len;
+                k = r.parent >= 0 && (len & (T - 1)) != 0 && first[r.parent] != b;
+            }
+            int total;
+            const int at = need + block_scan(k, s_warp, &total);
+            if (b < n) ws.prefix[b] = k ? at : -1, ws.blocks[b] = len;
+            need += total;
+        }
+        __syncthreads();
+        const bool enough = find_free(p.refs, p.n_pages, need, ws.list, s_warp);
+        if (enough) {
+            for (int base = 0; base < n; base += kPlanThreads) {
+                const int b = base + threadIdx.x, at = b < n ? ws.prefix[b] : -1;
+                if (at < 0) continue;
+                const int len = ws.blocks[b], page = ws.list[at];
+                ws.src[at] = p.table[(int64_t)parent[b] * p.max_pages + (len >> p.tshift)];
+                ws.dst[at] = page;
+                ws.list[at] = ((len & (T - 1)) + kKB - 1) / kKB;
+                p.refs[page] = 1;
+            }
+        }
+        if (threadIdx.x == 0) {
+            ws.plan->n = enough ? need : 0;
+            s_bad = !enough;
+            if (!enough) kv_error(err, KV_ERR_FULL);
+        }
+    }
+    cluster_sync();
+    if (cluster_peer(&s_bad, 0)) {                             // too few pages: the counts go back
+        for (int b = rank * warps + warp; b < n; b += ranks * warps)
+            reorder_refs(p, reorder_row(p, parent, b), b, ws.prefix[b] >= 0, -1);
+        cluster_sync();
+        return;
+    }
+    // the table, some columns of all rows at a time
+    for (int c0 = rank * cols; c0 < most; c0 += ranks * cols) {
+        const int nc = min(cols, most - c0);
+        for (int i = threadIdx.x; i < n * nc; i += kPlanThreads) {
+            const int b = i / nc, s = c0 + i - b * nc;
+            s_cells[i] = p.table[(int64_t)b * p.max_pages + s];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * nc; i += kPlanThreads) {
+            const int b = i / nc, s = c0 + i - b * nc;
+            const ReorderRow r = reorder_row(p, parent, b);
+            if (r.parent == b && ws.prefix[b] < 0) continue;
+            int page = -1;
+            if (s < r.now) page = s == r.now - 1 && ws.prefix[b] >= 0 ? ws.dst[ws.prefix[b]] : s_cells[r.parent * nc + s - c0];
+            if (s < max(r.held, r.now)) p.table[(int64_t)b * p.max_pages + s] = page;
+        }
+        __syncthreads();
+    }
+    cluster_sync();                                            // all have read the lengths
+    for (int b = rank * kPlanThreads + threadIdx.x; b < n; b += ranks * kPlanThreads) p.len[b] = ws.blocks[b];
+}
+
 constexpr int kCopyThreads = 256, kCopyChunk = 16384;
 
 __device__ __forceinline__ void copy_span(uint8_t *dst, const uint8_t *src, int bytes) {
@@ -381,6 +540,34 @@ int kv_launch_fork(const KvPages &p, const int32_t *parent, const int32_t *child
     const int64_t units = (int64_t)n * p.n_layers * 2 * p.H;
     const int grid = (int)(units < 8 * sm_count() ? units : 8 * sm_count());
     return cuda_error(launch_pdl(kv_copy_used_kernel, dim3(grid), dim3(kCopyThreads), 0, s, p, w), "mqkv_fork copy launch");
+}
+
+int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigned int *err, cudaStream_t s) {
+    const Ws w(ws, p.n_pages, p.n_seqs);
+    int cols = 32;
+    while (cols > 1 && (int64_t)cols * p.n_seqs > kReorderCells) cols >>= 1;
+    const int smem = cols * p.n_seqs * 4;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kv_reorder_kernel), kReorderCells * 4, kAttrSlotReorder);
+    if (rc != MQ_OK) return rc;
+    // one block for a small table, a cluster where there is much to check and to move
+    const unsigned blocks = (int64_t)p.n_seqs * p.max_pages <= 8192 ? 1 : kReorderCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    rc = cuda_error(cudaLaunchKernelEx(&cfg, kv_reorder_kernel, p, parent, w, cols, err), "mqkv_reorder plan launch");
+    if (rc != MQ_OK) return rc;
+    const int64_t units = (int64_t)p.n_seqs * p.n_layers * 2 * p.H;
+    const int grid = (int)(units < 8 * sm_count() ? units : 8 * sm_count());
+    return cuda_error(launch_pdl(kv_copy_used_kernel, dim3(grid), dim3(kCopyThreads), 0, s, p, w), "mqkv_reorder copy launch");
 }
 
 int kv_launch_compact(const KvPages &p, void *ws, unsigned int *err, cudaStream_t s) {

@@ -1,0 +1,121 @@
+// mqd_rope.cuh -- rotary positions: the angle of a pair as a fraction of a turn, its sine and cosine, and the rotation itself
+// (mqd_rope and mqkv_append_rope compute the same values, bit for bit).
+#pragma once
+
+#include "mqd.cuh"
+
+namespace mq {
+
+// (a cos, a sin) of the angle pos * F / 2^64 turns.  The product modulo 2^64 is exact, so far positions lose nothing; its upper 32 bits are cut
+// into the nearest quarter turn and a rest of at most an eighth, |t| <= pi / 4, where the Taylor series through t^9 and t^10 are off
+// by 3e-9 and 2e-10 (half an f32 step is 6e-8).  About 25 instructions for both, without a branch.
+__device__ __forceinline__ float2 rope_cos_sin(int32_t pos, uint64_t F, float amplitude) {
+    const uint32_t phase = (uint32_t)(((uint64_t)(int64_t)pos * F) >> 32);
+    const uint32_t quarter = (phase + 0x20000000u) >> 30;                   // (past 7/8 of a turn the sum wraps to quarter 0)
+    const float t = __fmul_rn((float)(int32_t)(phase - (quarter << 30)), 1.5707963267948966f * 0x1p-30f);
+    const float z = __fmul_rn(t, t);
+    float s = 2.75573192e-6f;                                               // 1 / 9!
+    s = __fmaf_rn(s, z, -1.98412698e-4f);
+    s = __fmaf_rn(s, z, 8.33333333e-3f);
+    s = __fmaf_rn(s, z, -1.66666667e-1f);
+    s = __fmaf_rn(__fmul_rn(s, z), t, t);
+    float c = -2.75573192e-7f;                                              // -1 / 10!
+    c = __fmaf_rn(c, z, 2.48015873e-5f);
+    c = __fmaf_rn(c, z, -1.38888889e-3f);
+    c = __fmaf_rn(c, z, 4.16666667e-2f);
+    c = __fmaf_rn(c, z, -0.5f);
+    c = __fmaf_rn(c, z, 1.0f);
+    const bool odd = quarter & 1;
+    const float x = odd ? s : c, y = odd ? c : s;
+    const float ax = ((quarter + 1) & 2) ? -amplitude : amplitude, ay = (quarter & 2) ? -amplitude : amplitude;
+    return make_float2(__fmul_rn(x, ax), __fmul_rn(y, ay));
+}
+
+__device__ __forceinline__ void rope_turn(float2 cs, float &u, float &v) {
+    const float a = __fmaf_rn(u, cs.x, -__fmul_rn(v, cs.y)), b = __fmaf_rn(v, cs.x, __fmul_rn(u, cs.y));
+    u = a, v = b;
+}
+
+constexpr int kRopeThreads = 256, kRopePairs = 512;         // pairs whose (cos, sin) a block holds
+
+template <typename T, int W>
+struct RawW;
+template <>
+struct RawW<float, 4> { float4 w; };
+template <>
+struct RawW<__half, 4> { uint2 w; };
+template <>
+struct RawW<__nv_bfloat16, 4> { uint2 w; };
+template <>
+struct RawW<__half, 8> { uint4 w; };
+template <>
+struct RawW<__nv_bfloat16, 8> { uint4 w; };
+
+template <typename T, int W>
+__device__ __forceinline__ void unpack_w(const RawW<T, W> &r, float (&x)[W]) {
+    if constexpr (W == 4) unpack4(*reinterpret_cast<const Raw4<T> *>(&r), x);
+    else unpack8(*reinterpret_cast<const Raw8<T> *>(&r), x);
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_w(T *p, const float (&x)[W]) {
+    if constexpr (W == 4) store4(p, x);
+    else store8(p, pack8(x, T()));
+}
+
+// Tokens [t0, t0 + n) by the block's threads: their (cos, sin) once for all heads, then a thread turns W pairs at a time, in pieces of 16 bytes (W = 4
+// of 16 bits: 8), two neighbouring ones (interleaved) or two that lie half the rotated part apart.  pos(t): token t's position; live(t): 1, 0 (its
+// row stays as it is) or 2 (its row becomes zeros; `zeros`: whether there is one).  s_cs: n * half pairs.
+template <typename T, int W, typename Pos, typename Live>
+__device__ __forceinline__ void rope_block(const RopePlan &plan, const RopeRows &r, int64_t t0, int n, float2 *s_cs, Pos pos, Live live, bool zeros) {
+    for (int i = threadIdx.x; i < n * plan.half; i += kRopeThreads) {
+        const int t = i / plan.half;
+        s_cs[i] = rope_cos_sin(pos(t0 + t), plan.turns[i - t * plan.half], plan.amplitude);
+    }
+    __syncthreads();
+    const bool copy = r.x != r.out || zeros;
+    const int pairs = plan.half / W, per = pairs + (copy ? (r.dim - 2 * plan.half) / W : 0);     // pieces of a head
+    const int all = n * r.heads * per;
+    for (int i = threadIdx.x; i < all; i += kRopeThreads) {
+        const int row = i / per, j = i - row * per, t = row / r.heads, h = row - t * r.heads;
+        const T *x = static_cast<const T *>(r.x) + (t0 + t) * r.xt + h * r.xh;
+        T *out = static_cast<T *>(r.out) + (t0 + t) * r.ot + h * r.oh;
+        const int what = live(t0 + t);
+        if (what == 0) continue;
+        if (j < pairs) {
+            const int a = plan.interleaved ? 2 * j * W : j * W, b = plan.interleaved ? a + W : a + plan.half;
+            float u[W], v[W];
+            unpack_w<T, W>(*reinterpret_cast<const RawW<T, W> *>(x + a), u);
+            unpack_w<T, W>(*reinterpret_cast<const RawW<T, W> *>(x + b), v);
+            const float2 *cs = s_cs + t * plan.half + j * W;
+            if (plan.interleaved) {
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) {
+                    rope_turn(cs[e], u[2 * e], u[2 * e + 1]);
+                    rope_turn(cs[W / 2 + e], v[2 * e], v[2 * e + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) rope_turn(cs[e], u[e], v[e]);
+            }
+            if (what == 2) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) u[e] = v[e] = 0.0f;
+            }
+            store_w<T, W>(out + a, u);
+            store_w<T, W>(out + b, v);
+        } else {
+            const int a = 2 * plan.half + (j - pairs) * W;
+            RawW<T, W> w = *reinterpret_cast<const RawW<T, W> *>(x + a);
+            if (what == 2) w.w = {};
+            *reinterpret_cast<RawW<T, W> *>(out + a) = w;
+        }
+    }
+}
+
+// whether pieces of 8 values of 16 bits fit: whole ones in both halves, and 16-byte boundaries everywhere
+inline bool rope_wide(const RopePlan &p, const RopeRows &r) {
+    return p.half % 8 == 0 && (r.dim - 2 * p.half) % 8 == 0 && aligned(r.x, 16) && aligned(r.out, 16) &&
+           (r.xt % 8 | r.xh % 8 | r.ot % 8 | r.oh % 8) == 0;
+}
+
+}  // namespace mq

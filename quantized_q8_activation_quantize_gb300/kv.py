@@ -48,6 +48,7 @@ def lib():
     """The loaded libmq.so with this header's argument types (raises if it was not built)."""
     global _L
     if _L is None:
+        from . import decoder
         L = binding.lib()
         P, I64, I32, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
         C, S = ctypes.POINTER(Cache), ctypes.POINTER(Sequences)
@@ -55,6 +56,7 @@ def lib():
         types = {
             "mqkv_page_layout": [I32, I32, I32, I32, ctypes.POINTER(Layout)],
             "mqkv_append": [C, S, I32, I32, *rows, *rows, P, I64, P],
+            "mqkv_append_rope": [C, S, I32, I32, ctypes.POINTER(decoder.RopePlan), P, *rows, *rows, I32, *rows, *rows, P, I64, P],
             "mqkv_read": [C, S, I32, I32, *rows, *rows, P, P, I64, P],
             "mqkv_attention": [C, S, I32, I32, *rows, *rows, I32, P, I64, I64, I64, I32, I64, F, P, SZ, P],
             "mqkv_attention_workspace_bytes": [C, S, I32, I32, I64, I64, I64],
@@ -62,6 +64,7 @@ def lib():
             "mqkv_extend": [C, S, P, P, SZ, P],
             "mqkv_release": [C, S, P, I32, P],
             "mqkv_fork": [C, S, P, P, I32, P, SZ, P],
+            "mqkv_reorder": [C, S, P, P, SZ, P],
             "mqkv_compact": [C, S, P, SZ, P],
             "mqkv_copy_pages": [C, P, P, I32, P],
             "mqkv_device_status": [P],
@@ -211,6 +214,19 @@ def mqkv_append(cache, seqs, layer: int, k, v, cu=None, stream=None):
                                             _i32("cu", cu, seqs.n_seqs + 1), n, _on(stream, k)))
 
 
+def mqkv_append_rope(cache, seqs, layer: int, plan, q, q_out, k, v, cu=None, pos=None, stream=None):
+    """mqkv_append of k and v [tokens, n_kv_heads, head_dim] with the keys turned by `plan` (decoder.rope_plan), and q [tokens, n_q_heads,
+    head_dim] (or None) turned into q_out (may be q itself); pos int32 [tokens], None: the cached positions."""
+    n, H, D = len(k), cache.n_kv_heads, cache.head_dim
+    dtype = k.dtype
+    if v.dtype is not dtype or (q is not None and (q.dtype is not dtype or q_out.dtype is not dtype)):
+        _bad(f"k is {dtype}, v is {v.dtype}" + ("" if q is None else f", q {q.dtype}, q_out {q_out.dtype}"))
+    heads = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
+    queries = (None, 0, 0, None, 0, 0) if q is None else (*_rows("q", q, n, heads, D), *_rows("q_out", q_out, n, heads, D))
+    return _check((_L or lib()).mqkv_append_rope(cache, seqs, layer, _dtype(dtype), plan, _i32("pos", pos, n), *queries, heads, *_rows("k", k, n, H, D),
+                                                 *_rows("v", v, n, H, D), _i32("cu", cu, seqs.n_seqs + 1), n, _on(stream, k)))
+
+
 def mqkv_read(cache, seqs, layer: int, k, v, cu=None, start=None, stream=None):
     """Into k, v [tokens, n_kv_heads, head_dim] (either may be None) the cached values from position start (int32
     [n_seqs]) of each sequence on, or the last ones."""
@@ -254,6 +270,11 @@ def mqkv_fork(cache, seqs, parent, child, workspace, stream=None):
     n = parent.numel()
     return _check((_L or lib()).mqkv_fork(cache, seqs, _i32("parent", parent), _i32("child", child, n), n, *_ws(workspace),
                                           _on(stream, workspace)))
+
+
+def mqkv_reorder(cache, seqs, parent, workspace, stream=None):
+    """Row b becomes what row parent[b] was (int32 [n_seqs]; -1: empty)."""
+    return _check((_L or lib()).mqkv_reorder(cache, seqs, _i32("parent", parent, seqs.n_seqs), *_ws(workspace), _on(stream, workspace)))
 
 
 def mqkv_compact(cache, seqs, workspace, stream=None):
