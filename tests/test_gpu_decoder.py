@@ -383,8 +383,8 @@ def check_select(logits, scores, n_cand, stop=-1):
         m = rows.max(1, keepdims=True)
         m0 = np.where(np.isfinite(m), m, 0)
         with np.errstate(divide="ignore", invalid="ignore"):
-            lse = m0 + np.log(np.exp(rows - m0).sum(1, keepdims=True))
-            base = cum[g][:, None] + (rows - lse)
+            # the largest first: at 1e30 even 64 bits would lose the logarithm beside it
+            base = cum[g][:, None] + ((rows - m0) - np.log(np.exp(rows - m0).sum(1, keepdims=True)))
         base = np.where(np.isneginf(rows) | ~(cum[g][:, None] > -np.inf), -np.inf, base)
         flat = base.reshape(-1)
         order = np.lexsort((np.arange(flat.size), -flat))[:n_cand]
