@@ -7,6 +7,7 @@
 // that only few values pass.  The join has a block per group: the rows' sums, then n_cand times the best of all lists' heads.
 // Within a row the order of the scores is that of the logits, so only the join needs the sums; it compares f32 pairs, 48 bits.
 #include <cfloat>
+#include <type_traits>
 
 #include "mq_rms.cuh"
 #include "mqd.cuh"
@@ -29,8 +30,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// exp(x) for x <= 0: x log2(e) with the constant in two parts
-__device__ __forceinline__ float exp_neg(float x) { return ex2(__fmaf_rn(x, 1.442695f, __fmul_rn(x, 1.925963e-8f))); }
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float exp_neg(float x) { return ex2(x * kLog2e); }
 
 struct BeamPiece {
     float m;            // largest value (-inf: none)
@@ -44,46 +45,62 @@ struct BeamWs {
     int64_t length;     // of a piece, a multiple of 8
 };
 
-// values of a tile in registers, -inf where there is none; vectors of 16 bytes from the boundary at or before the row's beginning (bytes of
+// values of the tile at place e0 in registers, -inf where there is none; vectors of 16 bytes from the boundary at or before the row's beginning (bytes of
 // a vector that holds a value of the row lie in that value's 16-byte granule, so no read leaves memory)
 template <typename T>
-__device__ __forceinline__ void load_tile(const T *base, int64_t first, int64_t end, int64_t e0, float (&x)[kScanPer]) {
+__device__ __forceinline__ void load_tile(const T *base, int first, int stop, int e0, float (&x)[kScanPer]) {
     constexpr int V = 16 / sizeof(T);
+    const T *p = base + e0 + threadIdx.x * V;
+    uint4 w[kScanPer / V];
+    if (e0 >= first && stop - e0 >= kTile) {                // nearly always
+#pragma unroll
+        for (int j = 0; j < kScanPer / V; ++j) w[j] = __ldcs(reinterpret_cast<const uint4 *>(p + j * kScanThreads * V));
+    } else {
+        const uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+#pragma unroll
+        for (int j = 0; j < kScanPer / V; ++j) {
+            const int e = e0 + (j * kScanThreads + (int)threadIdx.x) * V;
+            w[j] = make_uint4(none, none, none, none);
+            if (e + V > first && e < stop) w[j] = __ldcs(reinterpret_cast<const uint4 *>(p + j * kScanThreads * V));
+        }
+    }
 #pragma unroll
     for (int j = 0; j < kScanPer / V; ++j) {
-        const int64_t e = e0 + ((int64_t)j * kScanThreads + threadIdx.x) * V;
-        if (e + V > first && e < end) {
-            if constexpr (V == 4) {
-                const float4 w = __ldcs(reinterpret_cast<const float4 *>(base + e));
-                x[4 * j] = w.x, x[4 * j + 1] = w.y, x[4 * j + 2] = w.z, x[4 * j + 3] = w.w;
-            } else {
-                float v[8];
-                unpack8(Raw8<T>{__ldcs(reinterpret_cast<const uint4 *>(base + e))}, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[8 * j + i] = v[i];
-            }
-            if (e < first || e + V > end) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e + i < first || e + i >= end) x[V * j + i] = -INFINITY;
-            }
+        if constexpr (V == 4) {
+            x[4 * j] = __uint_as_float(w[j].x), x[4 * j + 1] = __uint_as_float(w[j].y);
+            x[4 * j + 2] = __uint_as_float(w[j].z), x[4 * j + 3] = __uint_as_float(w[j].w);
         } else {
+            float v[8];
+            unpack8(Raw8<T>{w[j]}, v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[V * j + i] = -INFINITY;
+            for (int i = 0; i < 8; ++i) x[8 * j + i] = v[i];
+        }
+    }
+    if (!(e0 >= first && stop - e0 >= kTile)) {
+#pragma unroll
+        for (int j = 0; j < kScanPer; ++j) {
+            const int e = e0 + (j / V * kScanThreads + (int)threadIdx.x) * V + j % V;
+            if (e < first || e >= stop) x[j] = -INFINITY;
         }
     }
 }
 
+// an entry of a list: value and token in the order of unsigned integers, the larger value first and of equals the lower token
+__device__ __forceinline__ uint64_t entry(float v, int token) { return ((uint64_t)ordered(v + 0.0f) << 32) | ~(uint32_t)token; }
+
 // the best k of the n entries in s_buf, sorted, to its front; returns how many.  A thread counts what is better than its entry: n^2 / 256 steps a thread,
 // for a few dozen entries
-__device__ __forceinline__ int keep_best(float2 *s_buf, float2 *s_best, int n, int k) {
+__device__ __forceinline__ int keep_best(uint64_t *s_buf, uint64_t *s_best, int n, int k) {
+    if (threadIdx.x == 0) s_buf[n] = 0;                     // (pairs are read)
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kScanThreads) {
-        const float2 a = s_buf[i];
+        const uint64_t a = s_buf[i];
+        const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(s_buf);
         int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) {
-            const float2 b = s_buf[j];
-            rank += b.x > a.x || (b.x == a.x && __float_as_int(b.y) < __float_as_int(a.y));
+#pragma unroll 4
+        for (int j = 0; j < n; j += 2) {
+            const ulonglong2 b = two[j / 2];
+            rank += (int)(b.x > a) + (int)(b.y > a);
         }
         if (rank < k) s_best[rank] = a;
     }
@@ -94,12 +111,29 @@ __device__ __forceinline__ int keep_best(float2 *s_buf, float2 *s_best, int n, i
     return n;
 }
 
+// sum of exp(v - m)
+__device__ __forceinline__ float tile_sum(const float (&v)[kScanPer], float m) {
+    const uint64_t neg = f2_pack(-m, -m), l = f2_pack(kLog2e, kLog2e);
+    uint64_t sum = f2_pack(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kScanPer; i += 2) {
+        float a, b;
+        f2_unpack(f2_mul(f2_add(f2_pack(v[i], v[i + 1]), neg), l), a, b);
+        sum = f2_add(sum, f2_pack(ex2(a), ex2(b)));
+    }
+    float a, b;
+    f2_unpack(sum, a, b);
+    return a + b;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *logits, int64_t stride, int64_t V, const float *scores, int k, BeamWs ws) {
     constexpr int VEC = 16 / sizeof(T);
-    __shared__ float2 s_buf[kTile + kBuffer];
-    __shared__ float2 s_best[kMaxCand];
-    __shared__ uint2 s_key[kScanThreads / 32];
+    __shared__ __align__(16) uint64_t s_buf[kTile + kBuffer + 2];
+    __shared__ uint64_t s_best[kMaxCand];
+    __shared__ uint32_t s_key[kScanThreads / 32];
+    __shared__ int s_hits[kScanThreads / 32];
+    __shared__ uint2 s_bar;
     __shared__ float s_m[kScanThreads / 32], s_s[kScanThreads / 32];
     __shared__ int s_n;
     grid_dep_launch();
@@ -112,102 +146,148 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
         return;
     }
     const T *p = logits + row * stride;
-    const int shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-    const T *base = p - shift;
-    const int64_t first = shift, end = shift + V;
-    const int64_t e0 = piece * ws.length, stop = min(end, e0 + ws.length);
+    const int first = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    const T *base = p - first;
+    const int e0 = (int)(piece * ws.length), stop = (int)min(first + V, e0 + ws.length);
     if (threadIdx.x == 0) s_n = 0;
     float m = -INFINITY, s = 0.0f, thr = -INFINITY;
     int have = 0;
-    bool sorted = true;
+
+    // token of place i of the tile at `at`
+    auto token = [&](int at, int i) { return at - first + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC; };
+    // NaN and +inf as what they count as; the largest
+    auto clean = [&](float(&v)[kScanPer]) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i) {
+            v[i] = v[i] == v[i] ? fminf(v[i], FLT_MAX) : -INFINITY;
+            top = fmaxf(top, v[i]);
+        }
+        return top;
+    };
+    // values past the bar (those equal to it: up to token `last`) into the list, as far as it has room
+    auto push = [&](const float(&v)[kScanPer], int at, float bar, int last) {
+#pragma unroll
+        for (int j = 0; j < kScanPer; j += 4) {
+            if (!(fmaxf(fmaxf(v[j], v[j + 1]), fmaxf(v[j + 2], v[j + 3])) >= bar)) continue;
+#pragma unroll
+            for (int i = j; i < j + 4; ++i)
+                if ((v[i] > bar) | ((v[i] == bar) & (token(at, i) <= last) & (v[i] > -INFINITY))) {
+                    const int n = atomicAdd(&s_n, 1);
+                    if (n < kTile + kBuffer) s_buf[n] = entry(v[i], token(at, i));
+                }
+        }
+    };
+    // (all threads, after a barrier) entries in the list; nobody adds to it before all know
+    auto count = [&]() {
+        const int n = s_n;
+        __syncthreads();
+        return n;
+    };
+    // (all threads) the best k of the n entries stay; what does not pass their last one is out
+    auto settle = [&](int n) {
+        if (n > have) {
+            have = keep_best(s_buf, s_best, n, k);
+            if (threadIdx.x == 0) s_n = have;
+            if (have == k) thr = from_ordered((uint32_t)(s_buf[k - 1] >> 32));
+            __syncthreads();
+        }
+    };
+
     float x[kScanPer];
     load_tile(base, first, stop, e0, x);
+    int span = e0, tiles = 1;                               // the list is settled after 1, 2, 4, 8 .. tiles
 #pragma unroll 1
-    for (int64_t at = e0; at < stop; at += kTile) {
+    for (int at = e0; at < stop; at += kTile) {
         float v[kScanPer], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kScanPer; ++i) {
-            v[i] = fminf(fmaxf(x[i], -INFINITY), FLT_MAX);  // (a NaN gives way to -inf)
-            top = fmaxf(top, v[i]);
+            v[i] = x[i];
+            top = fmaxf(top, v[i]);                         // (NaN aside)
         }
         if (at + kTile < stop) load_tile(base, first, stop, at + kTile, x);
-        if (top > -INFINITY) {
-            if (top > m) {
-                s *= exp_neg(m - top);                      // (m = -inf: zero)
-                m = top;
-            }
-            float a = 0.0f, b = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kScanPer; i += 2) a += exp_neg(v[i] - m), b += exp_neg(v[i + 1] - m);
-            s += a + b;
+        float sum = tile_sum(v, fmaxf(top, m));
+        if (!(sum <= FLT_MAX)) {                            // a NaN or +inf, or nothing yet but -inf
+            top = clean(v);
+            sum = fmaxf(top, m) > -INFINITY ? tile_sum(v, fmaxf(top, m)) : 0.0f;
         }
-        const int from = (int)(at - first);                 // token of the tile's first place
-        auto token = [&](int i) { return from + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC; };
-        float bar = thr;                                    // what passes: > bar, or = bar up to token last
-        int last = INT32_MIN;
+        if (top > m) {
+            s *= exp_neg(m - top);                          // (m = -inf: zero)
+            m = top;
+        }
+        s += sum;
         if (at == e0) {
             // every warp's ceil(k / 8)-th largest of its threads' largest values: at least k values are not below the least of these
-            int at_top = INT32_MAX;
-#pragma unroll
-            for (int i = kScanPer - 1; i >= 0; --i)
-                if (v[i] == top) at_top = token(i);
             const uint32_t own = top > -INFINITY ? ordered(top + 0.0f) : 0u;
-            uint32_t key = own, best = 0, who = 0;
+            uint32_t key = own, best = 0;
             for (int j = 0; j < (k + 7) / 8; ++j) {
                 best = __reduce_max_sync(kFull, key);
-                who = __reduce_min_sync(kFull, key == best ? (uint32_t)at_top : 0xffffffffu);
-                if (key == best && (uint32_t)at_top == who) key = 0;
+                if (lane == __ffs(__ballot_sync(kFull, key == best)) - 1) key = 0;
             }
-            if (lane == 0) s_key[warp] = make_uint2(best, who);
+            if (lane == 0) s_key[warp] = best;
             __syncthreads();
-            uint2 least = s_key[0];
+            uint32_t least = s_key[0];
 #pragma unroll
-            for (int w = 1; w < kScanThreads / 32; ++w) {
-                const uint2 o = s_key[w];
-                if (o.x < least.x || (o.x == least.x && o.y > least.y)) least = o;
+            for (int w = 1; w < kScanThreads / 32; ++w) least = min(least, s_key[w]);
+            float bar = least != 0 ? from_ordered(least) : -INFINITY;
+            int last = INT32_MAX, hits = 0;
+            if (top >= bar) {
+#pragma unroll
+                for (int i = 0; i < kScanPer; ++i) hits += v[i] >= bar;
             }
-            if (least.x == 0) {
-                // a warp has too few values (the end of a row, a mask): the k-th largest of all threads' largest
+            hits = __reduce_add_sync(kFull, hits);
+            if (lane == 0) s_hits[warp] = hits;
+            __syncthreads();
+            hits = 0;
+#pragma unroll
+            for (int w = 0; w < kScanThreads / 32; ++w) hits += s_hits[w];
+            if (hits > kBuffer) {
+                // a warp has too few values (the end of a row, a mask) or many are equal: the k-th of all threads' largest, by value and token
                 uint2 *s_all = reinterpret_cast<uint2 *>(s_buf);
+                int at_top = INT32_MAX;
+#pragma unroll
+                for (int i = kScanPer - 1; i >= 0; --i)
+                    if (v[i] == top) at_top = token(at, i);
                 s_all[threadIdx.x] = make_uint2(own, (uint32_t)at_top);
                 __syncthreads();
                 int rank = 0;
 #pragma unroll 8
                 for (int j = 0; j < kScanThreads; ++j) {
                     const uint2 o = s_all[j];
-                    rank += o.x > own || (o.x == own && o.y < (uint32_t)at_top);
+                    rank += (o.x > own) | ((o.x == own) & (o.y < (uint32_t)at_top));
                 }
-                if (own != 0 && rank == k - 1) s_key[0] = make_uint2(own, (uint32_t)at_top);
-                least = make_uint2(0, 0);
-                if (__syncthreads_or(own != 0 && rank == k - 1)) least = s_key[0];
+                const bool kth = own != 0 && rank == k - 1;
+                if (kth) s_bar = make_uint2(own, (uint32_t)at_top);
+                if (__syncthreads_or(kth)) bar = from_ordered(s_bar.x), last = (int)s_bar.y;
             }
-            if (least.x != 0) bar = from_ordered(least.x), last = (int)least.y;
+            if (top >= bar) push(v, at, bar, last);
+            __syncthreads();
+            settle(count());
+            span = at + kTile;
+            continue;
         }
-        bool hit = false;
-        if (top >= bar && top > -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kScanPer; ++i)
-                if (v[i] > bar || (v[i] == bar && token(i) <= last)) {
-                    s_buf[atomicAdd(&s_n, 1)] = make_float2(v[i], __int_as_float(token(i)));
-                    hit = true;
-                }
-        }
-        if (__syncthreads_or(hit)) {
-            const int n = s_n;
-            __syncthreads();                                // (all have read it before anyone adds to it)
-            if (at == e0 || n > kBuffer) {
-                have = keep_best(s_buf, s_best, n, k);
-                sorted = true;
-                if (threadIdx.x == 0) s_n = have;
-                if (have == k) thr = s_buf[k - 1].x;
+        if (top > thr) push(v, at, thr, INT32_MIN);         // (of equals the first, which the list holds)
+        if (at + kTile - span < tiles * kTile && at + kTile < stop) continue;
+        __syncthreads();
+        const int n = count();
+        if (n > kTile + kBuffer) {
+            // more than the list has room for: the span again, tile by tile
+            if (threadIdx.x == 0) s_n = have;
+            for (int again = span; again <= at; again += kTile) {
                 __syncthreads();
-            } else {
-                have = n, sorted = false;
+                load_tile(base, first, stop, again, v);
+                if (clean(v) > thr) push(v, again, thr, INT32_MIN);
+                __syncthreads();
+                settle(count());
             }
+        } else {
+            settle(n);
         }
+        span = at + kTile;
+        tiles = min(2 * tiles, 1 << 16);
     }
-    if (!sorted) have = keep_best(s_buf, s_best, have, k);
-    for (int i = threadIdx.x; i < have; i += kScanThreads) ws.list[(int64_t)blockIdx.x * k + i] = s_buf[i];
+    for (int i = threadIdx.x; i < have; i += kScanThreads) 
+        ws.list[(int64_t)blockIdx.x * k + i] = make_float2(from_ordered((uint32_t)(s_buf[i] >> 32)), __uint_as_float(~(uint32_t)s_buf[i]));
     float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -216,15 +296,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
     if (lane == 0) s_m[warp] = top, s_s[warp] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float all = s_m[0];
+    if (warp == 0) {
+        const float part = lane < kScanThreads / 32 ? s_m[lane] : -INFINITY;
+        float all = part, sum = 0.0f, rest = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kScanThreads / 32; ++w) all = fmaxf(all, s_m[w]);
-        float sum = 0.0f, rest = 0.0f;
+        for (int o = 4; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
+        if (part > -INFINITY) sum = s_s[lane] * exp_neg(part - all);
 #pragma unroll
-        for (int w = 0; w < kScanThreads / 32; ++w)
-            if (s_m[w] > -INFINITY) pair_add(sum, rest, s_s[w] * exp_neg(s_m[w] - all), 0.0f);
-        *out = {all, have, sum, rest};
+        for (int o = 4; o > 0; o >>= 1) pair_add(sum, rest, __shfl_xor_sync(kFull, sum, o), __shfl_xor_sync(kFull, rest, o));
+        if (lane == 0) *out = {all, have, sum, rest};
     }
 }
 
@@ -250,49 +330,42 @@ __device__ __forceinline__ void pair_log(float sh, float sl, float &h, float &l)
     l = __fadd_rn(l, __fmaf_rn(nf, 1.42860682e-6f, 2.0f * __fmaf_rn(t * z, p, t1)));
 }
 
-// a candidate of a group: its score as an f32 pair (hi the rounded sum, lo the rest: 48 bits), both in the order of unsigned integers (hi 0: none); beam, token
-struct Cand {
-    uint32_t hi, lo, beam, token;
-};
-__device__ __forceinline__ Cand make_cand(float cum, float x, float lh, float ll, uint32_t beam, uint32_t token) {
+// a candidate's score cum + x - (lh + ll) as an f32 pair (the rounded sum, the rest: 48 bits) in the order of unsigned integers (0: none)
+__device__ __forceinline__ uint64_t score_key(float cum, float x, float lh, float ll) {
     float d, e, h, l;
     two_sum(x, -lh, d, e);                                      // (|x| and the logarithm may be far apart either way)
     e = __fsub_rn(e, ll);
     two_sum(cum, d, h, l);
-    l = fabsf(h) <= FLT_MAX ? __fadd_rn(l, e) : 0.0f;           // (past f32 there is no rest)
+    const bool fits = fabsf(h) <= FLT_MAX;                      // (past f32 there is no rest)
+    l = fits ? __fadd_rn(l, e) : 0.0f;
     const float s = __fadd_rn(h, l);
-    l = __fsub_rn(l, __fsub_rn(s, h));
-    return {ordered(s + 0.0f), ordered(fabsf(h) <= FLT_MAX ? l + 0.0f : 0.0f), beam, token};
+    l = fits ? __fsub_rn(l, __fsub_rn(s, h)) : 0.0f;
+    return ((uint64_t)ordered(s + 0.0f) << 32) | ordered(l + 0.0f);
 }
-// whether this lane's is the best of the warp's (false everywhere: there is none left)
-__device__ __forceinline__ bool best_of_warp(const Cand &c, bool &none) {
-    const uint32_t hi = __reduce_max_sync(kFull, c.hi);
-    none = hi == 0;
-    bool mine = !none && c.hi == hi;
-    const uint32_t lo = __reduce_max_sync(kFull, mine ? c.lo : 0u);
-    mine = mine && c.lo == lo;
-    if (__popc(__ballot_sync(kFull, mine)) > 1) {           // equal scores: the lowest beam, then the lowest token
-        const uint32_t b = __reduce_min_sync(kFull, mine ? c.beam : 0xffffffffu);
-        mine = mine && c.beam == b;
-        const uint32_t t = __reduce_min_sync(kFull, mine ? c.token : 0xffffffffu);
-        mine = mine && c.token == t;
-    }
-    return mine;
-}
+// where it lies: beam, token (of equal scores the lowest comes first)
+__device__ __forceinline__ uint64_t place(int beam, float token) { return ((uint64_t)(uint32_t)beam << 32) | __float_as_uint(token); }
 
-constexpr int kJoinWarps = 32;
-
-__global__ void __launch_bounds__(kJoinWarps * 32) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
-                                                                    int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
-                                                                    int32_t *next_token) {
-    __shared__ Cand s_list[kJoinWarps][kMaxCand];
-    __shared__ int s_n[kJoinWarps];
+// A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted: a thread
+// per list; lists come in the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a
+// few k as a rule, whose ranks are counted again.
+__global__ void __launch_bounds__(kMaxLists) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
+                                                              int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
+                                                              int32_t *next_token) {
+    extern __shared__ __align__(16) uint64_t s_keys[];      // of the heads [lists, even], then key and place of the entries [2][k * min(k, lists)]
+    __shared__ uint64_t s_final[2][kMaxCand];
+    __shared__ int s_list[kMaxCand], s_n, s_lists;
     __shared__ float s_cum[kMaxCand], s_lh[kMaxCand], s_ll[kMaxCand];
     grid_dep_launch();
     grid_dep_wait();
     const int64_t g = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = ws.pieces;
-    for (int b = warp; b < B; b += kJoinWarps) {            // a warp per row: its sum of exponentials
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, P = ws.pieces, lists = B * P, l = threadIdx.x;
+    const int beam = l < lists ? l / P : 0;
+    const float2 *list = ws.list + g * lists * k;
+    float2 head = make_float2(0.0f, 0.0f);
+    int n = 0;
+    if (l < lists) n = ws.piece[g * lists + l].n, head = list[l * k];   // (not written where n is 0)
+    if (threadIdx.x == 0) s_n = 0, s_lists = 0;
+    for (int b = warp; b < B; b += warps) {                 // a warp per row: its sum of exponentials
         const BeamPiece *piece = ws.piece + (g * B + b) * P;
         float m = -INFINITY;
         for (int i = lane; i < P; i += 32) m = fmaxf(m, piece[i].m);
@@ -307,67 +380,75 @@ __global__ void __launch_bounds__(kJoinWarps * 32) beam_join_kernel(BeamWs ws, i
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pair_add(s, e, __shfl_xor_sync(kFull, s, o), __shfl_xor_sync(kFull, e, o));
         if (lane == 0) {
-            float h = 0.0f, l = 0.0f, a, c;                     // (a row without a value has no candidate)
-            if (s > 0.0f) pair_log(s, e, h, l);
-            two_sum(m > -INFINITY ? m : 0.0f, h, a, c);
-            s_lh[b] = a, s_ll[b] = __fadd_rn(c, l);
+            float h = 0.0f, c = 0.0f, a, d;                 // (a row without a value has no candidate)
+            if (s > 0.0f) pair_log(s, e, h, c);
+            two_sum(m > -INFINITY ? m : 0.0f, h, a, d);
+            s_lh[b] = a, s_ll[b] = __fadd_rn(d, c);
             s_cum[b] = scores[g * B + b];
         }
     }
     __syncthreads();
-    // a list per thread (neighbours of a row in different warps); every warp takes the best k of its lists
-    const int l = lane * kJoinWarps + warp, lists = B * P;
-    const int beam = l < lists ? l / P : 0;
-    const float2 *list = ws.list + (g * lists + (l < lists ? l : 0)) * k;
-    const int n = l < lists ? ws.piece[g * lists + l].n : 0;
-    const float cum = s_cum[beam], lh = s_lh[beam], ll = s_ll[beam];
-    int pos = 0;
-    float2 ahead = n > 1 ? list[1] : make_float2(0.f, 0.f);
-    Cand c = {0, 0, 0, 0};
-    if (n > 0) c = make_cand(cum, list[0].x, lh, ll, beam, __float_as_uint(list[0].y));
-    int got = 0;
-    for (; got < k; ++got) {
-        bool none;
-        const bool mine = best_of_warp(c, none);
-        if (none) break;
-        if (mine) {
-            s_list[warp][got] = c;
-            ++pos;
-            c = {0, 0, 0, 0};
-            if (pos < n) c = make_cand(cum, ahead.x, lh, ll, beam, __float_as_uint(ahead.y));
-            if (pos + 1 < n) ahead = list[pos + 1];
+    const int even = (lists + 1) & ~1;
+    const uint64_t key = n > 0 ? score_key(s_cum[beam], head.x, s_lh[beam], s_ll[beam]) : 0;
+    if (l < even) s_keys[l] = key;
+    __syncthreads();
+    if (n > 0) {
+        int rank = 0;
+        const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(s_keys);
+#pragma unroll 4
+        for (int j = 0; j < even; j += 2) {
+            const ulonglong2 o = two[j / 2];
+            rank += (o.x > key) | ((o.x == key) & (j < l));
+            rank += (o.y > key) | ((o.y == key) & (j + 1 < l));
+        }
+        if (rank < k) s_list[atomicAdd(&s_lists, 1)] = l;
+        if (rank == k - 1) s_final[0][0] = key, s_final[1][0] = place(beam, head.y);
+    }
+    __syncthreads();
+    const int left = s_lists;
+    const uint64_t bar = left == k ? s_final[0][0] : 0, at_bar = left == k ? s_final[1][0] : ~0ull;     // the k-th head, where there are as many
+    uint64_t *keys = s_keys + even, *places = keys + k * min(k, lists);
+    for (int i = warp; i < left; i += warps) {
+        const int from = s_list[i], of = from / P, len = ws.piece[g * lists + from].n;
+        for (int j = lane; j < len; j += 32) {
+            const float2 x = list[from * k + j];
+            const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]), at = place(of, x.y);
+            if (y > bar || (y == bar && at <= at_bar)) {
+                const int c = atomicAdd(&s_n, 1);
+                keys[c] = y, places[c] = at;
+            }
         }
     }
-    if (lane == 0) s_n[warp] = got;
+    __syncthreads();
+    const int all = s_n;
+    for (int i = threadIdx.x; i < all; i += blockDim.x) {
+        const uint64_t y = keys[i], at = places[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < all; ++j) rank += (keys[j] > y) | ((keys[j] == y) & (places[j] < at));
+        if (rank < k) s_final[0][rank] = y, s_final[1][rank] = at;
+    }
     __syncthreads();
     if (warp != 0) return;
-    // the best k of the warps' lists, one lane each
-    const int mine_n = s_n[lane];
-    pos = 0;
-    c = {0, 0, 0, 0};
-    if (mine_n > 0) c = s_list[lane][0];
+    const int got = min(all, k);
     int live = 0;                                           // candidates so far that do not end
-    for (int i = 0; i < k; ++i) {
-        bool none;
-        const bool mine = best_of_warp(c, none);
-        const int who = none ? 0 : __ffs(__ballot_sync(kFull, mine)) - 1;
-        const Cand w = {__shfl_sync(kFull, c.hi, who), __shfl_sync(kFull, c.lo, who), __shfl_sync(kFull, c.beam, who), __shfl_sync(kFull, c.token, who)};
-        const float score = none ? -INFINITY : from_ordered(w.hi);
-        const int row = none ? -1 : (int)(g * B + w.beam), token = none ? -1 : (int)w.token;
-        if (lane == 0) {
+    for (int i = lane; i < k + lane; i += 32) {             // (all lanes as often)
+        const bool in = i < got;
+        const float score = in ? from_ordered((uint32_t)(s_final[0][i] >> 32)) : -INFINITY;
+        const int row = in ? (int)(g * B + (int64_t)(s_final[1][i] >> 32)) : -1, token = in ? (int)(uint32_t)s_final[1][i] : -1;
+        if (i < k) {
             cand_score_out[g * k + i] = score;
             cand_row[g * k + i] = row;
             cand_token[g * k + i] = token;
         }
-        if (!none && token != stop && live < B) {
-            if (lane == 0 && next_row != nullptr) {
-                next_score[g * B + live] = score;
-                next_row[g * B + live] = row;
-                next_token[g * B + live] = token;
-            }
-            ++live;
+        const uint32_t goes = __ballot_sync(kFull, in && token != stop);
+        const int at = live + __popc(goes & ((1u << lane) - 1));
+        if (next_row != nullptr && (goes >> lane & 1) && at < B) {
+            next_score[g * B + at] = score;
+            next_row[g * B + at] = row;
+            next_token[g * B + at] = token;
         }
-        if (mine && !none) c = ++pos < mine_n ? s_list[lane][pos] : Cand{0, 0, 0, 0};
+        live += __popc(goes);
     }
     if (next_row != nullptr)
         for (int i = live + lane; i < B; i += 32) {
@@ -381,8 +462,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) beam_join_kernel(BeamWs ws, i
 void beam_split(int64_t rows, int B, int64_t V, BeamWs *ws) {
     const int64_t all = (V + 7 + kTile - 1) / kTile;        // (a row begins up to seven places past a boundary)
     const int64_t most = kMaxLists / B;                     // lists of a group: one per thread of the join
-    int64_t n = (6 * sm_count() + rows - 1) / rows;
+    int64_t n = 4 * sm_count() / rows;                      // one wave of blocks, four to an SM
     if (n > all) n = all;
+    if (n < 1) n = 1;
     if (n > most) n = most;
     ws->pieces = (int)n;
     ws->length = ((V + 7 + n - 1) / n + 7) / 8 * 8;
@@ -412,9 +494,15 @@ int launch_beam_select(int dtype, const void *logits, int64_t stride, int64_t n_
     cudaError_t e = dtype == MQD_F32   ? launch_pdl(beam_scan_kernel<float>, grid, block, 0, s, static_cast<const float *>(logits), stride, V, scores, k, ws)
                     : dtype == MQD_F16 ? launch_pdl(beam_scan_kernel<__half>, grid, block, 0, s, static_cast<const __half *>(logits), stride, V, scores, k, ws)
                                        : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, block, 0, s, static_cast<const __nv_bfloat16 *>(logits), stride, V, scores, k, ws);
-    if (e == cudaSuccess)
-        e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(kJoinWarps * 32), 0, s, ws, B, scores, k, stop, cand_score, cand_row, cand_token,
-                       next_score, next_row, next_token);
+    // a thread per list, a warp per row, at least eight warps
+    const int lists = B * ws.pieces, threads = lists > 256 || B > 8 ? (lists > 32 * B ? (lists + 31) / 32 * 32 : 32 * B < 1024 ? 32 * B : 1024) : 256;
+    const int entries = (lists + 1) / 2 * 2 + 2 * k * (k < lists ? k : lists);
+    if (e == cudaSuccess) {
+        const int rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (kMaxLists + 2 * kMaxCand * kMaxCand) * 8, kAttrSlotBeam);
+        if (rc != MQ_OK) return rc;
+        e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(threads), entries * 8, s, ws, B, scores, k, stop, cand_score, cand_row,
+                       cand_token, next_score, next_row, next_token);
+    }
     return cuda_error(e, "mqd_beam_select launch");
 }
 
