@@ -16,7 +16,8 @@ namespace mq {
 namespace {
 
 constexpr int kScanThreads = 256, kScanPer = 16, kTile = kScanThreads * kScanPer;    // values of a thread, of a block at a time
-constexpr int kBuffer = 256, kMaxCand = 64, kMaxLists = 1024;
+constexpr int kStages = 3;          // tiles of a block in flight or in work: 48 KB (f32), so that three blocks fit an SM
+constexpr int kBuffer = 256, kPart = 2048, kMaxCand = 64, kMaxLists = 1024, kRoom = kPart + kMaxCand;     // room of a piece's list while it is made
 
 // order of f32 values (no NaN; +-0 are to be made one before) as unsigned integers, and back
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -45,33 +46,43 @@ struct BeamWs {
     int64_t length;     // of a piece, a multiple of 8
 };
 
-// values of the tile at place e0 in registers, -inf where there is none; vectors of 16 bytes from the boundary at or before the row's beginning (bytes of
-// a vector that holds a value of the row lie in that value's 16-byte granule, so no read leaves memory)
+// A tile on its way: every thread copies its own vectors of 16 bytes into its own slots of a stage and waits for its own copies only, so stages need no
+// barriers.  Vectors begin at the boundary at or before the row's beginning, those without a value of the row are left out (bytes of a vector that
+// holds one lie in that value's 16-byte granule, so no read leaves memory).
 template <typename T>
-__device__ __forceinline__ void load_tile(const T *base, int first, int stop, int e0, float (&x)[kScanPer]) {
+__device__ __forceinline__ void ask_tile(const T *base, int first, int stop, int e0, uint4 *stage) {
     constexpr int V = 16 / sizeof(T);
     const T *p = base + e0 + threadIdx.x * V;
-    uint4 w[kScanPer / V];
+    const uint32_t to = smem_u32(stage + threadIdx.x);
     if (e0 >= first && stop - e0 >= kTile) {                // nearly always
 #pragma unroll
-        for (int j = 0; j < kScanPer / V; ++j) w[j] = __ldcs(reinterpret_cast<const uint4 *>(p + j * kScanThreads * V));
+        for (int j = 0; j < kScanPer / V; ++j)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * kScanThreads * 16), "l"(p + j * kScanThreads * V) : "memory");
     } else {
-        const uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 #pragma unroll
         for (int j = 0; j < kScanPer / V; ++j) {
             const int e = e0 + (j * kScanThreads + (int)threadIdx.x) * V;
-            w[j] = make_uint4(none, none, none, none);
-            if (e + V > first && e < stop) w[j] = __ldcs(reinterpret_cast<const uint4 *>(p + j * kScanThreads * V));
+            if (e + V > first && e < stop)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * kScanThreads * 16), "l"(p + j * kScanThreads * V) : "memory");
         }
     }
+}
+__device__ __forceinline__ void ask_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ask_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// its values, -inf where the row has none
+template <typename T>
+__device__ __forceinline__ void read_tile(const uint4 *stage, int first, int stop, int e0, float (&x)[kScanPer]) {
+    constexpr int V = 16 / sizeof(T);
 #pragma unroll
     for (int j = 0; j < kScanPer / V; ++j) {
+        const uint4 w = stage[j * kScanThreads + threadIdx.x];
         if constexpr (V == 4) {
-            x[4 * j] = __uint_as_float(w[j].x), x[4 * j + 1] = __uint_as_float(w[j].y);
-            x[4 * j + 2] = __uint_as_float(w[j].z), x[4 * j + 3] = __uint_as_float(w[j].w);
+            x[4 * j] = __uint_as_float(w.x), x[4 * j + 1] = __uint_as_float(w.y), x[4 * j + 2] = __uint_as_float(w.z), x[4 * j + 3] = __uint_as_float(w.w);
         } else {
             float v[8];
-            unpack8(Raw8<T>{w[j]}, v);
+            unpack8(Raw8<T>{w}, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[8 * j + i] = v[i];
         }
@@ -88,18 +99,17 @@ __device__ __forceinline__ void load_tile(const T *base, int first, int stop, in
 // an entry of a list: value and token in the order of unsigned integers, the larger value first and of equals the lower token
 __device__ __forceinline__ uint64_t entry(float v, int token) { return ((uint64_t)ordered(v + 0.0f) << 32) | ~(uint32_t)token; }
 
-// the best k of the n entries in s_buf, sorted, to its front; returns how many.  A thread counts what is better than its entry: n^2 / 256 steps a thread,
-// for a few dozen entries
+// the best k of the n entries in s_buf, sorted, to s_best and to its front (there for all after the next barrier); returns how many.  A thread counts what is
+// better than its entry: n^2 / 512 steps a thread, for a few dozen entries
 __device__ __forceinline__ int keep_best(uint64_t *s_buf, uint64_t *s_best, int n, int k) {
-    if (threadIdx.x == 0) s_buf[n] = 0;                     // (pairs are read)
-    __syncthreads();
+    const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(s_buf);
+#pragma unroll 1
     for (int i = threadIdx.x; i < n; i += kScanThreads) {
         const uint64_t a = s_buf[i];
-        const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(s_buf);
-        int rank = 0;
+        int rank = (n & 1) ? (int)(s_buf[n - 1] > a) : 0;
 #pragma unroll 4
-        for (int j = 0; j < n; j += 2) {
-            const ulonglong2 b = two[j / 2];
+        for (int j = 0; j < n / 2; ++j) {
+            const ulonglong2 b = two[j];
             rank += (int)(b.x > a) + (int)(b.y > a);
         }
         if (rank < k) s_best[rank] = a;
@@ -107,7 +117,6 @@ __device__ __forceinline__ int keep_best(uint64_t *s_buf, uint64_t *s_best, int 
     __syncthreads();
     n = min(n, k);
     if (threadIdx.x < n) s_buf[threadIdx.x] = s_best[threadIdx.x];
-    __syncthreads();
     return n;
 }
 
@@ -126,13 +135,19 @@ __device__ __forceinline__ float tile_sum(const float (&v)[kScanPer], float m) {
     return a + b;
 }
 
+// the largest f32 below x, which is finite
+__device__ __forceinline__ float below(float x) {
+    const uint32_t u = ordered(x + 0.0f);
+    return from_ordered(u - (u == 0x80000000u ? 2u : 1u));  // (minus zero is not below zero)
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *logits, int64_t stride, int64_t V, const float *scores, int k, BeamWs ws) {
-    constexpr int VEC = 16 / sizeof(T);
-    __shared__ __align__(16) uint64_t s_buf[kTile + kBuffer + 2];
+__global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *logits, int64_t stride, int64_t V, const float *scores, int k, BeamWs ws) {
+    constexpr int VEC = 16 / sizeof(T), kStageVecs = kTile / VEC;
+    extern __shared__ uint4 s_stage[];                      // [kStages][kStageVecs]
+    __shared__ __align__(16) uint64_t s_buf[kRoom + 2];
     __shared__ uint64_t s_best[kMaxCand];
     __shared__ uint32_t s_key[kScanThreads / 32];
-    __shared__ int s_hits[kScanThreads / 32];
     __shared__ uint2 s_bar;
     __shared__ float s_m[kScanThreads / 32], s_s[kScanThreads / 32];
     __shared__ int s_n;
@@ -149,12 +164,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
     const int first = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     const T *base = p - first;
     const int e0 = (int)(piece * ws.length), stop = (int)min(first + V, e0 + ws.length);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (e0 + i * kTile < stop) ask_tile(base, first, stop, e0 + i * kTile, s_stage + i * kStageVecs);
+        ask_done();
+    }
     if (threadIdx.x == 0) s_n = 0;
     float m = -INFINITY, s = 0.0f, thr = -INFINITY;
     int have = 0;
 
-    // token of place i of the tile at `at`
-    auto token = [&](int at, int i) { return at - first + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC; };
     // NaN and +inf as what they count as; the largest
     auto clean = [&](float(&v)[kScanPer]) {
         float top = -INFINITY;
@@ -165,47 +183,51 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
         }
         return top;
     };
-    // values past the bar (those equal to it: up to token `last`) into the list, as far as it has room
-    auto push = [&](const float(&v)[kScanPer], int at, float bar, int last) {
+    // Values past the bar into the list, as far as it has room; their count in any case.  Few pass: a mask of them, then one after the other, its value
+    // again from where it came (of the values that are equal to `tie` those up to token `last` pass too).
+    auto push = [&](const float(&v)[kScanPer], const T *from, int at, float bar, float tie, int last) {
+        const int t0 = at - first + (int)threadIdx.x * VEC;
+        uint32_t mask = 0;
 #pragma unroll
-        for (int j = 0; j < kScanPer; j += 4) {
-            if (!(fmaxf(fmaxf(v[j], v[j + 1]), fmaxf(v[j + 2], v[j + 3])) >= bar)) continue;
+        for (int i = 0; i < kScanPer; ++i) mask |= (uint32_t)(v[i] > bar) << i;
+        if (last != INT32_MIN) {
 #pragma unroll
-            for (int i = j; i < j + 4; ++i)
-                if ((v[i] > bar) | ((v[i] == bar) & (token(at, i) <= last) & (v[i] > -INFINITY))) {
-                    const int n = atomicAdd(&s_n, 1);
-                    if (n < kTile + kBuffer) s_buf[n] = entry(v[i], token(at, i));
-                }
+            for (int i = 0; i < kScanPer; ++i)
+                mask |= (uint32_t)((v[i] == tie) & (t0 + i / VEC * (kScanThreads * VEC) + i % VEC <= last)) << i;
+        }
+        if (mask == 0) return;
+        int n = atomicAdd(&s_n, __popc(mask));
+#pragma unroll 1
+        for (; mask != 0; mask &= mask - 1, ++n) {
+            const int i = __ffs(mask) - 1, e = i / VEC * (kScanThreads * VEC) + i % VEC;
+            if (n < kRoom) s_buf[n] = entry(fminf(to_f32(from[(int)threadIdx.x * VEC + e]), FLT_MAX), t0 + e);
         }
     };
-    // (all threads, after a barrier) entries in the list; nobody adds to it before all know
-    auto count = [&]() {
-        const int n = s_n;
-        __syncthreads();
-        return n;
-    };
-    // (all threads) the best k of the n entries stay; what does not pass their last one is out
+    // (all threads, after a barrier) the best k of the list's n entries stay; what does not pass their last one is out
     auto settle = [&](int n) {
         if (n > have) {
             have = keep_best(s_buf, s_best, n, k);
             if (threadIdx.x == 0) s_n = have;
-            if (have == k) thr = from_ordered((uint32_t)(s_buf[k - 1] >> 32));
-            __syncthreads();
+            if (have == k) thr = from_ordered((uint32_t)(s_best[k - 1] >> 32));
         }
+        __syncthreads();                                    // nobody adds to the list before all know its count
     };
 
-    float x[kScanPer];
-    load_tile(base, first, stop, e0, x);
-    int span = e0, tiles = 1;                               // the list is settled after 1, 2, 4, 8 .. tiles
+    int span = e0, tiles = 1, slot = 0;                     // the list is settled after 1, 2, 4, 8 .. tiles
 #pragma unroll 1
     for (int at = e0; at < stop; at += kTile) {
-        float v[kScanPer], top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kScanPer; ++i) {
-            v[i] = x[i];
-            top = fmaxf(top, v[i]);                         // (NaN aside)
+        {
+            const int next = at + (kStages - 1) * kTile, into = slot == 0 ? kStages - 1 : slot - 1;     // (the stage that was read last)
+            if (next < stop) ask_tile(base, first, stop, next, s_stage + into * kStageVecs);
+            ask_done();
+            ask_wait<kStages - 1>();
         }
-        if (at + kTile < stop) load_tile(base, first, stop, at + kTile, x);
+        float v[kScanPer], top = -INFINITY;
+        const uint4 *tile = s_stage + slot * kStageVecs;
+        read_tile<T>(tile, first, stop, at, v);
+        slot = slot == kStages - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i) top = fmaxf(top, v[i]);                                      // (NaN aside)
         float sum = tile_sum(v, fmaxf(top, m));
         if (!(sum <= FLT_MAX)) {                            // a NaN or +inf, or nothing yet but -inf
             top = clean(v);
@@ -216,7 +238,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
             m = top;
         }
         s += sum;
-        if (at == e0) {
+        float bar = thr, tie = 0.0f;                        // (of equals the first, which the list holds)
+        int last = INT32_MIN;
+        const bool begin = at == e0;
+        if (begin) {
             // every warp's ceil(k / 8)-th largest of its threads' largest values: at least k values are not below the least of these
             const uint32_t own = top > -INFINITY ? ordered(top + 0.0f) : 0u;
             uint32_t key = own, best = 0;
@@ -229,25 +254,17 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
             uint32_t least = s_key[0];
 #pragma unroll
             for (int w = 1; w < kScanThreads / 32; ++w) least = min(least, s_key[w]);
-            float bar = least != 0 ? from_ordered(least) : -INFINITY;
-            int last = INT32_MAX, hits = 0;
-            if (top >= bar) {
+            bar = least != 0 ? below(from_ordered(least)) : -INFINITY;
+            int hits = 0;
 #pragma unroll
-                for (int i = 0; i < kScanPer; ++i) hits += v[i] >= bar;
-            }
-            hits = __reduce_add_sync(kFull, hits);
-            if (lane == 0) s_hits[warp] = hits;
-            __syncthreads();
-            hits = 0;
-#pragma unroll
-            for (int w = 0; w < kScanThreads / 32; ++w) hits += s_hits[w];
-            if (hits > kBuffer) {
-                // a warp has too few values (the end of a row, a mask) or many are equal: the k-th of all threads' largest, by value and token
+            for (int i = 0; i < kScanPer; ++i) hits += v[i] > bar;
+            // a warp has too few values (the end of a row, a mask) or many are equal: the k-th of all threads' largest, by value and token
+            if (__syncthreads_or(__reduce_add_sync(kFull, hits) > kBuffer / (kScanThreads / 32))) {
                 uint2 *s_all = reinterpret_cast<uint2 *>(s_buf);
                 int at_top = INT32_MAX;
 #pragma unroll
                 for (int i = kScanPer - 1; i >= 0; --i)
-                    if (v[i] == top) at_top = token(at, i);
+                    if (v[i] == top) at_top = at - first + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
                 s_all[threadIdx.x] = make_uint2(own, (uint32_t)at_top);
                 __syncthreads();
                 int rank = 0;
@@ -258,35 +275,39 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const T *log
                 }
                 const bool kth = own != 0 && rank == k - 1;
                 if (kth) s_bar = make_uint2(own, (uint32_t)at_top);
-                if (__syncthreads_or(kth)) bar = from_ordered(s_bar.x), last = (int)s_bar.y;
+                if (__syncthreads_or(kth)) bar = tie = from_ordered(s_bar.x), last = (int)s_bar.y;
             }
-            if (top >= bar) push(v, at, bar, last);
-            __syncthreads();
-            settle(count());
-            span = at + kTile;
-            continue;
         }
-        if (top > thr) push(v, at, thr, INT32_MIN);         // (of equals the first, which the list holds)
-        if (at + kTile - span < tiles * kTile && at + kTile < stop) continue;
+        if (top > bar || last != INT32_MIN) push(v, reinterpret_cast<const T *>(tile), at, bar, tie, last);
+        if (!begin && at + kTile - span < tiles * kTile && at + kTile < stop) continue;
         __syncthreads();
-        const int n = count();
-        if (n > kTile + kBuffer) {
-            // more than the list has room for: the span again, tile by tile
+        const int n = s_n;
+        if (n > kRoom) {
+            // more than the list has room for: the span again, one vector of each thread at a time
+            __syncthreads();
             if (threadIdx.x == 0) s_n = have;
-            for (int again = span; again <= at; again += kTile) {
-                __syncthreads();
-                load_tile(base, first, stop, again, v);
-                if (clean(v) > thr) push(v, again, thr, INT32_MIN);
-                __syncthreads();
-                settle(count());
-            }
+#pragma unroll 1
+            for (int again = span; again <= at; again += kTile)
+#pragma unroll 1
+                for (int part = 0; part < kTile / kPart; ++part) {
+                    __syncthreads();
+                    float z[kScanPer];
+#pragma unroll
+                    for (int i = 0; i < kScanPer; ++i) {
+                        const int e = again + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
+                        z[i] = e >= first && e < stop && i / (kPart / kScanThreads) == part ? to_f32(base[e]) : -INFINITY;
+                    }
+                    if (clean(z) > thr) push(z, base + again, again, thr, 0.0f, INT32_MIN);
+                    __syncthreads();
+                    settle(s_n);
+                }
         } else {
             settle(n);
         }
         span = at + kTile;
-        tiles = min(2 * tiles, 1 << 16);
+        if (!begin) tiles = min(2 * tiles, 1 << 16);
     }
-    for (int i = threadIdx.x; i < have; i += kScanThreads) 
+    for (int i = threadIdx.x; i < have; i += kScanThreads)
         ws.list[(int64_t)blockIdx.x * k + i] = make_float2(from_ordered((uint32_t)(s_buf[i] >> 32)), __uint_as_float(~(uint32_t)s_buf[i]));
     float top = m;
 #pragma unroll
@@ -342,91 +363,135 @@ __device__ __forceinline__ uint64_t score_key(float cum, float x, float lh, floa
     l = fits ? __fsub_rn(l, __fsub_rn(s, h)) : 0.0f;
     return ((uint64_t)ordered(s + 0.0f) << 32) | ordered(l + 0.0f);
 }
-// where it lies: beam, token (of equal scores the lowest comes first)
-__device__ __forceinline__ uint64_t place(int beam, float token) { return ((uint64_t)(uint32_t)beam << 32) | __float_as_uint(token); }
+// How many of the n (a multiple of 4) numbers are larger than this one (EQUAL: or the same).  Four lanes share the count; all of them get it.
+template <bool EQUAL>
+__device__ __forceinline__ int rank_of(const uint32_t *his, int n, uint32_t hi) {
+    const uint4 *four = reinterpret_cast<const uint4 *>(his);
+    const uint32_t x = EQUAL ? hi - 1 : hi;                 // (hi > 0)
+    int rank = 0;
+#pragma unroll 4
+    for (int j = threadIdx.x & 3; j < n / 4; j += 4) {
+        const uint4 o = four[j];
+        rank += (int)(o.x > x) + (int)(o.y > x) + (int)(o.z > x) + (int)(o.w > x);
+    }
+    rank += __shfl_xor_sync(kFull, rank, 1);
+    return rank + __shfl_xor_sync(kFull, rank, 2);
+}
+// The rank of item i among n by upper halves, where it is below k; items that look the same: by lower halves and place, lies_before(j, i).  All four lanes of an
+// item, all lanes of a warp.
+template <typename Before>
+__device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *los, int n, int n4, int i, int k, Before lies_before) {
+    const uint32_t hi = his[i];
+    int rank = rank_of<false>(his, n4, hi);
+    const bool in = hi != 0 && rank < k;
+    if (!__any_sync(kFull, in)) return k;
+    const int same = rank_of<true>(his, n4, max(hi, 1u));
+    if (__any_sync(kFull, in && same > rank + 1)) {
+        int more = 0;
+        for (int j = threadIdx.x & 3; j < n; j += 4)
+            more += (int)((his[j] == hi) & ((los[j] > los[i]) | ((los[j] == los[i]) & lies_before(j, i))));
+        more += __shfl_xor_sync(kFull, more, 1);
+        rank += more + __shfl_xor_sync(kFull, more, 2);
+    }
+    return in ? rank : k;
+}
 
-// A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted: a thread
-// per list; lists come in the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a
-// few k as a rule, whose ranks are counted again.
-__global__ void __launch_bounds__(kMaxLists) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
-                                                              int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
-                                                              int32_t *next_token) {
-    extern __shared__ __align__(16) uint64_t s_keys[];      // of the heads [lists, even], then key and place of the entries [2][k * min(k, lists)]
-    __shared__ uint64_t s_final[2][kMaxCand];
-    __shared__ int s_list[kMaxCand], s_n, s_lists;
+// A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted; lists come in
+// the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a few k as a rule, whose
+// ranks are counted again.  (Taking the best of all heads k times cost 300 clocks each.)
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
+                                                                 int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
+                                                                 int32_t *next_token) {
+    // of the heads, then of the entries (k * min(k, lists) of them): the upper halves of the keys, to compare, padded with zeros; the lower halves; the entries' places
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    __shared__ uint32_t s_bar[3];
+    __shared__ float s_score[kMaxCand];
+    __shared__ int s_row[kMaxCand], s_token[kMaxCand], s_list[kMaxCand], s_n, s_lists;
     __shared__ float s_cum[kMaxCand], s_lh[kMaxCand], s_ll[kMaxCand];
+    __shared__ int s_len[kMaxLists];
     grid_dep_launch();
     grid_dep_wait();
     const int64_t g = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, P = ws.pieces, lists = B * P, l = threadIdx.x;
-    const int beam = l < lists ? l / P : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P, l = threadIdx.x;
     const float2 *list = ws.list + g * lists * k;
     float2 head = make_float2(0.0f, 0.0f);
-    int n = 0;
-    if (l < lists) n = ws.piece[g * lists + l].n, head = list[l * k];   // (not written where n is 0)
+    if (l < lists) s_len[l] = ws.piece[g * lists + l].n, head = list[l * k];    // (not written where there is none)
     if (threadIdx.x == 0) s_n = 0, s_lists = 0;
     for (int b = warp; b < B; b += warps) {                 // a warp per row: its sum of exponentials
-        const BeamPiece *piece = ws.piece + (g * B + b) * P;
-        float m = -INFINITY;
-        for (int i = lane; i < P; i += 32) m = fmaxf(m, piece[i].m);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        float s = 0.0f, e = 0.0f;
-        for (int i = lane; i < P; i += 32)
-            if (piece[i].m > -INFINITY) {
-                const float f = exp_neg(piece[i].m - m), p = __fmul_rn(piece[i].s, f);
-                pair_add(s, e, p, __fmaf_rn(piece[i].s, f, -p) + piece[i].e * f);
+        const float4 *piece = reinterpret_cast<const float4 *>(ws.piece + (g * B + b) * P);
+        float m = -INFINITY, s = 0.0f, e = 0.0f;
+        for (int i = lane; i < P; i += 32) {
+            const float4 o = piece[i];                      // m, n, s, e
+            if (!(o.x > -INFINITY)) continue;
+            if (o.x > m) {
+                const float f = exp_neg(m - o.x);           // (m = -inf: zero)
+                s *= f, e *= f, m = o.x;
             }
+            const float f = exp_neg(o.x - m), p = __fmul_rn(o.z, f);
+            pair_add(s, e, p, __fmaf_rn(o.z, f, -p) + o.w * f);
+        }
+        float all = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
+        if (m > -INFINITY) {
+            const float f = exp_neg(m - all), p = __fmul_rn(s, f);
+            e = __fmaf_rn(s, f, -p) + e * f, s = p;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pair_add(s, e, __shfl_xor_sync(kFull, s, o), __shfl_xor_sync(kFull, e, o));
         if (lane == 0) {
             float h = 0.0f, c = 0.0f, a, d;                 // (a row without a value has no candidate)
             if (s > 0.0f) pair_log(s, e, h, c);
-            two_sum(m > -INFINITY ? m : 0.0f, h, a, d);
+            two_sum(all > -INFINITY ? all : 0.0f, h, a, d);
             s_lh[b] = a, s_ll[b] = __fadd_rn(d, c);
             s_cum[b] = scores[g * B + b];
         }
     }
     __syncthreads();
-    const int even = (lists + 1) & ~1;
-    const uint64_t key = n > 0 ? score_key(s_cum[beam], head.x, s_lh[beam], s_ll[beam]) : 0;
-    if (l < even) s_keys[l] = key;
-    __syncthreads();
-    if (n > 0) {
-        int rank = 0;
-        const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(s_keys);
-#pragma unroll 4
-        for (int j = 0; j < even; j += 2) {
-            const ulonglong2 o = two[j / 2];
-            rank += (o.x > key) | ((o.x == key) & (j < l));
-            rank += (o.y > key) | ((o.y == key) & (j + 1 < l));
-        }
-        if (rank < k) s_list[atomicAdd(&s_lists, 1)] = l;
-        if (rank == k - 1) s_final[0][0] = key, s_final[1][0] = place(beam, head.y);
+    const int n4 = (lists + 3) & ~3;
+    uint32_t *his = s_keys, *los = his + n4;
+    if (l < n4) {
+        const int of = l < lists ? l / P : 0;
+        const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head.x, s_lh[of], s_ll[of]) : 0;
+        his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
     }
     __syncthreads();
-    const int left = s_lists;
-    const uint64_t bar = left == k ? s_final[0][0] : 0, at_bar = left == k ? s_final[1][0] : ~0ull;     // the k-th head, where there are as many
-    uint64_t *keys = s_keys + even, *places = keys + k * min(k, lists);
+    for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
+        const int at = min(i, n4 - 1);
+        const int rank = rank_below(his, los, n4, n4, at, k, [](int a, int b) { return a < b; });
+        if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
+        s_list[atomicAdd(&s_lists, 1)] = i;
+        if (rank == k - 1) s_bar[0] = his[i], s_bar[1] = los[i], s_bar[2] = (uint32_t)i;
+    }
+    __syncthreads();
+    const int left = s_lists, room = (k * min(k, lists) + 4) & ~3;
+    // the k-th head, where there are as many
+    const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
+    const int at_bar = left == k ? (int)s_bar[2] : lists;
+    uint32_t *ehi = los + n4, *elo = ehi + room, *etoken = elo + room, *ebeam = etoken + room;
     for (int i = warp; i < left; i += warps) {
-        const int from = s_list[i], of = from / P, len = ws.piece[g * lists + from].n;
-        for (int j = lane; j < len; j += 32) {
+        const int from = s_list[i], of = from / P;
+        for (int j = lane; j < s_len[from]; j += 32) {
             const float2 x = list[from * k + j];
-            const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]), at = place(of, x.y);
-            if (y > bar || (y == bar && at <= at_bar)) {
+            const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]);
+            // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
+            if ((y > bar) | ((y == bar) & (from <= at_bar))) {
                 const int c = atomicAdd(&s_n, 1);
-                keys[c] = y, places[c] = at;
+                ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), ebeam[c] = of;
             }
         }
     }
     __syncthreads();
-    const int all = s_n;
-    for (int i = threadIdx.x; i < all; i += blockDim.x) {
-        const uint64_t y = keys[i], at = places[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < all; ++j) rank += (keys[j] > y) | ((keys[j] == y) & (places[j] < at));
-        if (rank < k) s_final[0][rank] = y, s_final[1][rank] = at;
+    const int all = s_n, all4 = (all + 3) & ~3;
+    if (threadIdx.x < all4 - all) ehi[all + threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x >> 2; i < (all4 + 7 & ~7); i += kJoinThreads / 4) {
+        const int at = min(i, all4 - 1);
+        const int rank = rank_below(ehi, elo, all, all4, at, k, [&](int a, int b) {
+            return (ebeam[a] < ebeam[b]) | ((ebeam[a] == ebeam[b]) & (etoken[a] < etoken[b]));
+        });
+        if (i < all && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = ebeam[i], s_token[rank] = (int)etoken[i];
     }
     __syncthreads();
     if (warp != 0) return;
@@ -434,8 +499,8 @@ __global__ void __launch_bounds__(kMaxLists) beam_join_kernel(BeamWs ws, int B, 
     int live = 0;                                           // candidates so far that do not end
     for (int i = lane; i < k + lane; i += 32) {             // (all lanes as often)
         const bool in = i < got;
-        const float score = in ? from_ordered((uint32_t)(s_final[0][i] >> 32)) : -INFINITY;
-        const int row = in ? (int)(g * B + (int64_t)(s_final[1][i] >> 32)) : -1, token = in ? (int)(uint32_t)s_final[1][i] : -1;
+        const float score = in ? s_score[i] : -INFINITY;
+        const int row = in ? (int)(g * B) + s_row[i] : -1, token = in ? s_token[i] : -1;
         if (i < k) {
             cand_score_out[g * k + i] = score;
             cand_row[g * k + i] = row;
@@ -462,12 +527,21 @@ __global__ void __launch_bounds__(kMaxLists) beam_join_kernel(BeamWs ws, int B, 
 void beam_split(int64_t rows, int B, int64_t V, BeamWs *ws) {
     const int64_t all = (V + 7 + kTile - 1) / kTile;        // (a row begins up to seven places past a boundary)
     const int64_t most = kMaxLists / B;                     // lists of a group: one per thread of the join
-    int64_t n = 4 * sm_count() / rows;                      // one wave of blocks, four to an SM
+    int64_t n = 3 * sm_count() / rows;                      // one wave of blocks, three to an SM
     if (n > all) n = all;
     if (n < 1) n = 1;
     if (n > most) n = most;
     ws->pieces = (int)n;
     ws->length = ((V + 7 + n - 1) / n + 7) / 8 * 8;
+}
+
+template <typename T>
+int launch_scan(const void *logits, int64_t stride, int64_t V, const float *scores, int k, const BeamWs &ws, int64_t blocks, int slot, cudaStream_t s) {
+    constexpr int stages = kStages * kTile * (int)sizeof(T);
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_scan_kernel<T>), stages, slot);
+    if (rc != MQ_OK) return rc;
+    return cuda_error(launch_pdl(beam_scan_kernel<T>, dim3((unsigned)blocks), dim3(kScanThreads), stages, s, static_cast<const T *>(logits), stride, V, scores, k, ws),
+                      "mqd_beam_select launch");
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -490,19 +564,15 @@ int launch_beam_select(int dtype, const void *logits, int64_t stride, int64_t n_
     if (n > INT32_MAX) return set_error(MQ_ERR_SHAPE, "mqd_beam_select: %lld pieces of rows, below 2^31 wanted (fewer groups a call)", (long long)n);
     ws.piece = static_cast<BeamPiece *>(workspace);
     ws.list = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + round256((size_t)n * sizeof(BeamPiece)));
-    const dim3 grid((unsigned)n), block(kScanThreads);
-    cudaError_t e = dtype == MQD_F32   ? launch_pdl(beam_scan_kernel<float>, grid, block, 0, s, static_cast<const float *>(logits), stride, V, scores, k, ws)
-                    : dtype == MQD_F16 ? launch_pdl(beam_scan_kernel<__half>, grid, block, 0, s, static_cast<const __half *>(logits), stride, V, scores, k, ws)
-                                       : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, block, 0, s, static_cast<const __nv_bfloat16 *>(logits), stride, V, scores, k, ws);
-    // a thread per list, a warp per row, at least eight warps
-    const int lists = B * ws.pieces, threads = lists > 256 || B > 8 ? (lists > 32 * B ? (lists + 31) / 32 * 32 : 32 * B < 1024 ? 32 * B : 1024) : 256;
-    const int entries = (lists + 1) / 2 * 2 + 2 * k * (k < lists ? k : lists);
-    if (e == cudaSuccess) {
-        const int rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (kMaxLists + 2 * kMaxCand * kMaxCand) * 8, kAttrSlotBeam);
-        if (rc != MQ_OK) return rc;
-        e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(threads), entries * 8, s, ws, B, scores, k, stop, cand_score, cand_row,
-                       cand_token, next_score, next_row, next_token);
-    }
+    int rc = dtype == MQD_F32   ? launch_scan<float>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam, s)
+             : dtype == MQD_F16 ? launch_scan<__half>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 1, s)
+                                : launch_scan<__nv_bfloat16>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 2, s);
+    if (rc != MQ_OK) return rc;
+    const int lists = B * ws.pieces, words = 2 * (lists + 3) + 4 * (k * (k < lists ? k : lists) + 4);
+    rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (2 * (kMaxLists + 3) + 4 * (kMaxCand * kMaxCand + 4)) * 4, kAttrSlotBeam + 3);
+    if (rc != MQ_OK) return rc;
+    const cudaError_t e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(kJoinThreads), words * 4, s, ws, B, scores, k, stop, cand_score, cand_row,
+                                     cand_token, next_score, next_row, next_token);
     return cuda_error(e, "mqd_beam_select launch");
 }
 
