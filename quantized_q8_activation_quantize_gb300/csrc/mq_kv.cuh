@@ -55,6 +55,22 @@ struct KvRows {
     }
 };
 
+// the last sequence whose rows begin at or before row t (cu not falling): 32 ends at a time, one a lane
+__device__ __forceinline__ int kv_find_seq(const KvRows &rows, int n_seqs, int64_t t, int step_per_seq, int shift) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = n_seqs;                                   // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int stride = (n + 31) / 32, at = min(lane * stride, n - 1);
+        const int64_t begin = (rows.begin(lo + at) >> shift) + (int64_t)step_per_seq * (lo + at);
+        const uint32_t yes = __ballot_sync(0xffffffffu, lane == 0 || begin <= t);
+        // lanes past the end repeat the last sequence: the highest lane that says yes names its stride's beginning
+        const int k = 31 - __clz(yes), from = min(k * stride, n - 1);
+        lo += from;
+        n = min(stride, n - from);
+    }
+    return lo;
+}
+
 // pairs of f32 in one register pair: half the issue slots
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
     uint64_t r;

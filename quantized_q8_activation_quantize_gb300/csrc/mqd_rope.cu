@@ -5,13 +5,13 @@ namespace mq {
 namespace {
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopePlan plan, RopeRows r, const int32_t *__restrict__ pos) {
-    __shared__ float2 s_cs[kRopePairs];
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopePlan plan, RopeRows r, const int32_t *__restrict__ pos) {
+    __shared__ __align__(16) float s_cos[kRopePairs], s_sin[kRopePairs];
     grid_dep_launch();
     grid_dep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * r.per_block;
-    rope_block<T, W>(plan, r, t0, (int)min((int64_t)r.per_block, r.n_tokens - t0), s_cs, [&](int64_t t) { return pos[t]; },
-                     [](int64_t) { return 1; }, false);
+    rope_block<T, W>(plan, r, t0, (int)min((int64_t)r.per_block, r.n_tokens - t0), s_cos, s_sin, [&](int t) { return pos[t0 + t]; },
+                     [](int) { return 1; }, false);
 }
 
 }  // namespace

@@ -62,40 +62,69 @@ __device__ __forceinline__ void store_w(T *p, const float (&x)[W]) {
     else store8(p, pack8(x, T()));
 }
 
+// two neighbouring pairs of different halves, u = (u0, u1) and v = (v0, v1), as rope_turn on each: c = (c0, c1), s = (s0, s1)
+__device__ __forceinline__ void rope_turn2(uint64_t c, uint64_t s, uint64_t minus_s, uint64_t &u, uint64_t &v) {
+    const uint64_t a = f2_fma(u, c, f2_mul(v, minus_s)), b = f2_fma(v, c, f2_mul(u, s));
+    u = a, v = b;
+}
+// two neighbouring values of one pair, x = (u, v): (u c - v s, v c + u s)
+__device__ __forceinline__ uint64_t rope_turn_pair(float c, float s, uint64_t x) {
+    float u, v;
+    f2_unpack(x, u, v);
+    return f2_fma(x, f2_pack(c, c), f2_mul(f2_pack(v, u), f2_pack(-s, s)));
+}
+
 // Tokens [t0, t0 + n) by the block's threads: their (cos, sin) once for all heads, then a thread turns W pairs at a time, in pieces of 16 bytes (W = 4
-// of 16 bits: 8), two neighbouring ones (interleaved) or two that lie half the rotated part apart.  pos(t): token t's position; live(t): 1, 0 (its
-// row stays as it is) or 2 (its row becomes zeros; `zeros`: whether there is one).  s_cs: n * half pairs.
+// of 16 bits: 8), two neighbouring ones (interleaved) or two that lie half the rotated part apart.  pos(t): position of token t0 + t; live(t): 1, 0 (its
+// row stays as it is) or 2 (its row becomes zeros; `zeros`: whether there is one).  s_cos, s_sin: n * half each.
 template <typename T, int W, typename Pos, typename Live>
-__device__ __forceinline__ void rope_block(const RopePlan &plan, const RopeRows &r, int64_t t0, int n, float2 *s_cs, Pos pos, Live live, bool zeros) {
+__device__ __forceinline__ void rope_block(const RopePlan &plan, const RopeRows &r, int64_t t0, int n, float *s_cos, float *s_sin, Pos pos, Live live, bool zeros) {
     for (int i = threadIdx.x; i < n * plan.half; i += kRopeThreads) {
         const int t = i / plan.half;
-        s_cs[i] = rope_cos_sin(pos(t0 + t), plan.turns[i - t * plan.half], plan.amplitude);
+        const float2 cs = rope_cos_sin(pos(t), plan.turns[i - t * plan.half], plan.amplitude);
+        s_cos[i] = cs.x, s_sin[i] = cs.y;
     }
     __syncthreads();
     const bool copy = r.x != r.out || zeros;
     const int pairs = plan.half / W, per = pairs + (copy ? (r.dim - 2 * plan.half) / W : 0);     // pieces of a head
-    const int all = n * r.heads * per;
-    for (int i = threadIdx.x; i < all; i += kRopeThreads) {
-        const int row = i / per, j = i - row * per, t = row / r.heads, h = row - t * r.heads;
-        const T *x = static_cast<const T *>(r.x) + (t0 + t) * r.xt + h * r.xh;
-        T *out = static_cast<T *>(r.out) + (t0 + t) * r.ot + h * r.oh;
-        const int what = live(t0 + t);
-        if (what == 0) continue;
-        if (j < pairs) {
+    // piece j of head h of token t; the next of this thread is kRopeThreads pieces on
+    int j = threadIdx.x % per, h = threadIdx.x / per, t = h / r.heads;
+    h -= t * r.heads;
+    const int dj = kRopeThreads % per, dr = kRopeThreads / per, dt = dr / r.heads, dh = dr - dt * r.heads;
+    const T *x0 = static_cast<const T *>(r.x) + t0 * r.xt;
+    T *out0 = static_cast<T *>(r.out) + t0 * r.ot;
+#pragma unroll 1
+    while (t < n) {
+        const T *x = x0 + t * r.xt + h * r.xh;
+        T *out = out0 + t * r.ot + h * r.oh;
+        const int what = live(t);
+        if (what != 0 && j < pairs) {
             const int a = plan.interleaved ? 2 * j * W : j * W, b = plan.interleaved ? a + W : a + plan.half;
-            float u[W], v[W];
-            unpack_w<T, W>(*reinterpret_cast<const RawW<T, W> *>(x + a), u);
-            unpack_w<T, W>(*reinterpret_cast<const RawW<T, W> *>(x + b), v);
-            const float2 *cs = s_cs + t * plan.half + j * W;
+            const RawW<T, W> ra = *reinterpret_cast<const RawW<T, W> *>(x + a), rb = *reinterpret_cast<const RawW<T, W> *>(x + b);
+            float u[W], v[W], c[W], s[W];
+            const float4 *cs = reinterpret_cast<const float4 *>(s_cos + t * plan.half + j * W), *ss = reinterpret_cast<const float4 *>(s_sin + t * plan.half + j * W);
+#pragma unroll
+            for (int e = 0; e < W; e += 4) {
+                const float4 y = cs[e / 4], z = ss[e / 4];
+                c[e] = y.x, c[e + 1] = y.y, c[e + 2] = y.z, c[e + 3] = y.w;
+                s[e] = z.x, s[e + 1] = z.y, s[e + 2] = z.z, s[e + 3] = z.w;
+            }
+            unpack_w<T, W>(ra, u);
+            unpack_w<T, W>(rb, v);
             if (plan.interleaved) {
 #pragma unroll
                 for (int e = 0; e < W / 2; ++e) {
-                    rope_turn(cs[e], u[2 * e], u[2 * e + 1]);
-                    rope_turn(cs[W / 2 + e], v[2 * e], v[2 * e + 1]);
+                    f2_unpack(rope_turn_pair(c[e], s[e], f2_pack(u[2 * e], u[2 * e + 1])), u[2 * e], u[2 * e + 1]);
+                    f2_unpack(rope_turn_pair(c[W / 2 + e], s[W / 2 + e], f2_pack(v[2 * e], v[2 * e + 1])), v[2 * e], v[2 * e + 1]);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < W; ++e) rope_turn(cs[e], u[e], v[e]);
+                for (int e = 0; e < W; e += 2) {
+                    uint64_t y = f2_pack(u[e], u[e + 1]), z = f2_pack(v[e], v[e + 1]);
+                    rope_turn2(f2_pack(c[e], c[e + 1]), f2_pack(s[e], s[e + 1]), f2_pack(-s[e], -s[e + 1]), y, z);
+                    f2_unpack(y, u[e], u[e + 1]);
+                    f2_unpack(z, v[e], v[e + 1]);
+                }
             }
             if (what == 2) {
 #pragma unroll
@@ -103,12 +132,15 @@ __device__ __forceinline__ void rope_block(const RopePlan &plan, const RopeRows 
             }
             store_w<T, W>(out + a, u);
             store_w<T, W>(out + b, v);
-        } else {
+        } else if (what != 0) {
             const int a = 2 * plan.half + (j - pairs) * W;
             RawW<T, W> w = *reinterpret_cast<const RawW<T, W> *>(x + a);
             if (what == 2) w.w = {};
             *reinterpret_cast<RawW<T, W> *>(out + a) = w;
         }
+        j += dj, h += dh, t += dt;
+        if (j >= per) j -= per, ++h;
+        if (h >= r.heads) h -= r.heads, ++t;
     }
 }
 
