@@ -178,7 +178,7 @@ MQ_API int mqkv_fork(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32
  * at once, so that parent is any map of the rows (a step of beam search: mqd_beam_select's next_row).  Rows that continue the same sequence share its full
  * pages; of a partly filled last page the lowest such row keeps the page and the others get copies of its used blocks.  Pages that nobody continues are
  * free, and are taken for the copies at once.  All or nothing: with too few free pages, a bad entry of parent, a bad length or table entry no
- * row changes (MQKV_ERR_STATE).  At most 32768 sequences. */
+ * row changes (MQKV_ERR_STATE).  At most 4096 sequences. */
 MQ_API int mqkv_reorder(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *parent, void *workspace, size_t workspace_bytes,
                         mq_stream_t stream);
 

@@ -221,6 +221,7 @@ int kv_launch_extend(const KvPages &p, const int32_t *add, void *ws, unsigned in
 int kv_launch_release(const KvPages &p, const int32_t *ids, int n, unsigned int *err, cudaStream_t s);
 int kv_launch_fork(const KvPages &p, const int32_t *parent, const int32_t *child, int n, void *ws, unsigned int *err,
                    cudaStream_t s);
+constexpr int kKvReorderRows = 4096;        // rows that a reordering may have
 int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigned int *err, cudaStream_t s);
 int kv_launch_compact(const KvPages &p, void *ws, unsigned int *err, cudaStream_t s);
 int kv_launch_copy(const KvPages &p, const int32_t *src, const int32_t *dst, int n, unsigned int *err, cudaStream_t s);

@@ -389,7 +389,7 @@ int mqkv_reorder(const mqkv_cache *cache, const mqkv_seqs *seqs, const int32_t *
     mqkv_layout lay;
     KV_TRY(check_cache(fn, cache, &lay, true));
     KV_TRY(check_seqs(fn, seqs));
-    if (seqs->n_seqs > 32768) return set_error(MQ_ERR_SHAPE, "%s: n_seqs=%d above 32768", fn, seqs->n_seqs);
+    if (seqs->n_seqs > kKvReorderRows) return set_error(MQ_ERR_SHAPE, "%s: n_seqs=%d above %d", fn, seqs->n_seqs, kKvReorderRows);
     if (seqs->n_seqs == 0) return MQ_OK;
     if (parent == nullptr) return set_error(MQ_ERR_ARG, "%s: NULL parent", fn);
     if (!aligned(parent, 4)) return set_error(MQ_ERR_ALIGN, "%s: parent %p not 4-byte aligned", fn, (const void *)parent);

@@ -306,17 +306,21 @@ __device__ __forceinline__ void remap_row(const KvPages &p, const Ws &ws, int b,
 }
 
 // ---------------------------------------------------------------- reorder ---
-// Row b becomes what row parent[b] was.  One cluster of blocks does the bookkeeping (its barriers order the phases: checks, reference counts, pages
-// for the copies, the table), a second kernel copies the used blocks of the last pages that two rows would share.
+// Row b becomes what row parent[b] was.  A block, or for large tables a cluster of them, does the bookkeeping; a second kernel copies the used blocks of the last
+// pages that two rows would share.  A plan of a few thousand integers is all latency: parents, lengths and the table are read once into shared memory
+// and every phase works on them there.  Each block knows all rows and takes some columns of the table; the cluster's barriers order the phases (checks, reference counts, pages
+// for the copies, the table).  (With the table read again in every phase, 24k clocks for 4 rows of 53 pages; 6k now.)
 constexpr int kReorderCluster = 8, kReorderCells = 32768;      // cells of the table that a block holds at a time
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 __device__ __forceinline__ int cluster_rank() {
     int r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
+}
+// all threads of the cluster
+__device__ __forceinline__ void cluster_sync(int ranks) {
+    if (ranks == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // the int at `p` of this block's shared memory, in block `rank` of the cluster
 __device__ __forceinline__ int cluster_peer(const int *p, int rank) {
@@ -327,27 +331,29 @@ __device__ __forceinline__ int cluster_peer(const int *p, int rank) {
     return v;
 }
 
-// what row b holds now and shall hold: pages (of its own, of its parent), tokens
-struct ReorderRow {
-    int parent, held, now, len;
+// rows in shared memory: parent; own length; the copy's number, -1: none
+struct ReorderRows {
+    int *parent, *len, *copy;
+    int n, tshift;
+    __device__ __forceinline__ int pages(int len) const { return (int)(((int64_t)len + (1 << tshift) - 1) >> tshift); }
+    __device__ __forceinline__ int held(int b) const { return pages(len[b]); }
+    __device__ __forceinline__ int new_len(int b) const { return parent[b] >= 0 ? len[parent[b]] : 0; }
 };
-__device__ __forceinline__ ReorderRow reorder_row(const KvPages &p, const int32_t *parent, int b) {
-    const int T = 1 << p.tshift;
-    ReorderRow r;
-    r.parent = parent[b];
-    r.len = r.parent >= 0 ? p.len[r.parent] : 0;
-    r.held = (int)(((int64_t)p.len[b] + T - 1) >> p.tshift);
-    r.now = (int)(((int64_t)r.len + T - 1) >> p.tshift);
-    return r;
+
+// the table's columns [c0, c0 + nc) of all rows; what lies past a row's pages is -1
+__device__ __forceinline__ void reorder_load(const KvPages &p, const ReorderRows &r, int c0, int nc, int32_t *s_cells) {
+    for (int i = threadIdx.x; i < r.n * nc; i += kPlanThreads) {
+        const int b = i / nc, s = c0 + i - b * nc;
+        s_cells[i] = s < r.held(b) ? p.table[(int64_t)b * p.max_pages + s] : -1;
+    }
 }
 
-// the reference counts' change for row b by one warp (sign -1: taken back): pages that both the row and its parent hold in the same place stay
-__device__ __forceinline__ void reorder_refs(const KvPages &p, const ReorderRow &r, int b, bool copies, int sign) {
-    if (r.parent == b && !copies) return;
-    const int32_t *own = p.table + (int64_t)b * p.max_pages, *from = p.table + (int64_t)(r.parent >= 0 ? r.parent : 0) * p.max_pages;
-    const int shared = r.now - copies;                         // the last page of a row that copies is its own
-    for (int s = threadIdx.x & 31; s < max(r.held, shared); s += 32) {
-        const int a = s < r.held ? own[s] : -1, c = s < shared ? from[s] : -1;
+// the reference counts' change (sign -1: taken back) in these columns: pages that a row and its parent hold in the same place stay
+__device__ __forceinline__ void reorder_refs(const KvPages &p, const ReorderRows &r, int c0, int nc, const int32_t *s_cells, int sign) {
+    for (int i = threadIdx.x; i < r.n * nc; i += kPlanThreads) {
+        const int b = i / nc, s = c0 + i - b * nc, parent = r.parent[b];
+        const bool mine = r.copy[b] >= 0 && s == r.pages(r.new_len(b)) - 1;    // the last page of a row that copies is its own
+        const int a = s_cells[i], c = parent >= 0 && !mine ? s_cells[parent * nc + s - c0] : -1;
         if (a == c) continue;
         if (a >= 0) atomicAdd(&p.refs[a], -sign);
         if (c >= 0) atomicAdd(&p.refs[c], sign);
@@ -355,79 +361,87 @@ __device__ __forceinline__ void reorder_refs(const KvPages &p, const ReorderRow 
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_reorder_kernel(KvPages p, const int32_t *parent, Ws ws, int cols, unsigned int *err) {
-    extern __shared__ int32_t s_cells[];                       // [n_seqs][cols]
+    extern __shared__ int32_t s_rows[];                        // parent, length, copy, first [n_seqs each], cells [n_seqs][cols]
     __shared__ int s_warp[32], s_bad, s_most;
     grid_dep_launch();
     grid_dep_wait();
-    const int T = 1 << p.tshift, n = p.n_seqs, rank = cluster_rank(), ranks = gridDim.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kPlanThreads / 32;
-    int32_t *first = ws.dst;                                   // the lowest row that continues each row
+    const int T = 1 << p.tshift, n = p.n_seqs, ranks = gridDim.x, rank = ranks == 1 ? 0 : cluster_rank();
+    const ReorderRows r{s_rows, s_rows + n, s_rows + 2 * n, n, p.tshift};
+    int *first = s_rows + 3 * n;                               // the lowest row that continues each row
+    int32_t *s_cells = s_rows + 4 * n;
     if (threadIdx.x == 0) s_bad = 0, s_most = 0;
-    for (int b = rank * kPlanThreads + threadIdx.x; b < n; b += ranks * kPlanThreads) first[b] = INT32_MAX;
-    cluster_sync();
-    // checks, a warp per row
+    for (int b = threadIdx.x; b < n; b += kPlanThreads) r.parent[b] = parent[b], r.len[b] = p.len[b], first[b] = INT32_MAX;
+    __syncthreads();
     unsigned bad = 0;
     int most = 0;
-    for (int b = rank * warps + warp; b < n; b += ranks * warps) {
-        const int a = parent[b];
-        const int64_t held = ((int64_t)p.len[b] + T - 1) >> p.tshift;
-        if (a < -1 || a >= n) bad |= KV_ERR_SEQ;
-        else if (a >= 0 && lane == 0) atomicMin(&first[a], b);
-        if (p.len[b] < 0 || held > p.max_pages) {
-            bad |= KV_ERR_LEN;
-            continue;
-        }
-        most = max(most, (int)held);
-        for (int s = lane; s < held; s += 32) {
-            const int page = p.table[(int64_t)b * p.max_pages + s];
-            if (page < 0 || page >= p.n_pages) bad |= KV_ERR_PAGE;
+    for (int b = threadIdx.x; b < n; b += kPlanThreads) {
+        const int a = r.parent[b], len = r.len[b];
+        if (a < -1 || a >= n) bad |= KV_ERR_SEQ, r.parent[b] = -1;
+        else if (a >= 0) atomicMin(&first[a], b);
+        if (len < 0 || r.pages(len) > p.max_pages) bad |= KV_ERR_LEN, r.len[b] = 0;
+        most = max(most, r.held(b));
+    }
+    atomicMax(&s_most, most);
+    __syncthreads();
+    most = s_most;
+    int need = 0;                                              // copies, in the order of the rows
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int b = base + threadIdx.x;
+        const bool k = b < n && r.parent[b] >= 0 && (r.len[r.parent[b]] & (T - 1)) != 0 && first[r.parent[b]] != b;
+        int total;
+        const int at = need + block_scan((int)k, s_warp, &total);
+        if (b < n) r.copy[b] = k ? at : -1;
+        need += total;
+    }
+    __syncthreads();
+    // this block's columns; they stay in shared memory if they fit
+    const int each = (most + ranks - 1) / ranks, from = min(rank * each, most), to = min(from + each, most);
+    const bool fits = to - from <= cols;
+    for (int c0 = from; c0 < to; c0 += cols) {
+        const int nc = min(cols, to - c0);
+        if (c0 > from) __syncthreads();
+        reorder_load(p, r, c0, nc, s_cells);
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * nc; i += kPlanThreads) {
+            const int b = i / nc, s = c0 + i - b * nc, page = s_cells[i];
+            if (s < r.held(b) && (page < 0 || page >= p.n_pages)) bad |= KV_ERR_PAGE;
         }
     }
     if (bad) atomicOr(&s_bad, (int)bad);
-    if (lane == 0) atomicMax(&s_most, most);
-    cluster_sync();
-    bad = 0, most = 0;
-    for (int i = 0; i < ranks; ++i) bad |= (unsigned)cluster_peer(&s_bad, i), most = max(most, cluster_peer(&s_most, i));
+    cluster_sync(ranks);
+    if (ranks == 1) bad = (unsigned)s_bad;
+    else
+        for (int i = 0; i < ranks; ++i) bad |= (unsigned)cluster_peer(&s_bad, i);
     if (bad) {                                                 // nothing has changed
         if (rank == 0 && threadIdx.x == 0) {
             kv_error(err, bad);
             ws.plan->n = 0;
         }
-        cluster_sync();                                        // (no block ends while another reads its shared memory)
+        cluster_sync(ranks);                                   // (no block ends while another reads its shared memory)
         return;
     }
-    for (int b = rank * warps + warp; b < n; b += ranks * warps) {
-        const ReorderRow r = reorder_row(p, parent, b);
-        reorder_refs(p, r, b, r.parent >= 0 && (r.len & (T - 1)) != 0 && first[r.parent] != b, 1);
-    }
-    cluster_sync();
-    if (rank == 0) {
-        int need = 0;
-        for (int base = 0; base < n; base += kPlanThreads) {
-            const int b = base + threadIdx.x;
-            int k = 0, len = 0;
-            if (b < n) {
-                const ReorderRow r = reorder_row(p, parent, b);
-                len = r.len;
-                k = r.parent >= 0 && (len & (T - 1)) != 0 && first[r.parent] != b;
+    auto count = [&](int sign) {
+        for (int c0 = from; c0 < to; c0 += cols) {
+            const int nc = min(cols, to - c0);
+            if (!fits) {
+                __syncthreads();
+                reorder_load(p, r, c0, nc, s_cells);
+                __syncthreads();
             }
-            int total;
-            const int at = need + block_scan(k, s_warp, &total);
-            if (b < n) ws.prefix[b] = k ? at : -1, ws.blocks[b] = len;
-            need += total;
+            reorder_refs(p, r, c0, nc, s_cells, sign);
         }
-        __syncthreads();
-        const bool enough = find_free(p.refs, p.n_pages, need, ws.list, s_warp);
+    };
+    count(1);
+    __threadfence();
+    cluster_sync(ranks);
+    if (rank == 0) {
+        const bool enough = find_free(p.refs, p.n_pages, need, ws.dst, s_warp);
         if (enough) {
-            for (int base = 0; base < n; base += kPlanThreads) {
-                const int b = base + threadIdx.x, at = b < n ? ws.prefix[b] : -1;
-                if (at < 0) continue;
-                const int len = ws.blocks[b], page = ws.list[at];
-                ws.src[at] = p.table[(int64_t)parent[b] * p.max_pages + (len >> p.tshift)];
-                ws.dst[at] = page;
-                ws.list[at] = ((len & (T - 1)) + kKB - 1) / kKB;
-                p.refs[page] = 1;
-            }
+            for (int b = threadIdx.x; b < n; b += kPlanThreads)
+                if (r.copy[b] >= 0) {
+                    p.refs[ws.dst[r.copy[b]]] = 1;
+                    ws.list[r.copy[b]] = ((r.new_len(b) & (T - 1)) + kKB - 1) / kKB;
+                }
         }
         if (threadIdx.x == 0) {
             ws.plan->n = enough ? need : 0;
@@ -435,33 +449,32 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reorder_kernel(KvPages p, con
             if (!enough) kv_error(err, KV_ERR_FULL);
         }
     }
-    cluster_sync();
-    if (cluster_peer(&s_bad, 0)) {                             // too few pages: the counts go back
-        for (int b = rank * warps + warp; b < n; b += ranks * warps)
-            reorder_refs(p, reorder_row(p, parent, b), b, ws.prefix[b] >= 0, -1);
-        cluster_sync();
+    cluster_sync(ranks);
+    if (ranks == 1 ? s_bad : cluster_peer(&s_bad, 0)) {        // too few pages: the counts go back
+        count(-1);
+        cluster_sync(ranks);
         return;
     }
-    // the table, some columns of all rows at a time
-    for (int c0 = rank * cols; c0 < most; c0 += ranks * cols) {
-        const int nc = min(cols, most - c0);
-        for (int i = threadIdx.x; i < n * nc; i += kPlanThreads) {
-            const int b = i / nc, s = c0 + i - b * nc;
-            s_cells[i] = p.table[(int64_t)b * p.max_pages + s];
+    for (int c0 = from; c0 < to; c0 += cols) {
+        const int nc = min(cols, to - c0);
+        if (!fits) {
+            __syncthreads();
+            reorder_load(p, r, c0, nc, s_cells);
+            __syncthreads();
         }
-        __syncthreads();
         for (int i = threadIdx.x; i < n * nc; i += kPlanThreads) {
-            const int b = i / nc, s = c0 + i - b * nc;
-            const ReorderRow r = reorder_row(p, parent, b);
-            if (r.parent == b && ws.prefix[b] < 0) continue;
-            int page = -1;
-            if (s < r.now) page = s == r.now - 1 && ws.prefix[b] >= 0 ? ws.dst[ws.prefix[b]] : s_cells[r.parent * nc + s - c0];
-            if (s < max(r.held, r.now)) p.table[(int64_t)b * p.max_pages + s] = page;
+            const int b = i / nc, s = c0 + i - b * nc, up = r.parent[b], now = r.pages(r.new_len(b));
+            int page = up >= 0 ? s_cells[up * nc + s - c0] : -1;
+            if (s == now - 1 && r.copy[b] >= 0) {
+                ws.src[r.copy[b]] = page;
+                page = ws.dst[r.copy[b]];
+            }
+            if (page != s_cells[i] && s < max(r.held(b), now)) p.table[(int64_t)b * p.max_pages + s] = page;
         }
-        __syncthreads();
     }
-    cluster_sync();                                            // all have read the lengths
-    for (int b = rank * kPlanThreads + threadIdx.x; b < n; b += ranks * kPlanThreads) p.len[b] = ws.blocks[b];
+    if (rank == 0)                                             // (all have read the lengths)
+        for (int b = threadIdx.x; b < n; b += kPlanThreads) p.len[b] = r.new_len(b);
+    cluster_sync(ranks);
 }
 
 constexpr int kCopyThreads = 256, kCopyChunk = 16384;
@@ -544,13 +557,12 @@ int kv_launch_fork(const KvPages &p, const int32_t *parent, const int32_t *child
 
 int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigned int *err, cudaStream_t s) {
     const Ws w(ws, p.n_pages, p.n_seqs);
-    int cols = 32;
-    while (cols > 1 && (int64_t)cols * p.n_seqs > kReorderCells) cols >>= 1;
-    const int smem = cols * p.n_seqs * 4;
-    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kv_reorder_kernel), kReorderCells * 4, kAttrSlotReorder);
+    const int fit = kReorderCells / p.n_seqs, cols = fit < p.max_pages ? fit : p.max_pages;     // (8 at least where there are as many)
+    const int smem = (4 * p.n_seqs + cols * p.n_seqs) * 4;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kv_reorder_kernel), (4 * kKvReorderRows + kReorderCells) * 4, kAttrSlotReorder);
     if (rc != MQ_OK) return rc;
     // one block for a small table, a cluster where there is much to check and to move
-    const unsigned blocks = (int64_t)p.n_seqs * p.max_pages <= 8192 ? 1 : kReorderCluster;
+    const unsigned blocks = (int64_t)p.n_seqs * p.max_pages <= 1024 ? 1 : kReorderCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kPlanThreads);

@@ -195,7 +195,7 @@ def test_reorder_refusals(L):
     for kw, status in BAD_SEQS:
         assert rc(_1=seqs(**kw)) == status, kw
     assert rc(_0=None) == ARG and rc(_1=None) == ARG and rc(_0=cache(refs=None)) == ARG and rc(_1=seqs(n_seqs=0)) == OK
-    assert rc(_1=seqs(n_seqs=32769)) == SHAPE and rc(_2=None) == ARG and rc(_2=CU + 2) == ALIGN
+    assert rc(_1=seqs(n_seqs=4097)) == SHAPE and rc(_2=None) == ARG and rc(_2=CU + 2) == ALIGN
     assert rc(_3=None) == ARG and rc(_3=WS + 8) == ALIGN and rc(_4=need - 1) == ARG and "workspace" in B.last_error()
 
 
