@@ -3,7 +3,7 @@
 #include <cfloat>
 #include <type_traits>
 
-#include "mq_kv.cuh"
+#include "mqd.cuh"
 
 namespace mq {
 namespace {
@@ -178,12 +178,12 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(TIN) == 4 ? 2 : 3) kv_a
 
 constexpr int kReadTokens = 16, kReadThreads = 256;
 
-// One CTA per 16 rows of the output, a warp per row and 8 of its 2 H vectors (half, head) at a time: their loads fly together.  Moves 5
-// (f32) or 3 bytes a value.
-template <typename TOUT, int D>
+// One CTA per 16 rows of the output, a warp per row and some of its 2 H vectors (half, head) at a time: their loads fly together.  Moves 5
+// (f32) or 3 bytes a value.  A lane takes CPL codes: 4, or where 16-byte stores of 16-bit values fit 8.
+template <typename TOUT, int D, int CPL>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows rows, TOUT *k, int64_t kt, int64_t kh, TOUT *v,
                                                                int64_t vt, int64_t vh, const int32_t *start, unsigned int *err) {
-    constexpr int LPR = D / 4, RPW = 32 / LPR, B = 8 / RPW;               // lanes per vector, vectors per load, loads in flight
+    constexpr int LPR = D / CPL, RPW = 32 / LPR, B = 2 * CPL / RPW, VECS = RPW * B;    // lanes per vector, vectors per load, loads in flight
     __shared__ const uint8_t *s_slab[kReadTokens];
     __shared__ int s_slot[kReadTokens];
     grid_dep_launch();
@@ -221,16 +221,24 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows 
     for (int t = warp; t < nt; t += kReadThreads / 32) {
         const uint8_t *slab = s_slab[t];
         const int slot = s_slot[t];
-        for (int v0 = 0; v0 < heads; v0 += 8) {
-            uint32_t w[B];
+        for (int v0 = 0; v0 < heads; v0 += VECS) {
+            uint32_t w[B][CPL / 4];
             float d[B];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 const int vec = v0 + i * RPW + lane / LPR;
-                w[i] = 0x80808080u, d[i] = 0.0f;
+                d[i] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < CPL / 4; ++q) w[i][q] = 0x80808080u;
                 if (slab != nullptr && vec < heads) {
                     // K of every head, then V of every head: one run of vectors
-                    w[i] = *reinterpret_cast<const uint32_t *>(slab + ((int64_t)vec * c.T + slot) * D + 4 * quad);
+                    const uint8_t *src = slab + ((int64_t)vec * c.T + slot) * D + CPL * quad;
+                    if constexpr (CPL == 8) {
+                        const uint2 two = *reinterpret_cast<const uint2 *>(src);
+                        w[i][0] = two.x, w[i][1] = two.y;
+                    } else {
+                        w[i][0] = *reinterpret_cast<const uint32_t *>(src);
+                    }
                     d[i] = reinterpret_cast<const float *>(slab + c.off_s)[vec * spp + slot / kKB];
                 }
             }
@@ -239,10 +247,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows 
                 const int vec = v0 + i * RPW + lane / LPR, half = vec >= c.H, h = vec - half * c.H;
                 TOUT *dst = half ? v : k;
                 if (vec >= heads || dst == nullptr) continue;
-                float x[4];
+                dst += (t0 + t) * (half ? vt : kt) + h * (half ? vh : kh) + CPL * quad;
+                float x[CPL];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(code_value(w[i], e), d[i]);
-                store4(dst + (t0 + t) * (half ? vt : kt) + h * (half ? vh : kh) + 4 * quad, x);
+                for (int e = 0; e < CPL; ++e) x[e] = __fmul_rn(code_value(w[i][e / 4], e % 4), d[i]);
+                if constexpr (CPL == 8) store8(dst, pack8(x, TOUT()));
+                else store4(dst, x);
             }
         }
     }
@@ -267,7 +277,11 @@ template <typename T>
 int read_t(const KvView &c, const KvRows &r, void *k, int64_t kt, int64_t kh, void *v, int64_t vt, int64_t vh,
            const int32_t *start, unsigned int *err, cudaStream_t s) {
     const dim3 grid((unsigned)((r.n_tokens + kReadTokens - 1) / kReadTokens));
-    auto fn = c.D == 128 ? kv_read_kernel<T, 128> : kv_read_kernel<T, 64>;
+    auto fn = c.D == 128 ? kv_read_kernel<T, 128, 4> : kv_read_kernel<T, 64, 4>;
+    if constexpr (sizeof(T) == 2) {
+        // 41k tokens of 8 heads of 128 to bf16: 8 codes a lane 69 us, 4 81
+        if (aligned(k, 16) && aligned(v, 16) && (kt % 8 | kh % 8 | vt % 8 | vh % 8) == 0) fn = c.D == 128 ? kv_read_kernel<T, 128, 8> : kv_read_kernel<T, 64, 8>;
+    }
     return cuda_error(launch_pdl(fn, grid, dim3(kReadThreads), 0, s, c, r, static_cast<T *>(k), kt, kh, static_cast<T *>(v), vt,
                                  vh, start, err),
                       "mqkv_read launch");
