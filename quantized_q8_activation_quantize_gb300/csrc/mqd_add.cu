@@ -73,7 +73,7 @@ __device__ __forceinline__ void norm8(float (&v)[8], float r, const float *w) {
 // One row per group of WT = 2^wt_log2 warps, warp g of it holding chunks g, g + WT, .. of 256 values (at most NC; lane l: values
 // 8 l .. 8 l + 7 of each).
 template <typename T, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 1024 : 256, NC == 1 ? 1 : 3) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {
+__global__ void __launch_bounds__(NC == 1 ? 1024 : 256, NC == 1 ? 1 : sizeof(T) == 4 ? 3 : 4) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {
     __shared__ float2 s_part[32];
     __shared__ double s_partd[32];
     grid_dep_launch();

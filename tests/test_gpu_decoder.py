@@ -677,3 +677,77 @@ def test_reorder_refuses_what_does_not_fit_and_bad_input():
         s.check()
     with pytest.raises(B.MQError):
         kv.mqkv_reorder(s.cache, s.seqs, i32([0, 1]), s.ws)
+
+
+# ------------------------------------------------------------------------------- all of it, as it is used ---
+
+@pytest.mark.parametrize("layers,heads,kv_heads,dim,prompt,beams,steps,page", [(2, 4, 2, 64, 45, 4, 40, 32), (1, 6, 1, 128, 7, 3, 9, 64), (3, 4, 4, 64, 96, 5, 33, 32)])
+def test_beam_search_keeps_every_hypothesis_in_the_cache(layers, heads, kv_heads, dim, prompt, beams, steps, page):
+    """Residuals, norms, planes, projections, rotations, appends, attention, head, selection and reordering in one captured step.  What the cache holds
+    for each beam at the end is what its tokens give when they are run alone: but for the f32 sums of attention, which may move a code of the next plane by one
+    (2e-2 of a state's size in all, as tests/test_gpu_kv.py has it), and for codes that then fall on the other side of a border (1 / 254 of a block's largest); rows
+    that are not the beam's own would be off by their whole size."""
+    import torch
+    from examples import kv_decode
+    ids = np.random.default_rng(9).integers(0, 300, prompt).tolist()
+
+    def model():
+        return kv_decode.Attention(layers, 512, heads, kv_heads, dim, beams, prompt + steps + 2, page)
+    m = model()
+    s = kv_decode.Search(m, beams, 300)
+    paths, scores = s.run(ids, steps)
+    assert all(len(p) == steps for p in paths) and len({tuple(p) for p in paths}) == beams
+    assert scores == sorted(scores, reverse=True) and np.isfinite(scores).all()
+    status()
+    B.mq_device_status()
+    assert m.len.tolist() == [prompt + steps - 1] * beams
+    # every page is named as often as its count says
+    names = torch.bincount(m.table[m.table >= 0].long(), minlength=len(m.refs))
+    assert torch.equal(names.int(), m.refs)
+
+    def cached(mm, seqs, layer, n, count):
+        k, v = (torch.empty((count * n, kv_heads, dim), device="cuda") for _ in range(2))
+        kv.mqkv_read(mm.cache, seqs, layer, k, v)
+        return k.view(count, n, -1), v.view(count, n, -1)
+    n = prompt + steps - 1
+    alone = model()
+    for b in range(beams):
+        alone.step(s.table[torch.tensor(ids, device="cuda")], 1)
+        for token in paths[b][:-1]:
+            alone.step(s.table[token:token + 1].clone(), 1)
+        for layer in range(layers):
+            for got, want in zip(cached(m, m.seqs(beams), layer, n, beams), cached(alone, alone.seqs(1), layer, n, 1)):
+                # per token: a single wrong row would show
+                err = ((got[b] - want[0]).norm(dim=1) / want[0].norm(dim=1)).max().item()
+                assert err < 0.05, (b, layer, err)
+        kv.mqkv_release(alone.cache, alone.all, i32([0]))
+    status()
+
+
+def test_captured_search_step_equals_the_same_calls():
+    import torch
+    from examples import kv_decode
+    got = []
+    for captured in (False, True):
+        m = kv_decode.Attention(2, 512, 4, 2, 64, 4, 120, 32)
+        m.pool.zero_()                                         # (what no token has written)
+        s = kv_decode.Search(m, 4, 500)
+        x = s.table[:4].clone()
+        m.step(x, 4)
+        s.scores.copy_(torch.tensor([[-0.5, -0.25, -1.0, -2.0]]))
+        if captured:
+            stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+            m.buffers(4, 4)
+            with torch.cuda.graph(graph, stream=stream):
+                s.step(x)
+            with torch.cuda.stream(stream):
+                for _ in range(40):
+                    graph.replay()
+        else:
+            for _ in range(40):
+                s.step(x)
+        sync()
+        status()
+        got.append([t.clone() for t in (x, s.scores, s.row, s.token, m.table, m.len, m.refs, m.pool)])
+    for a, b in zip(*got):
+        same(a, b)
