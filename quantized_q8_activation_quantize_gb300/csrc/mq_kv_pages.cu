@@ -574,7 +574,7 @@ int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigne
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = blocks, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
     rc = cuda_error(cudaLaunchKernelEx(&cfg, kv_reorder_kernel, p, parent, w, cols, err), "mqkv_reorder plan launch");
     if (rc != MQ_OK) return rc;
     const int64_t units = (int64_t)p.n_seqs * p.n_layers * 2 * p.H;

@@ -8,6 +8,7 @@ no Python or CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -55,61 +56,79 @@ def lib():
     return _L
 
 
-_float32 = None
+_float32 = _int32 = None
 
 
-def _mat(name, t, rows=None, cols=None):
+def _types():
+    """What of torch the calls compare with, resolved on the first one."""
+    global _float32, _int32
+    import torch
+    _float32, _int32 = torch.float32, torch.int32
+
+
+def _mat(name, t, rows, cols):
     """(pointer, row stride) of a [rows, cols] CUDA tensor with contiguous rows."""
-    if t.dim() != 2 or (rows is not None and t.shape != (rows, cols)):
-        _bad(f"{name} has shape {tuple(t.shape)}, {'two dimensions' if rows is None else f'[{rows}, {cols}]'} wanted")
+    if t.shape != (rows, cols):
+        _bad(f"{name} has shape {tuple(t.shape)}, [{rows}, {cols}] wanted")
     if not t.is_cuda:
         _bad(f"{name} is not a CUDA tensor")
     a, b = t.stride()
-    if b != 1 and t.shape[1] > 1:
+    if b != 1 and cols > 1:
         _bad(f"{name}: rows are not contiguous (strides {t.stride()})")
-    return t.data_ptr(), a if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), a if rows > 1 else cols
+
+
+def _two(name, t):
+    if len(t.shape) != 2:
+        _bad(f"{name} has shape {tuple(t.shape)}, two dimensions wanted")
+    return t.shape
 
 
 def _f32(name, t, *shape):
-    global _float32
     if _float32 is None:
-        import torch
-        _float32 = torch.float32
-    if t.dtype is not _float32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        _types()
+    if t.dtype is not _float32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _bad(f"{name} is not a contiguous float32 CUDA tensor of {list(shape)}")
     return t.data_ptr()
+
+
+def _ints(name, t, *shape):
+    if t.dtype is not _int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(f"{name} is not a contiguous int32 CUDA tensor of {list(shape)}")
+    return t.data_ptr()
+
+
+_plane_bytes = functools.lru_cache(maxsize=256)(binding.mq_q8_plane_bytes)
 
 
 def _plane(t, M, K):
     """A plane's pointer; where it is a tensor, it has to be contiguous CUDA memory of enough bytes."""
     if isinstance(t, int):
         return t
-    p, n = _ws(t)
-    if n < binding.mq_q8_plane_bytes(M, K):
-        _bad(f"the plane has {n} bytes, {binding.mq_q8_plane_bytes(M, K)} needed")
-    return p
+    if t.nbytes < _plane_bytes(M, K) or not t.is_cuda or not t.is_contiguous():
+        _bad(f"the plane is not contiguous CUDA memory of {_plane_bytes(M, K)} bytes")
+    return t.data_ptr()
 
 
 # ------------------------------------------------------------------ residual, RMSNorm, Q8 plane ---
 
 def mqd_add_quantize_q8(x, res, h, rms_w, eps: float, sections: int, plane, stream=None):
     """h = x + res ([M, K], one dtype; x None: no addition, h is not used) and the Q8 plane of RMSNorm(h) rms_w."""
-    r = _mat("res", res)
-    M, K = res.shape
-    if x is None:
-        a = b = (None, 0)
-    else:
-        if x.dtype is not res.dtype or h.dtype is not res.dtype:
-            _bad(f"x is {x.dtype}, res is {res.dtype}, h is {h.dtype}")
+    M, K = _two("res", res)
+    dtype = res.dtype
+    a = b = (None, 0)
+    if x is not None:
+        if x.dtype is not dtype or h.dtype is not dtype:
+            _bad(f"x is {x.dtype}, res is {dtype}, h is {h.dtype}")
         a, b = _mat("x", x, M, K), _mat("h", h, M, K)
-    return _check((_L or lib()).mqd_add_quantize_q8(_dtype(res.dtype), *a, *r, *b, M, K, _f32("rms_w", rms_w, K), eps, sections, _plane(plane, M, K),
+    return _check((_L or lib()).mqd_add_quantize_q8(_dtype(dtype), *a, *_mat("res", res, M, K), *b, M, K, _f32("rms_w", rms_w, K), eps, sections, _plane(plane, M, K),
                                                     _on(stream, res)))
 
 
 def mqd_dequantize_q8(plane, sections: int, y, stream=None):
     """The values of the plane of a y.shape activation into y (any of the three dtypes); sections: what the plane holds."""
-    p = _mat("y", y)
-    M, K = y.shape
+    M, K = _two("y", y)
+    p = _mat("y", y, M, K)
     return _check((_L or lib()).mqd_dequantize_q8(_plane(plane, M, K), M, K, sections, _dtype(y.dtype), *p, _on(stream, y)))
 
 
@@ -159,16 +178,18 @@ def alloc_beam_workspace(n_groups: int, n_beams: int, vocab: int, n_cand: int):
 
 def _triple(name, t, rows, n):
     """(score f32, row int32, token int32) of [rows, n] each"""
-    return _f32(f"{name}'s score", t[0], rows, n), _i32(f"{name}'s row", t[1], rows * n), _i32(f"{name}'s token", t[2], rows * n)
+    score, row, token = t
+    return _f32(name, score, rows, n), _ints(name, row, rows, n), _ints(name, token, rows, n)
 
 
 def mqd_beam_select(logits, scores, cand, next, stop: int, workspace, stream=None):
     """The best continuations of logits [n_groups * n_beams, vocab] by scores (f32 [n_groups, n_beams]): cand = (score f32, row int32, token
     int32) of [n_groups, n_cand] each; next (or None) the same of [n_groups, n_beams], without the token `stop` (-1: none)."""
-    if scores.dim() != 2:
+    if len(scores.shape) != 2:
         _bad(f"scores has shape {tuple(scores.shape)}, [n_groups, n_beams] wanted")
     G, B = scores.shape
     V, n = logits.shape[-1], cand[0].shape[-1]
+    own = _f32("scores", scores, G, B)
     p, stride = _mat("logits", logits, G * B, V)
-    return _check((_L or lib()).mqd_beam_select(_dtype(logits.dtype), p, stride, G, B, V, _f32("scores", scores, G, B), n, stop, *_triple("cand", cand, G, n),
+    return _check((_L or lib()).mqd_beam_select(_dtype(logits.dtype), p, stride, G, B, V, own, n, stop, *_triple("cand", cand, G, n),
                                                 *((None,) * 3 if next is None else _triple("next", next, G, B)), *_ws(workspace), _on(stream, logits)))
