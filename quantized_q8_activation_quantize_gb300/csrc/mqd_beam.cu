@@ -377,10 +377,10 @@ __device__ __forceinline__ int rank_of(const uint32_t *his, int n, uint32_t hi) 
     rank += __shfl_xor_sync(kFull, rank, 1);
     return rank + __shfl_xor_sync(kFull, rank, 2);
 }
-// The rank of item i among n by upper halves, where it is below k; items that look the same: by lower halves and place, lies_before(j, i).  All four lanes of an
-// item, all lanes of a warp.
-template <typename Before>
-__device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *los, int n, int n4, int i, int k, Before lies_before) {
+// The rank of item i among n by upper halves, where it is below k (else k); items that look the same: by lower halves and place(j), the lowest first.  All four lanes
+// of an item, all lanes of a warp.
+template <typename Place>
+__device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *los, int n, int n4, int i, int k, Place place) {
     const uint32_t hi = his[i];
     int rank = rank_of<false>(his, n4, hi);
     const bool in = hi != 0 && rank < k;
@@ -388,8 +388,10 @@ __device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *l
     const int same = rank_of<true>(his, n4, max(hi, 1u));
     if (__any_sync(kFull, in && same > rank + 1)) {
         int more = 0;
+        const uint32_t lo = los[i], at = place(i);
+#pragma unroll 4
         for (int j = threadIdx.x & 3; j < n; j += 4)
-            more += (int)((his[j] == hi) & ((los[j] > los[i]) | ((los[j] == los[i]) & lies_before(j, i))));
+            more += (int)((his[j] == hi) & ((los[j] > lo) | ((los[j] == lo) & (place(j) < at))));
         more += __shfl_xor_sync(kFull, more, 1);
         rank += more + __shfl_xor_sync(kFull, more, 2);
     }
@@ -399,8 +401,8 @@ __device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *l
 // A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted; lists come in
 // the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a few k as a rule, whose
 // ranks are counted again.  (Taking the best of all heads k times cost 300 clocks each.)
-constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
+constexpr int kJoinThreads = 512;      // with 40 registers: room beside the scan's blocks, so that it waits on its SM when they end
+__global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
                                                                  int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
                                                                  int32_t *next_token) {
     // of the heads, then of the entries (k * min(k, lists) of them): the upper halves of the keys, to compare, padded with zeros; the lower halves; the entries' places
@@ -413,10 +415,14 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int 
     grid_dep_launch();
     grid_dep_wait();
     const int64_t g = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P, l = threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P, n4 = (lists + 3) & ~3;
     const float2 *list = ws.list + g * lists * k;
-    float2 head = make_float2(0.0f, 0.0f);
-    if (l < lists) s_len[l] = ws.piece[g * lists + l].n, head = list[l * k];    // (not written where there is none)
+    float head[kMaxLists / kJoinThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
+        const int l = threadIdx.x + i * kJoinThreads;
+        if (l < lists) s_len[l] = ws.piece[g * lists + l].n, head[i] = list[l * k].x;   // (not written where there is none)
+    }
     if (threadIdx.x == 0) s_n = 0, s_lists = 0;
     for (int b = warp; b < B; b += warps) {                 // a warp per row: its sum of exponentials
         const float4 *piece = reinterpret_cast<const float4 *>(ws.piece + (g * B + b) * P);
@@ -449,17 +455,17 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int 
         }
     }
     __syncthreads();
-    const int n4 = (lists + 3) & ~3;
     uint32_t *his = s_keys, *los = his + n4;
-    if (l < n4) {
-        const int of = l < lists ? l / P : 0;
-        const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head.x, s_lh[of], s_ll[of]) : 0;
-        his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
+#pragma unroll
+    for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
+        const int l = threadIdx.x + i * kJoinThreads, of = l < lists ? l / P : 0;
+        const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head[i], s_lh[of], s_ll[of]) : 0;
+        if (l < n4) his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
     }
     __syncthreads();
     for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
         const int at = min(i, n4 - 1);
-        const int rank = rank_below(his, los, n4, n4, at, k, [](int a, int b) { return a < b; });
+        const int rank = rank_below(his, los, n4, n4, at, k, [](int a) { return (uint32_t)a; });
         if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
         s_list[atomicAdd(&s_lists, 1)] = i;
         if (rank == k - 1) s_bar[0] = his[i], s_bar[1] = los[i], s_bar[2] = (uint32_t)i;
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int 
     // the k-th head, where there are as many
     const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
     const int at_bar = left == k ? (int)s_bar[2] : lists;
-    uint32_t *ehi = los + n4, *elo = ehi + room, *etoken = elo + room, *ebeam = etoken + room;
+    uint32_t *ehi = los + n4, *elo = ehi + room, *etoken = elo + room, *eplace = etoken + room;        // (place: list, and where in it)
     for (int i = warp; i < left; i += warps) {
         const int from = s_list[i], of = from / P;
         for (int j = lane; j < s_len[from]; j += 32) {
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int 
             // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
             if ((y > bar) | ((y == bar) & (from <= at_bar))) {
                 const int c = atomicAdd(&s_n, 1);
-                ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), ebeam[c] = of;
+                ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), eplace[c] = from * kMaxCand + j;
             }
         }
     }
@@ -488,10 +494,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamWs ws, int 
     __syncthreads();
     for (int i = threadIdx.x >> 2; i < (all4 + 7 & ~7); i += kJoinThreads / 4) {
         const int at = min(i, all4 - 1);
-        const int rank = rank_below(ehi, elo, all, all4, at, k, [&](int a, int b) {
-            return (ebeam[a] < ebeam[b]) | ((ebeam[a] == ebeam[b]) & (etoken[a] < etoken[b]));
-        });
-        if (i < all && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = ebeam[i], s_token[rank] = (int)etoken[i];
+        const int rank = rank_below(ehi, elo, all, all4, at, k, [&](int a) { return eplace[a]; });
+        if (i < all && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = (int)(eplace[i] / kMaxCand) / P, s_token[rank] = (int)etoken[i];
     }
     __syncthreads();
     if (warp != 0) return;
