@@ -64,25 +64,31 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
     const int64_t row0 = lo + s0 - p0;                                          // row of slot 0
     const int y1 = min(y0 + in.each, c.H);
 
+    const bool whole = fresh == kKB;                                            // nearly always, in a large call
+    // the two quads of a lane (in values), of a turned key and of another vector
+    const bool turns = j < quads;
+    const int ka = plan.interleaved ? 8 * j : turns ? 4 * j : 2 * plan.half + 8 * (j - quads), kz = !plan.interleaved && turns ? ka + plan.half : ka + 4;
+
     Raw4<T> raw[IT][2];
-    // the two quads of a lane in a vector (in values)
-    auto places = [&](int vec, int &a, int &z) {
-        const bool apart = vec < c.H && !plan.interleaved;
-        a = !apart ? 8 * j : j < quads ? 4 * j : 2 * plan.half + 8 * (j - quads);
-        z = apart && j < quads ? a + plan.half : a + 4;
-    };
     auto ask = [&](int y) {
-        const int vec = 2 * y + team, half = vec >= c.H, h = vec - half * c.H;
-        int a, z;
-        places(vec, a, z);
+        const int vec = 2 * y + team, half = vec >= c.H, h = vec - half * c.H, a = half ? 8 * j : ka, z = half ? 8 * j + 4 : kz;
         const int64_t st = half ? in.vt : in.kt;
         const T *src = static_cast<const T *>(half ? in.v : in.k) + h * (half ? in.vh : in.kh) + (row0 + r0) * st;
+        const int64_t step = RPW * st;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            raw[i][0].w = {}, raw[i][1].w = {};
-            if (r0 + i * RPW >= new0 && r0 + i * RPW < new1) {
-                raw[i][0] = *reinterpret_cast<const Raw4<T> *>(src + i * RPW * st + a);
-                raw[i][1] = *reinterpret_cast<const Raw4<T> *>(src + i * RPW * st + z);
+            for (int i = 0; i < IT; ++i, src += step) {
+                raw[i][0] = *reinterpret_cast<const Raw4<T> *>(src + a);
+                raw[i][1] = *reinterpret_cast<const Raw4<T> *>(src + z);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i, src += step) {
+                raw[i][0].w = {}, raw[i][1].w = {};
+                if (r0 + i * RPW >= new0 && r0 + i * RPW < new1) {
+                    raw[i][0] = *reinterpret_cast<const Raw4<T> *>(src + a);
+                    raw[i][1] = *reinterpret_cast<const Raw4<T> *>(src + z);
+                }
             }
         }
     };
@@ -98,9 +104,7 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
     }
 #pragma unroll 1
     for (int y = y0; y < y1; ++y) {
-        const int vec = 2 * y + team, half = vec >= c.H;
-        int a, z;
-        places(vec, a, z);
+        const int vec = 2 * y + team, half = vec >= c.H, a = half ? 8 * j : ka, z = half ? 8 * j + 4 : kz;
         float x[IT][8];
 #pragma unroll
         for (int i = 0; i < IT; ++i) unpack4(raw[i][0], x[i]), unpack4(raw[i][1], x[i] + 4);
@@ -109,7 +113,7 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
         float *scale = reinterpret_cast<float *>(slab + c.off_s) + vec * (c.T / kKB) + slot0 / kKB;
         float d_old = new0 > 0 ? *scale : 0.0f;                                 // slots of earlier tokens share the block
         if (!(d_old >= 0.0f && d_old <= FLT_MAX)) d_old = 0.0f;
-        if (!half && j < quads) {
+        if (!half && turns) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int at = min(max(r0 + i * RPW - new0, 0), fresh - 1) * plan.half + 4 * j;         // (rows of no new token are zeros)
@@ -157,17 +161,20 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
         d = fmaxf(d, d_old);
         const float id = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
         const uint64_t f = f2_pack(id, id);
+        if (!finite) {                                                          // NaN is zero, an infinity the end of the range
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r = r0 + i * RPW;
-            if (r < new0 || r >= new1) continue;
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] == x[i][e] ? fminf(fmaxf(x[i][e], -127.0f * d), 127.0f * d) : 0.0f;
+        }
+        uint8_t *dst = codes + r0 * D;
+#pragma unroll
+        for (int i = 0; i < IT; ++i, dst += RPW * D) {
             float(&w)[8] = x[i];
-            if (!finite) {                                                      // NaN is zero, an infinity the end of the range
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = w[e] == w[e] ? fminf(fmaxf(w[e], -127.0f * d), 127.0f * d) : 0.0f;
+            if (whole || (r0 + i * RPW >= new0 && r0 + i * RPW < new1)) {
+                *reinterpret_cast<uint32_t *>(dst + a) = pack_codes(f2_mul(f2_pack(w[0], w[1]), f), f2_mul(f2_pack(w[2], w[3]), f));
+                *reinterpret_cast<uint32_t *>(dst + z) = pack_codes(f2_mul(f2_pack(w[4], w[5]), f), f2_mul(f2_pack(w[6], w[7]), f));
             }
-            *reinterpret_cast<uint32_t *>(codes + r * D + a) = pack_codes(f2_mul(f2_pack(w[0], w[1]), f), f2_mul(f2_pack(w[2], w[3]), f));
-            *reinterpret_cast<uint32_t *>(codes + r * D + z) = pack_codes(f2_mul(f2_pack(w[4], w[5]), f), f2_mul(f2_pack(w[6], w[7]), f));
         }
         if (new0 > 0 && d > d_old) {                                            // earlier codes under a larger scale
             const float shrink = __fdiv_rn(d_old, d);
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) kv_rope_rows_kernel(KvView c,
 }
 
 template <typename T, int W, int D>
-__global__ void __launch_bounds__(kTurnThreads, sizeof(T) == 4 ? 2 : 3) kv_append_rope_kernel(KvView c, KvRows rows, int gy, RopePlan plan, const int32_t *pos, RopeRows q,
+__global__ void __launch_bounds__(kTurnThreads, 2) kv_append_rope_kernel(KvView c, KvRows rows, int gy, RopePlan plan, const int32_t *pos, RopeRows q,
                                                                                              unsigned q_blocks, TurnedRows in, unsigned int *err) {
     __shared__ __align__(16) float s_cos[kKB * D / 2], s_sin[kKB * D / 2];      // (kRopeTokens * D / 2 at most for queries)
     grid_dep_launch();
