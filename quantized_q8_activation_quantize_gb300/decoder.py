@@ -66,16 +66,14 @@ def _types():
     _float32, _int32 = torch.float32, torch.int32
 
 
-def _mat(name, t, rows, cols):
-    """(pointer, row stride) of a [rows, cols] CUDA tensor with contiguous rows."""
-    if t.shape != (rows, cols):
-        _bad(f"{name} has shape {tuple(t.shape)}, [{rows}, {cols}] wanted")
-    if not t.is_cuda:
-        _bad(f"{name} is not a CUDA tensor")
+def _mat(name, t, shape):
+    """(pointer, row stride) of a CUDA tensor of this shape [rows, columns] with contiguous rows."""
+    if t.shape != shape or not t.is_cuda:
+        _bad(f"{name} is not a CUDA tensor of {list(shape)}, but {tuple(t.shape)} on {t.device}")
     a, b = t.stride()
-    if b != 1 and cols > 1:
+    if b != 1 and shape[1] > 1:
         _bad(f"{name}: rows are not contiguous (strides {t.stride()})")
-    return t.data_ptr(), a if rows > 1 else cols
+    return t.data_ptr(), a if shape[0] > 1 else shape[1]
 
 
 def _two(name, t):
@@ -84,7 +82,7 @@ def _two(name, t):
     return t.shape
 
 
-def _f32(name, t, *shape):
+def _f32(name, t, shape):
     if _float32 is None:
         _types()
     if t.dtype is not _float32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
@@ -92,7 +90,7 @@ def _f32(name, t, *shape):
     return t.data_ptr()
 
 
-def _ints(name, t, *shape):
+def _ints(name, t, shape):
     if t.dtype is not _int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _bad(f"{name} is not a contiguous int32 CUDA tensor of {list(shape)}")
     return t.data_ptr()
@@ -101,35 +99,43 @@ def _ints(name, t, *shape):
 _plane_bytes = functools.lru_cache(maxsize=256)(binding.mq_q8_plane_bytes)
 
 
-def _plane(t, M, K):
-    """A plane's pointer; where it is a tensor, it has to be contiguous CUDA memory of enough bytes."""
-    if isinstance(t, int):
-        return t
-    if t.nbytes < _plane_bytes(M, K) or not t.is_cuda or not t.is_contiguous():
-        _bad(f"the plane is not contiguous CUDA memory of {_plane_bytes(M, K)} bytes")
-    return t.data_ptr()
+def _bad_plane(M, K):
+    _bad(f"the plane is not contiguous CUDA memory of {_plane_bytes(M, K)} bytes")
 
 
 # ------------------------------------------------------------------ residual, RMSNorm, Q8 plane ---
 
 def mqd_add_quantize_q8(x, res, h, rms_w, eps: float, sections: int, plane, stream=None):
     """h = x + res ([M, K], one dtype; x None: no addition, h is not used) and the Q8 plane of RMSNorm(h) rms_w."""
+    shape, dtype = res.shape, res.dtype
     M, K = _two("res", res)
-    dtype = res.dtype
-    a = b = (None, 0)
-    if x is not None:
+    if x is None:
+        a = b = (None, 0)
+    else:
         if x.dtype is not dtype or h.dtype is not dtype:
             _bad(f"x is {x.dtype}, res is {dtype}, h is {h.dtype}")
-        a, b = _mat("x", x, M, K), _mat("h", h, M, K)
-    return _check((_L or lib()).mqd_add_quantize_q8(_dtype(dtype), *a, *_mat("res", res, M, K), *b, M, K, _f32("rms_w", rms_w, K), eps, sections, _plane(plane, M, K),
+        a, b = _mat("x", x, shape), _mat("h", h, shape)
+    if isinstance(plane, int):
+        at = plane
+    else:
+        at = plane.data_ptr()
+        if plane.nbytes < _plane_bytes(M, K) or not plane.is_cuda or not plane.is_contiguous():
+            _bad_plane(M, K)
+    return _check((_L or lib()).mqd_add_quantize_q8(_dtype(dtype), *a, *_mat("res", res, shape), *b, M, K, _f32("rms_w", rms_w, (K,)), eps, sections, at,
                                                     _on(stream, res)))
 
 
 def mqd_dequantize_q8(plane, sections: int, y, stream=None):
     """The values of the plane of a y.shape activation into y (any of the three dtypes); sections: what the plane holds."""
     M, K = _two("y", y)
-    p = _mat("y", y, M, K)
-    return _check((_L or lib()).mqd_dequantize_q8(_plane(plane, M, K), M, K, sections, _dtype(y.dtype), *p, _on(stream, y)))
+    out = _mat("y", y, y.shape)
+    if isinstance(plane, int):
+        at = plane
+    else:
+        at = plane.data_ptr()
+        if plane.nbytes < _plane_bytes(M, K) or not plane.is_cuda or not plane.is_contiguous():
+            _bad_plane(M, K)
+    return _check((_L or lib()).mqd_dequantize_q8(at, M, K, sections, _dtype(y.dtype), *out, _on(stream, y)))
 
 
 # ----------------------------------------------------------------------------- rotary positions ---
@@ -179,7 +185,8 @@ def alloc_beam_workspace(n_groups: int, n_beams: int, vocab: int, n_cand: int):
 def _triple(name, t, rows, n):
     """(score f32, row int32, token int32) of [rows, n] each"""
     score, row, token = t
-    return _f32(name, score, rows, n), _ints(name, row, rows, n), _ints(name, token, rows, n)
+    shape = rows, n
+    return _f32(name, score, shape), _ints(name, row, shape), _ints(name, token, shape)
 
 
 def mqd_beam_select(logits, scores, cand, next, stop: int, workspace, stream=None):
@@ -189,7 +196,7 @@ def mqd_beam_select(logits, scores, cand, next, stop: int, workspace, stream=Non
         _bad(f"scores has shape {tuple(scores.shape)}, [n_groups, n_beams] wanted")
     G, B = scores.shape
     V, n = logits.shape[-1], cand[0].shape[-1]
-    own = _f32("scores", scores, G, B)
-    p, stride = _mat("logits", logits, G * B, V)
+    own = _f32("scores", scores, scores.shape)
+    p, stride = _mat("logits", logits, (G * B, V))
     return _check((_L or lib()).mqd_beam_select(_dtype(logits.dtype), p, stride, G, B, V, own, n, stop, *_triple("cand", cand, G, n),
                                                 *((None,) * 3 if next is None else _triple("next", next, G, B)), *_ws(workspace), _on(stream, logits)))
