@@ -517,6 +517,26 @@ def test_select_is_the_same_every_time_and_in_a_graph():
             assert np.array_equal(a.cpu().numpy(), b)
 
 
+def test_select_rows_past_32_bits_and_heads_of_one_row():
+    import torch
+    # rows 2^31 + 40 elements apart
+    buf = torch.full((2 ** 31 + 40 + 3001,), 7.0, dtype=torch.float16, device="cuda")
+    logits = torch.as_strided(buf, (2, 3001), (2 ** 31 + 40, 1), 0)
+    logits.copy_(torch.randn((2, 3001), device="cuda") * 2)
+    check_select(logits, torch.tensor([[0.0, -0.5]], device="cuda"), 6)
+    check_select(logits[:1].expand(3, -1).contiguous(), torch.tensor([[-1.0, -1.0, -1.0]], device="cuda"), 9)      # every score three times
+
+
+def test_rope_of_one_head_for_six():
+    import torch
+    x = torch.randn((5, 1, 64), device="cuda")
+    out = torch.empty((5, 6, 64), device="cuda")
+    pos = np.arange(5, dtype=np.int32) * 1000
+    dec.mqd_rope(dec.rope_plan(64), x.expand(5, 6, 64), out, dev(pos))
+    sync()
+    check_turned(out, x.expand(5, 6, 64), pos, dec.mqd_rope_turns(64), 64, False, 1.0, "f32")
+
+
 def test_select_without_next():
     import torch
     cand, nxt = select(torch.randn((6, 999), device="cuda"), torch.zeros((2, 3), device="cuda"), 5, next=False)
