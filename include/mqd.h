@@ -28,14 +28,15 @@ typedef enum { MQD_F32 = 0, MQD_F16 = 1, MQD_BF16 = 2 } mqd_dtype;  /* the numbe
  *              stack's first norm in 16 bits)
  *   res        [M][K], the residual stream
  *   h          [M][K] output, x + res in f32 rounded once to dtype; may be res or x itself (same pointer and stride),
- *              and otherwise may not overlap them; ignored where x is NULL
+ *              and otherwise may not overlap them (rows of one buffer and one stride, side by side, do not); ignored where x
+ *              is NULL
  *   *_stride   of rows, at least K and multiples of 8; bases 16-byte aligned
  *   rms_w      f32 [K], 16-byte aligned
  *   eps, sections, plane   as mq_quantize_q8_ex
  *
  * The plane holds what mq_quantize_q8_ex writes for h (as it is stored, widened to f32), rms_w and eps: the same bits, but
  * for about one row in 10^7, whose r lies within the f64 sums' own rounding of an f32 border.
- * K as in mq.h (a positive multiple of 256); M == 0 is an empty call.
+ * K as in mq.h (a positive multiple of 256); M below 2^31, M == 0 is an empty call.
  */
 MQ_API int mqd_add_quantize_q8(int32_t dtype, const void *x, int64_t x_stride, const void *res, int64_t res_stride, void *h,
                                int64_t h_stride, int64_t M, int64_t K, const float *rms_w, float eps, unsigned sections,
@@ -89,8 +90,9 @@ typedef struct {
  * mqd_rope -- out = x with the first rot_dim values of every head turned, in f32, rounded once to dtype.
  *
  *   x, out     [n_tokens][n_heads][head_dim] of dtype, head_dim a multiple of 8 from 8 to 1024 and at least rot_dim, values of a
- *              head contiguous, strides multiples of 4, bases aligned to 4 elements; out may be x (same pointer and strides), and
- *              otherwise may not overlap it
+ *              head contiguous, strides multiples of 4 (of x: 0 repeats), bases aligned to 4 elements; out may be x (same pointer and
+ *              strides), and otherwise may not overlap it (tokens of one buffer and one stride, side by side, do not).  Fewer than
+ *              2^31 tokens, up to 65536 heads
  *   pos        int32 [n_tokens], any sign (a negative one turns back)
  */
 MQ_API int mqd_rope(const mqd_rope_plan *plan, int32_t dtype, const void *x, int64_t x_token_stride, int64_t x_head_stride,
@@ -114,8 +116,8 @@ MQ_API int mqd_rope(const mqd_rope_plan *plan, int32_t dtype, const void *x, int
  *   stop       the token that ends a sequence, or -1
  *   workspace  mqd_beam_workspace_bytes(...) bytes, 256-byte aligned, not shared by calls in flight
  *
- * Scores are compared as f32 pairs (48 bits: two beams' continuations may differ by less than an f32 step) and returned rounded to f32;
- * a row's logarithm is good to about 1e-7.  n_beams 1 .. 64, n_groups * n_beams < 2^24, vocab < 2^31 - 2^16.
+ * Scores are compared as f32 pairs (48 bits: two beams' continuations may differ by less than an f32 step) and returned rounded to f32; of
+ * those that agree in all 48 bits, tokens of one row may come in the order of their logits.  A row's logarithm is good to about 1e-7.  n_beams 1 .. 64, n_groups * n_beams < 2^24, vocab < 2^31 - 2^16.
  */
 MQ_API size_t mqd_beam_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand);
 MQ_API int mqd_beam_select(int32_t dtype, const void *logits, int64_t row_stride, int64_t n_groups, int32_t n_beams, int64_t vocab,

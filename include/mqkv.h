@@ -92,11 +92,12 @@ MQ_API int mqkv_append(const mqkv_cache *cache, const mqkv_seqs *seqs, int32_t l
 
 /*
  * mqkv_append_rope -- mqkv_append of keys turned by their positions (mqd_rope), with the queries turned beside it: what a layer does
- * between its projections and mqkv_attention, in one launch.
+ * between its projections and mqkv_attention, in one call.
  *
  *   plan       rot_dim at most head_dim
  *   pos        int32 [n_tokens], the position of every row; NULL: the cached ones (kv_len[b] - n_b + i)
- *   q, q_out   [n_tokens][n_q_heads][head_dim] of dtype, as x and out of mqd_rope (q_out may be q itself); n_q_heads = 0: no queries
+ *   q, q_out   [n_tokens][n_q_heads][head_dim] of dtype, as x and out of mqd_rope (q_out may be q itself), up to 65536 heads; n_q_heads = 0:
+ *              no queries
  *   k, v, cu   as in mqkv_append; q_out may lie in one buffer with k and v (one projection's output) where their heads do not meet
  *
  * Keys are turned in f32 and quantized as they come out, without a rounding to dtype; q_out holds what mqd_rope gives.  Rows of q that

@@ -97,17 +97,6 @@ bool rows_apart(int64_t n, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
     return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (n - 1) * ts + dim);
 }
 
-// whether the values of two [n][width] tensors of the given token strides are surely apart: their spans are, or both have one stride and their rows'
-// places in it do not meet
-bool values_apart(const void *a, size_t na, int64_t as, int64_t aw, const void *b, size_t nb, int64_t bs, int64_t bw, int64_t n, int32_t dtype) {
-    if (!overlaps(a, na, b, nb)) return true;
-    if (n <= 1 || as != bs || as <= 0) return false;
-    const int64_t size = type_bytes(dtype), s = as * size;
-    int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % s;
-    if (d < 0) d += s;
-    return aw * size <= d && d + bw * size <= s;
-}
-
 KvView view_of(const mqkv_cache &c, const mqkv_seqs &s, const mqkv_layout &lay, int32_t layer) {
     KvView v;
     v.pool = static_cast<uint8_t *>(c.pool) + (size_t)layer * lay.layer_bytes;

@@ -561,8 +561,9 @@ int kv_launch_reorder(const KvPages &p, const int32_t *parent, void *ws, unsigne
     const int smem = (4 * p.n_seqs + cols * p.n_seqs) * 4;
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(kv_reorder_kernel), (4 * kKvReorderRows + kReorderCells) * 4, kAttrSlotReorder);
     if (rc != MQ_OK) return rc;
-    // one block for a small table, a cluster where there is much to check and to move
-    const unsigned blocks = (int64_t)p.n_seqs * p.max_pages <= 1024 ? 1 : kReorderCluster;
+    // One block for a small table, a cluster where there is much to check and to move.  Both kernels in a graph, one block and eight: 256 cells 7.9 and 10.1 us, 1024 8.9 and
+    // 10.7, 2048 9.9 and 10.8, 4096 12.2 and 10.3, 16384 26 and 12.
+    const unsigned blocks = (int64_t)p.n_seqs * p.max_pages <= 2048 ? 1 : kReorderCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kPlanThreads);

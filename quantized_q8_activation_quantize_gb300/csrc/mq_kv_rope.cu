@@ -252,17 +252,21 @@ __global__ void __launch_bounds__(kTurnThreads, 2) kv_append_rope_kernel(KvView 
 template <typename T, int W>
 int append_rope_t(const KvView &c, const KvRows &r, const RopePlan &plan, const int32_t *pos, const RopeRows &q, TurnedRows in, unsigned int *err, cudaStream_t s) {
     const int64_t q_all = q.x != nullptr ? (q.n_tokens + q.per_block - 1) / q.per_block : 0;
+    // 28:4 heads of bf16, 1216 tokens in one launch 8.9 us, in two 11.4; 2432 16.2 and 15.7; 4864 30.0 and 26.6; 9728 56 and 46
     const bool apart = q_all > 4 * sm_count();
+    const int64_t units = r.cu == nullptr ? c.n_seqs * (r.each / kKB + 2) : r.n_tokens / kKB + 2 * (int64_t)c.n_seqs;
+    // As many pairs of vectors a block as leave one wave of blocks, two an SM; all where there is more than a wave (the angles are then computed once).  f32, 8
+    // heads, with 1, 2, 4, 8 pairs a block: 1024 tokens 6.4 7.9 10.3 14.6 us, 2048 10.2 8.2 11.3 14.9, 4096 18.2 15.6 13.8 20.5, 16384 61 49 46 44; a token of 64
+    // sequences 8.5 6.9 8.5 12.7.
+    const int64_t about = r.n_tokens / kKB + c.n_seqs, fit = 2 * sm_count() / about;         // blocks of slots that hold a token, nearly
+    in.each = fit > 1 ? (int)((c.H + fit - 1) / fit) : c.H;
+    const int gy = (c.H + in.each - 1) / in.each;
+    const int64_t q_blocks = apart ? 0 : q_all, blocks = q_blocks + units * gy;
+    if (blocks > INT32_MAX) return set_error(MQ_ERR_SHAPE, "mqkv_append_rope: %lld blocks, below 2^31 wanted (fewer tokens a call)", (long long)blocks);
     if (apart) {
         const int rc = cuda_error(launch_pdl(kv_rope_rows_kernel<T, W>, dim3((unsigned)q_all), dim3(kRopeThreads), 0, s, c, r, plan, pos, q), "mqkv_append_rope launch");
         if (rc != MQ_OK) return rc;
     }
-    const int64_t units = r.cu == nullptr ? c.n_seqs * (r.each / kKB + 2) : r.n_tokens / kKB + 2 * (int64_t)c.n_seqs;
-    // all vectors of a block of slots where that leaves a few blocks per SM (the angles are then computed once), two where it would not
-    in.each = units >= 8 * sm_count() ? c.H : 1;
-    const int gy = (c.H + in.each - 1) / in.each;
-    const int64_t q_blocks = apart ? 0 : q_all, blocks = q_blocks + units * gy;
-    if (blocks > INT32_MAX) return set_error(MQ_ERR_SHAPE, "mqkv_append_rope: %lld blocks, below 2^31 wanted (fewer tokens a call)", (long long)blocks);
     auto fn = c.D == 128 ? kv_append_rope_kernel<T, W, 128> : kv_append_rope_kernel<T, W, 64>;
     return cuda_error(launch_pdl(fn, dim3((unsigned)blocks), dim3(kTurnThreads), 0, s, c, r, gy, plan, pos, q, (unsigned)q_blocks, in, err), "mqkv_append_rope launch");
 }
@@ -271,7 +275,8 @@ int append_rope_t(const KvView &c, const KvRows &r, const RopePlan &plan, const 
 
 int kv_launch_append_rope(const KvView &c, const KvRows &r, int dtype, const RopePlan &plan, const int32_t *pos, const KvRopeRows &q, const void *k,
                           int64_t kt, int64_t kh, const void *v, int64_t vt, int64_t vh, unsigned int *err, cudaStream_t s) {
-    const RopeRows rows{q.x, q.out, q.xt, q.xh, q.ot, q.oh, r.n_tokens, q.heads, c.D, r.n_tokens <= 4 * sm_count() ? 1 : kRopePairs / plan.half < kRopeTokens ? kRopePairs / plan.half : kRopeTokens};
+    RopeRows rows{q.x, q.out, q.xt, q.xh, q.ot, q.oh, r.n_tokens, q.heads, c.D, 1};
+    if (q.heads > 0) rows.per_block = rope_tokens(plan, rows);
     const bool wide = rope_wide(plan, rows);
     auto fn = dtype == MQKV_F32   ? append_rope_t<float, 4>
               : dtype == MQKV_F16 ? (wide ? append_rope_t<__half, 8> : append_rope_t<__half, 4>)

@@ -52,6 +52,20 @@ template <typename T>
 __device__ __forceinline__ void store8(T *p, const Raw8<T> &r) {
     *reinterpret_cast<uint4 *>(p) = r.w;
 }
+// store8 by all lanes of a warp, lane l to base + 8 l.  f32: neighbouring lanes exchange quarters, so that a store fills whole sectors of 32 bytes
+__device__ __forceinline__ void store8_row(float *p, const Raw8<float> &r, int lane) {
+    const bool odd = lane & 1;
+    const float4 give = odd ? r.a : r.b;
+    float4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1), got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, 1), got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+    reinterpret_cast<float4 *>(p)[odd ? -1 : 0] = odd ? got : r.a;
+    reinterpret_cast<float4 *>(p)[odd ? 1 : 2] = odd ? r.b : got;
+}
+template <typename T>
+__device__ __forceinline__ void store8_row(T *p, const Raw8<T> &r, int) {
+    store8(p, r);
+}
 
 // launchers (arguments already validated)
 struct AddQuantize {
@@ -90,6 +104,7 @@ int rope_plan_of(const char *fn, const mqd_rope_plan *plan, int32_t head_dim, Ro
 int check_rope_heads(const char *fn, const char *what, const void *p, int64_t ts, int64_t hs, int32_t dtype);
 int check_rope_out(const char *fn, const void *x, int64_t xt, int64_t xh, const void *out, int64_t ot, int64_t oh, int64_t n, int64_t heads, int64_t dim,
                    int32_t dtype);
+bool values_apart(const void *a, size_t na, int64_t as, int64_t aw, const void *b, size_t nb, int64_t bs, int64_t bw, int64_t n, int32_t dtype);
 size_t heads_span(int64_t n, int64_t heads, int64_t dim, int64_t ts, int64_t hs, int32_t dtype);
 
 }  // namespace mq

@@ -47,6 +47,17 @@ int check_beams(const char *fn, int64_t n_groups, int32_t n_beams, int64_t vocab
 
 }  // namespace
 
+// whether the values of two [n][width] tensors of the given token strides are surely apart: their spans are, or both have one stride and their rows'
+// places in it do not meet
+bool values_apart(const void *a, size_t na, int64_t as, int64_t aw, const void *b, size_t nb, int64_t bs, int64_t bw, int64_t n, int32_t dtype) {
+    if (!overlaps(a, na, b, nb)) return true;
+    if (n <= 1 || as != bs || as <= 0) return false;
+    const int64_t size = type_bytes(dtype), s = as * size;
+    int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % s;
+    if (d < 0) d += s;
+    return aw * size <= d && d + bw * size <= s;
+}
+
 int rope_plan_of(const char *fn, const mqd_rope_plan *plan, int32_t head_dim, RopePlan *out) {
     if (plan == nullptr) return set_error(MQ_ERR_ARG, "%s: NULL plan", fn);
     MQD_TRY(check_rot(fn, plan->rot_dim));
@@ -78,7 +89,9 @@ int check_rope_out(const char *fn, const void *x, int64_t xt, int64_t xh, const 
                        : n <= 1             ? oh >= dim
                                             : (oh >= dim && ot >= (heads - 1) * oh + dim) || (ot >= dim && oh >= (n - 1) * ot + dim);
     if (!apart) return set_error(MQ_ERR_ARG, "%s: heads of out overlap (strides %lld, %lld)", fn, (long long)ot, (long long)oh);
-    if (overlaps(out, heads_span(n, heads, dim, ot, oh, dtype), x, heads_span(n, heads, dim, xt, xh, dtype)) && !(out == x && ot == xt && oh == xh))
+    if (!values_apart(out, heads_span(n, heads, dim, ot, oh, dtype), ot, (heads - 1) * oh + dim, x, heads_span(n, heads, dim, xt, xh, dtype), xt,
+                      (heads - 1) * xh + dim, n, dtype) &&
+        !(out == x && ot == xt && oh == xh))
         return set_error(MQ_ERR_ARG, "%s: out %p overlaps the input %p without being it", fn, out, x);
     return MQ_OK;
 }
@@ -111,8 +124,8 @@ int mqd_add_quantize_q8(int32_t dtype, const void *x, int64_t x_stride, const vo
                  xb = x != nullptr ? rows_span(M, K, x_stride, dtype) : 0, hb = x != nullptr ? rows_span(M, K, h_stride, dtype) : 0;
     if (overlaps(plane, pb, x, xb) || overlaps(plane, pb, res, rb) || overlaps(plane, pb, h, hb) || overlaps(plane, pb, rms_w, wb))
         return set_error(MQ_ERR_ARG, "%s: plane %p overlaps x %p, res %p, h %p or rms_w %p", fn, plane, x, res, h, (const void *)rms_w);
-    if (overlaps(h, hb, rms_w, wb) || (overlaps(h, hb, x, xb) && !(h == x && h_stride == x_stride)) ||
-        (overlaps(h, hb, res, rb) && !(h == res && h_stride == res_stride)))
+    if (overlaps(h, hb, rms_w, wb) || (!values_apart(h, hb, h_stride, K, x, xb, x_stride, K, M, dtype) && !(h == x && h_stride == x_stride)) ||
+        (!values_apart(h, hb, h_stride, K, res, rb, res_stride, K, M, dtype) && !(h == res && h_stride == res_stride)))
         return set_error(MQ_ERR_ARG, "%s: h %p overlaps rms_w %p, or x %p or res %p without being it", fn, h, (const void *)rms_w, x, res);
     unsigned int *err = nullptr;
     MQD_TRY(device_state(&err));

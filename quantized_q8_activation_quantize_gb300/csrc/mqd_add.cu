@@ -38,8 +38,12 @@ __device__ __forceinline__ float row_scale(float2 hi, float2 lo, int64_t K, floa
     if (WT > 1) {
         if (lane == 0) s_part[warp] = make_float2(th, tl);
         named_bar(bar, WT * 32);
-        th = s_part[first].x, tl = s_part[first].y;
-        for (int k = 1; k < WT; ++k) pair_add(th, tl, s_part[first + k].x, s_part[first + k].y);
+        const float2 part = s_part[first + (lane & WT - 1)];   // (WT is a power of two: every lane ends with all of them)
+        th = part.x, tl = part.y;
+        for (int o = WT >> 1; o > 0; o >>= 1) {
+            const float bh = __shfl_xor_sync(kFull, th, o), bl = __shfl_xor_sync(kFull, tl, o);
+            pair_add(th, tl, bh, bl);
+        }
     }
     float r;
     if (!rms_scale_from_pair(th, tl, K, eps, r)) {          // (the same in all warps of the row)
@@ -71,9 +75,10 @@ __device__ __forceinline__ void norm8(float (&v)[8], float r, const float *w) {
 }
 
 // One row per group of WT = 2^wt_log2 warps, warp g of it holding chunks g, g + WT, .. of 256 values (at most NC; lane l: values
-// 8 l .. 8 l + 7 of each).
-template <typename T, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 1024 : 256, NC == 1 ? 1 : sizeof(T) == 4 ? 3 : 4) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {
+// 8 l .. 8 l + 7 of each).  Bound by HBM for many rows: 333 rows .. thousands reach 5.5 TB/s of their algorithmic bytes (2048 rows of bf16, 4096 wide ADDFIG).  A quarter
+// of the registers of an SM (16-bit) or a third (f32) per block of eight warps, so that one group's sums hide under the others' loads.
+template <typename T, int NC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(T) == 4 ? 3 : 4) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {
     __shared__ float2 s_part[32];
     __shared__ double s_partd[32];
     grid_dep_launch();
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 256, NC == 1 ? 1 : sizeof(T) 
         for (int j = 0; j < NC; ++j) {
             Raw8<T> o;
             add8(rx[j], rr[j], v[j], o);
-            if (j < nvalid) store8(h + (g + j * WT) * 256, o);
+            if (j < nvalid) store8_row(h + (g + j * WT) * 256, o, lane);
         }
     } else {
 #pragma unroll
@@ -122,8 +127,8 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 256, NC == 1 ? 1 : sizeof(T) 
     quantize_chunks<NC>(v, nvalid, g, WT, lane, a.sections, p, a.M, a.K, m);
 }
 
-// Rows too long for registers: a block per row, h written in the first pass and read again (from L2, by the thread that wrote
-// it) in the second.
+// Rows too long for registers: a block per row, h written in the first pass and read again (from L2, by the warp that wrote it)
+// in the second.  4000 rows of 16384 f32 values take 185 us (the floor's bytes at 5.6 TB/s ADDLONG).
 template <typename T>
 __global__ void __launch_bounds__(256) add_quantize_kernel(AddQuantize a, Plane p) {
     __shared__ float2 s_part[8];
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(256) add_quantize_kernel(AddQuantize a, Plane 
         if (a.x != nullptr) {
             Raw8<T> o;
             add8(load8(x + (int64_t)c * 256), load8(res + (int64_t)c * 256), v, o);
-            store8(h + (int64_t)c * 256, o);
+            store8_row(h + (int64_t)c * 256, o, lane);
         } else {
             unpack8(load8(res + (int64_t)c * 256), v);
         }
@@ -169,15 +174,24 @@ __global__ void __launch_bounds__(256) add_quantize_kernel(AddQuantize a, Plane 
 template <typename T>
 int add_quantize_t(const AddQuantize &a, const Plane &p, cudaStream_t s) {
     const int64_t nch = a.K / 256;
-    cudaError_t e;
-    if (nch <= 32 && a.M <= 2 * sm_count()) {               // few rows: a warp for every chunk
-        int wl = 0;
+    cudaError_t e = cudaSuccess;
+    const int64_t sms = sm_count();
+    int wl = 0;
+    // Few rows: a warp for every chunk, up to 32 warps and 4 blocks an SM.  Against four chunks a warp (us in a graph, f32): 1 row of 4096 3.4 and 3.9, 152 4.0 and
+    // 5.3, 304 5.2 and 5.5, 608 11.0 and 11.2 (bf16 9.5 and 7.0); 608 rows of 1024 3.5 and 5.1, 1216 6.0 and 5.2; 152 of 8192 5.5 and 5.5, 304 11.8 and 11.0.
+    if (nch <= 32 && a.M <= 4 * sms && a.M * nch <= 32 * sms) {
         while ((1 << wl) < nch) ++wl;
-        e = launch_pdl(add_quantize_regs_kernel<T, 1>, dim3((unsigned)a.M), dim3(32u << wl), 0, s, a, p, wl);
+        e = launch_pdl(add_quantize_regs_kernel<T, 1, 1024>, dim3((unsigned)a.M), dim3(32u << wl), 0, s, a, p, wl);
     } else if (nch <= 32) {
-        int wl = 0;
         while ((4 << wl) < nch) ++wl;
-        e = launch_pdl(add_quantize_regs_kernel<T, 4>, dim3((unsigned)((a.M + (8 >> wl) - 1) / (8 >> wl))), dim3(256), 0, s, a, p, wl);
+        e = launch_pdl(add_quantize_regs_kernel<T, 4, 256>, dim3((unsigned)((a.M + (8 >> wl) - 1) / (8 >> wl))), dim3(256), 0, s, a, p, wl);
+    } else if (sizeof(T) == 2 && nch <= 128) {
+        // 1000 rows of bf16: of 16384 values 36 us, in the loop 50; of 32768 82 and 93; of 20480 (a warp then holds two or three chunks) 63 and 64.  f32 rows
+        // would spill: 58 and 56 at 16384.
+        if constexpr (sizeof(T) == 2) {
+            while ((4 << wl) < nch) ++wl;
+            e = launch_pdl(add_quantize_regs_kernel<T, 4, 1024>, dim3((unsigned)a.M), dim3(32u << wl), 0, s, a, p, wl);
+        }
     } else {
         e = launch_pdl(add_quantize_kernel<T>, dim3((unsigned)a.M), dim3(256), 0, s, a, p);
     }
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(Plane p, int64_t M, int
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], d[j]);
-            store8(y + m * ys + (int64_t)(c0 + j) * 256 + lane * 8, pack8(v, T()));
+            store8_row(y + m * ys + (int64_t)(c0 + j) * 256 + lane * 8, pack8(v, T()), lane);
         }
 }
 

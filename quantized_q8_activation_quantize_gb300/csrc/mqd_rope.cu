@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopePlan plan, Ro
 }  // namespace
 
 int launch_rope(const RopePlan &plan, RopeRows r, int dtype, const int32_t *pos, cudaStream_t s) {
-    r.per_block = r.n_tokens <= 4 * sm_count() ? 1 : kRopePairs / plan.half < 4 ? kRopePairs / plan.half : 4;
+    r.per_block = rope_tokens(plan, r);
     const dim3 grid((unsigned)((r.n_tokens + r.per_block - 1) / r.per_block)), block(kRopeThreads);
     const bool wide = rope_wide(plan, r);
     cudaError_t e = dtype == MQD_F32   ? launch_pdl(rope_kernel<float, 4>, grid, block, 0, s, plan, r, pos)

@@ -527,6 +527,49 @@ def test_select_rows_past_32_bits_and_heads_of_one_row():
     check_select(logits[:1].expand(3, -1).contiguous(), torch.tensor([[-1.0, -1.0, -1.0]], device="cuda"), 9)      # every score three times
 
 
+def test_tensors_side_by_side_in_one_buffer():
+    import torch
+    M, H, D = 9, 3, 64
+    K = 2 * 256
+    both = torch.randn((M, 2 * K), device="cuda")
+    x, h = both[:, :K], both[:, K:]
+    res, w = torch.randn((M, K), device="cuda"), torch.ones(K, device="cuda")
+    want, kept = x + res, x.clone()
+    plane, plain = B.alloc_plane(M, K), B.alloc_plane(M, K)
+    dec.mqd_add_quantize_q8(x, res, h, w, 1e-6, B.PLANE_ALL, plane)
+    B.mq_quantize_q8(want, M, K, w, 1e-6, plain)
+    sync()
+    assert torch.equal(h, want) and torch.equal(x, kept)
+    assert all(torch.equal(a, b) for a, b in zip(B.plane_views(plane, M, K), B.plane_views(plain, M, K)))
+    rows = torch.randn((M, 2 * H, D), device="cuda")
+    x, out = rows[:, :H], rows[:, H:]
+    kept = x.clone()
+    pos = np.arange(M, dtype=np.int32) * 77
+    dec.mqd_rope(dec.rope_plan(D), x, out, dev(pos))
+    sync()
+    assert torch.equal(x, kept)
+    check_turned(out, kept, pos, dec.mqd_rope_turns(D), D, False, 1.0, "f32")
+    with pytest.raises(B.MQError):
+        dec.mqd_add_quantize_q8(both[:, 8:K + 8], res, both[:, :K], w, 1e-6, B.PLANE_ALL, plane)
+    with pytest.raises(B.MQError):
+        dec.mqd_rope(dec.rope_plan(D), rows[:, :H + 1], rows[:, H - 1:], dev(pos))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M, K", [(5, 9216), (2, 16384), (3, 24832), (7, 32768), (3, 33024), (1, 49408)])
+def test_add_of_long_rows_in_place(M, K, dtype):
+    import torch
+    t = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    x, res, w = torch.randn((M, K), device="cuda").to(t), torch.randn((M, K), device="cuda").to(t), 1 + 0.1 * torch.randn(K, device="cuda")
+    want = (x.float() + res.float()).to(t)
+    plane, plain = B.alloc_plane(M, K), B.alloc_plane(M, K)
+    dec.mqd_add_quantize_q8(x, res, x, w, 1e-5, B.PLANE_ALL, plane)
+    B.mq_quantize_q8(want.float(), M, K, w, 1e-5, plain)
+    sync()
+    assert torch.equal(x, want)
+    assert all(torch.equal(a, b) for a, b in zip(B.plane_views(plane, M, K), B.plane_views(plain, M, K)))
+
+
 def test_rope_of_one_head_for_six():
     import torch
     x = torch.randn((5, 1, 64), device="cuda")
