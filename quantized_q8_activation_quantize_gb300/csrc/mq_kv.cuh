@@ -154,6 +154,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *x) {
 __device__ __forceinline__ float code_value(uint32_t w, int e) {
     return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + e)) - 8388736.0f;              // byte e, minus 128
 }
+__device__ __forceinline__ uint64_t code_values(uint32_t w, int e) {       // of bytes e and e + 1
+    return f2_add(f2_pack(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + e)), __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7541 + e))),
+                  f2_pack(-8388736.0f, -8388736.0f));
+}
 __device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));

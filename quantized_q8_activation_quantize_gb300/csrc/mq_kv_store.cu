@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(TIN) == 4 ? 2 : 3) kv_a
 constexpr int kReadTokens = 16, kReadThreads = 256;
 
 // One CTA per 16 rows of the output, a warp per row and some of its 2 H vectors (half, head) at a time: their loads fly together.  Moves 5
-// (f32) or 3 bytes a value.  A lane takes CPL codes: 4, or where 16-byte stores of 16-bit values fit 8.
+// (f32) or 3 bytes a value: 40960 tokens of 8 heads of 128 at 6.3 and 6.1 TB/s (66 and 41 us).  A lane takes CPL codes: 4, or where 16-byte stores of 16-bit values
+// fit 8.  32 rows a CTA: 67 and 41, and 64 tokens 5.2 for 3.6.
 template <typename TOUT, int D, int CPL>
-__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows rows, TOUT *k, int64_t kt, int64_t kh, TOUT *v,
+__global__ void __launch_bounds__(kReadThreads, 3) kv_read_kernel(KvView c, KvRows rows, TOUT *k, int64_t kt, int64_t kh, TOUT *v,
                                                                int64_t vt, int64_t vh, const int32_t *start, unsigned int *err) {
     constexpr int LPR = D / CPL, RPW = 32 / LPR, B = 2 * CPL / RPW, VECS = RPW * B;    // lanes per vector, vectors per load, loads in flight
     __shared__ const uint8_t *s_slab[kReadTokens];
@@ -217,40 +218,43 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvView c, KvRows 
         }
     }
     __syncthreads();
-    const int spp = c.T / kKB;
+    const int spp = c.T / kKB, step = RPW * c.T * D;
     for (int t = warp; t < nt; t += kReadThreads / 32) {
         const uint8_t *slab = s_slab[t];
-        const int slot = s_slot[t];
+        const int slot = s_slot[t], sub = lane / LPR;
+        const uint8_t *src = slab + ((int64_t)sub * c.T + slot) * D + CPL * quad;
+        const float *scale = reinterpret_cast<const float *>(slab + c.off_s) + sub * spp + slot / kKB;
+        TOUT *to_k = k + (t0 + t) * kt + sub * kh + CPL * quad, *to_v = v + (t0 + t) * vt + (sub - c.H) * vh + CPL * quad;
         for (int v0 = 0; v0 < heads; v0 += VECS) {
             uint32_t w[B][CPL / 4];
             float d[B];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                const int vec = v0 + i * RPW + lane / LPR;
                 d[i] = 0.0f;
 #pragma unroll
                 for (int q = 0; q < CPL / 4; ++q) w[i][q] = 0x80808080u;
-                if (slab != nullptr && vec < heads) {
+                if (slab != nullptr && v0 + i * RPW + sub < heads) {
                     // K of every head, then V of every head: one run of vectors
-                    const uint8_t *src = slab + ((int64_t)vec * c.T + slot) * D + CPL * quad;
                     if constexpr (CPL == 8) {
                         const uint2 two = *reinterpret_cast<const uint2 *>(src);
                         w[i][0] = two.x, w[i][1] = two.y;
                     } else {
                         w[i][0] = *reinterpret_cast<const uint32_t *>(src);
                     }
-                    d[i] = reinterpret_cast<const float *>(slab + c.off_s)[vec * spp + slot / kKB];
+                    d[i] = *scale;
                 }
+                src += step, scale += RPW * spp;
             }
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                const int vec = v0 + i * RPW + lane / LPR, half = vec >= c.H, h = vec - half * c.H;
-                TOUT *dst = half ? v : k;
-                if (vec >= heads || dst == nullptr) continue;
-                dst += (t0 + t) * (half ? vt : kt) + h * (half ? vh : kh) + CPL * quad;
+                const int vec = v0 + i * RPW + sub;
+                const bool half = vec >= c.H;
+                TOUT *dst = half ? to_v : to_k;
+                to_k += RPW * kh, to_v += RPW * vh;
+                if (vec >= heads || (half ? v : k) == nullptr) continue;
                 float x[CPL];
 #pragma unroll
-                for (int e = 0; e < CPL; ++e) x[e] = __fmul_rn(code_value(w[i][e / 4], e % 4), d[i]);
+                for (int e = 0; e < CPL; e += 2) f2_unpack(f2_mul(code_values(w[i][e / 4], e % 4), f2_pack(d[i], d[i])), x[e], x[e + 1]);
                 if constexpr (CPL == 8) store8(dst, pack8(x, TOUT()));
                 else store4(dst, x);
             }
@@ -279,7 +283,7 @@ int read_t(const KvView &c, const KvRows &r, void *k, int64_t kt, int64_t kh, vo
     const dim3 grid((unsigned)((r.n_tokens + kReadTokens - 1) / kReadTokens));
     auto fn = c.D == 128 ? kv_read_kernel<T, 128, 4> : kv_read_kernel<T, 64, 4>;
     if constexpr (sizeof(T) == 2) {
-        // 41k tokens of 8 heads of 128 to bf16: 8 codes a lane 69 us, 4 81
+        // 40960 tokens of 8 heads of 128 to bf16: 8 codes a lane 41 us, 4 50; 64 tokens 3.6 and 4.3
         if (aligned(k, 16) && aligned(v, 16) && (kt % 8 | kh % 8 | vt % 8 | vh % 8) == 0) fn = c.D == 128 ? kv_read_kernel<T, 128, 8> : kv_read_kernel<T, 64, 8>;
     }
     return cuda_error(launch_pdl(fn, grid, dim3(kReadThreads), 0, s, c, r, static_cast<T *>(k), kt, kh, static_cast<T *>(v), vt,

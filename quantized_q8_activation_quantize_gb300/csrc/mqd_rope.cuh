@@ -151,7 +151,7 @@ inline bool rope_wide(const RopePlan &p, const RopeRows &r) {
 }
 
 // Tokens of a block: of few tokens as many as its threads turn in one go, else four.  32 heads of 128, bf16: 24 tokens one a block 2.1 us, four 3.3; 304 2.4 and 3.6;
-// 608 3.6 and 3.5; 2432 9.2 and 9.6.  8 heads (four in one go): 304 tokens 2.1, one a block 2.3; 608 2.2 and 2.8.  20000 tokens of 28 heads: 25.3 four, 26.0 two, 27.9 eight.
+// 608 3.6 and 3.5; 2432 9.2 and 9.6.  8 heads (four in one go): 304 tokens 2.1, one a block 2.3; 608 2.2 and 2.8.  7001 tokens of 40 heads: 25.3 four, 26.0 two, 27.9 eight.
 inline int rope_tokens(const RopePlan &p, const RopeRows &r) {
     const int pieces = r.heads * (r.dim / (rope_wide(p, r) ? 16 : 8)), most = kRopePairs / p.half < 4 ? kRopePairs / p.half : 4;
     const int go = kRopeThreads / pieces < 1 ? 1 : kRopeThreads / pieces;
