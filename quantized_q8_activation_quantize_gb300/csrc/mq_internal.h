@@ -124,6 +124,6 @@ void *tensor_map_encoder();
 constexpr int kAttrSlotSmall = kAttrSlotSwiglu + 8;
 // attribute slots of the cache's attention: 2 * dtype + (head_dim == 128), 8 per kernel
 constexpr int kAttrSlotKv = kAttrSlotSmall + 16;
-constexpr int kAttrSlotReorder = kAttrSlotKv + 32, kAttrSlotBeam = kAttrSlotReorder + 1;
+constexpr int kAttrSlotReorder = kAttrSlotKv + 32, kAttrSlotBeam = kAttrSlotReorder + 1, kAttrSlotRope = kAttrSlotBeam + 4;
 
 }  // namespace mq

@@ -4,6 +4,7 @@
 // Small calls are one launch: the grid's first blocks take the queries (a few tokens of all heads each, mqd_rope.cuh), the others the keys and values.  Large ones
 // are two, since the queries need half the registers.  The keys are turned in f32 and never rounded before their codes.
 #include <cfloat>
+#include <type_traits>
 
 #include "mqd_rope.cuh"
 
@@ -11,6 +12,16 @@ namespace mq {
 namespace {
 
 constexpr int kTurnThreads = kRopeThreads, kTurnWarps = 4;      // warps of a vector: 8 slots each, two vectors at a time
+
+// Stages of the ring that keys and values pass, one asked for while the other is worked on, and their bytes.  40960 tokens of 8 heads: bf16 67 us, three stages
+// 68, four 70, six 81 (what the ring takes the L1 lacks); f32 78, three stages 110.  The next pair in registers: 86 and 102.
+constexpr int kTurnStages = 2;
+template <typename T, int D>
+constexpr int kTurnStage = kKB * D * 2 * (int)sizeof(T);
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, bool full) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(full ? BYTES : 0) : "memory");
+}
 
 struct TurnedRows {
     const void *k, *v;
@@ -24,7 +35,7 @@ struct TurnedRows {
 // U(b) = begin(b) / 32 + 2 b, as in mqkv_append, whose arithmetic this is.
 template <typename T, int D>
 __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &rows, int64_t u, int y0, const RopePlan &plan, const int32_t *pos, const TurnedRows &in,
-                                              float *s_cos, float *s_sin, unsigned int *err) {
+                                              float *s_cos, float *s_sin, uint8_t *s_ring, unsigned int *err) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, IT = kKB / kTurnWarps / RPW;     // lanes per row, rows per warp and step, steps
     __shared__ float s_amax[2][8];
     int b;
@@ -69,30 +80,23 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
     const bool turns = j < quads;
     const int ka = plan.interleaved ? 8 * j : turns ? 4 * j : 2 * plan.half + 8 * (j - quads), kz = !plan.interleaved && turns ? ka + plan.half : ka + 4;
 
-    Raw4<T> raw[IT][2];
-    auto ask = [&](int y) {
+    // the vectors of pair y on their way into this thread's own slots of a stage of shared memory (so no barriers); zeros where a slot has no new token
+    uint8_t *stage = s_ring + threadIdx.x * sizeof(Raw4<T>);
+    auto ask = [&](int y, int s) {
         const int vec = 2 * y + team, half = vec >= c.H, h = vec - half * c.H, a = half ? 8 * j : ka, z = half ? 8 * j + 4 : kz;
-        const int64_t st = half ? in.vt : in.kt;
+        const int64_t st = half ? in.vt : in.kt, step = RPW * st;
         const T *src = static_cast<const T *>(half ? in.v : in.k) + h * (half ? in.vh : in.kh) + (row0 + r0) * st;
-        const int64_t step = RPW * st;
-        if (whole) {
+        uint32_t to = smem_u32(stage + s * kTurnStage<T, D>);
 #pragma unroll
-            for (int i = 0; i < IT; ++i, src += step) {
-                raw[i][0] = *reinterpret_cast<const Raw4<T> *>(src + a);
-                raw[i][1] = *reinterpret_cast<const Raw4<T> *>(src + z);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < IT; ++i, src += step) {
-                raw[i][0].w = {}, raw[i][1].w = {};
-                if (r0 + i * RPW >= new0 && r0 + i * RPW < new1) {
-                    raw[i][0] = *reinterpret_cast<const Raw4<T> *>(src + a);
-                    raw[i][1] = *reinterpret_cast<const Raw4<T> *>(src + z);
-                }
-            }
+        for (int i = 0; i < IT; ++i, src += step, to += 2 * kTurnThreads * sizeof(Raw4<T>)) {
+            const bool in_it = whole || (r0 + i * RPW >= new0 && r0 + i * RPW < new1);
+            const T *from = in_it ? src : static_cast<const T *>(in.k);
+            copy_async<sizeof(Raw4<T>)>(to, from + a, in_it);
+            copy_async<sizeof(Raw4<T>)>(to + kTurnThreads * sizeof(Raw4<T>), from + z, in_it);
         }
     };
-    ask(y0);
+    ask(y0, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
     if (2 * y0 < c.H) {
         for (int i = threadIdx.x; i < fresh * plan.half; i += kTurnThreads) {
             const int slot = i / plan.half;
@@ -102,13 +106,19 @@ __device__ __forceinline__ void append_turned(const KvView &c, const KvRows &row
         }
         __syncthreads();
     }
+    int slot = 0;
 #pragma unroll 1
     for (int y = y0; y < y1; ++y) {
         const int vec = 2 * y + team, half = vec >= c.H, a = half ? 8 * j : ka, z = half ? 8 * j + 4 : kz;
+        if (y + 1 < y1) ask(y + 1, 1 - slot);                                   // (the stage that was read last)
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kTurnStages - 1) : "memory");
         float x[IT][8];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) unpack4(raw[i][0], x[i]), unpack4(raw[i][1], x[i] + 4);
-        if (y + 1 < y1) ask(y + 1);
+        for (int i = 0; i < IT; ++i) {
+            const Raw4<T> *raw = reinterpret_cast<const Raw4<T> *>(stage + slot * kTurnStage<T, D>) + i * 2 * kTurnThreads;
+            unpack4(raw[0], x[i]), unpack4(raw[kTurnThreads], x[i] + 4);
+        }
+        slot = 1 - slot;
         uint8_t *codes = slab + (int64_t)vec * c.T * D + (int64_t)slot0 * D;    // (K of every head, then V of every head)
         float *scale = reinterpret_cast<float *>(slab + c.off_s) + vec * (c.T / kKB) + slot0 / kKB;
         float d_old = new0 > 0 ? *scale : 0.0f;                                 // slots of earlier tokens share the block
@@ -238,6 +248,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) kv_rope_rows_kernel(KvView c,
 template <typename T, int W, int D>
 __global__ void __launch_bounds__(kTurnThreads, 2) kv_append_rope_kernel(KvView c, KvRows rows, int gy, RopePlan plan, const int32_t *pos, RopeRows q,
                                                                                              unsigned q_blocks, TurnedRows in, unsigned int *err) {
+    extern __shared__ __align__(16) uint8_t s_ring[];
     __shared__ __align__(16) float s_cos[kKB * D / 2], s_sin[kKB * D / 2];      // (kRopeTokens * D / 2 at most for queries)
     grid_dep_launch();
     grid_dep_wait();
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kTurnThreads, 2) kv_append_rope_kernel(KvView 
         return;
     }
     const unsigned unit = blockIdx.x - q_blocks;
-    append_turned<T, D>(c, rows, unit / gy, (int)(unit % gy) * in.each, plan, pos, in, s_cos, s_sin, err);
+    append_turned<T, D>(c, rows, unit / gy, (int)(unit % gy) * in.each, plan, pos, in, s_cos, s_sin, s_ring, err);
 }
 
 template <typename T, int W>
@@ -268,7 +279,10 @@ int append_rope_t(const KvView &c, const KvRows &r, const RopePlan &plan, const 
         if (rc != MQ_OK) return rc;
     }
     auto fn = c.D == 128 ? kv_append_rope_kernel<T, W, 128> : kv_append_rope_kernel<T, W, 64>;
-    return cuda_error(launch_pdl(fn, dim3((unsigned)blocks), dim3(kTurnThreads), 0, s, c, r, gy, plan, pos, q, (unsigned)q_blocks, in, err), "mqkv_append_rope launch");
+    const int smem = kTurnStages * (c.D == 128 ? kTurnStage<T, 128> : kTurnStage<T, 64>);
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), smem, kAttrSlotRope + (sizeof(T) == 4 ? 0 : std::is_same_v<T, __half> ? 2 : 6) + (W == 8 ? 2 : 0) + (c.D == 128));
+    if (rc != MQ_OK) return rc;
+    return cuda_error(launch_pdl(fn, dim3((unsigned)blocks), dim3(kTurnThreads), smem, s, c, r, gy, plan, pos, q, (unsigned)q_blocks, in, err), "mqkv_append_rope launch");
 }
 
 }  // namespace
