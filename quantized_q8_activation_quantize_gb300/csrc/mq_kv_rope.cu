@@ -2,7 +2,7 @@
 // with the values.
 //
 // Small calls are one launch: the grid's first blocks take the queries (a few tokens of all heads each, mqd_rope.cuh), the others the keys and values.  Large ones
-// are two, since the queries need half the registers.  The keys are turned in f32 and never rounded before their codes.
+// are two, since the queries need half the registers (five blocks an SM; 38376 tokens of 32 heads beside the append and the read 207 us, with four 209, with six 218).  The keys are turned in f32 and never rounded before their codes.
 #include <cfloat>
 #include <type_traits>
 
@@ -30,7 +30,9 @@ struct TurnedRows {
 };
 
 // One block of 32 slots of a sequence and `each` pairs of its 2 H vectors (half, head), from pair y0 on: the angles once for all heads, then two vectors at a time, four
-// warps each, all of a lane's values in registers between the maximum and the codes, the next vectors' asked for before these are worked on.  A lane holds two quads of a row that
+// warps each, all of a lane's values in registers between the maximum and the codes, the next vectors on their way into shared memory.  Bound by instructions (17 a value) at 16
+// warps an SM: 40960 tokens of 8 heads of 128 take 67 us from bf16 (3.7 TB/s) and 78 from f32 (5.4 TB/s); one vector at a time by eight warps, half the registers, 91 and 105
+// for 86 and 102 then.  A lane holds two quads of a row that
 // are turned with one another (quads j and j + half / 4, or neighbours), so that a turn needs no exchange.  Unit u belongs to the last sequence b with U(b) <= u,
 // U(b) = begin(b) / 32 + 2 b, as in mqkv_append, whose arithmetic this is.
 template <typename T, int D>
@@ -245,6 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) kv_rope_rows_kernel(KvView c,
     rope_rows<T, W>(c, rows, plan, pos, q, blockIdx.x, s_cos, s_sin);
 }
 
+// (three blocks an SM spill: 75 us for 68 from bf16)
 template <typename T, int W, int D>
 __global__ void __launch_bounds__(kTurnThreads, 2) kv_append_rope_kernel(KvView c, KvRows rows, int gy, RopePlan plan, const int32_t *pos, RopeRows q,
                                                                                              unsigned q_blocks, TurnedRows in, unsigned int *err) {
@@ -280,7 +283,8 @@ int append_rope_t(const KvView &c, const KvRows &r, const RopePlan &plan, const 
     }
     auto fn = c.D == 128 ? kv_append_rope_kernel<T, W, 128> : kv_append_rope_kernel<T, W, 64>;
     const int smem = kTurnStages * (c.D == 128 ? kTurnStage<T, 128> : kTurnStage<T, 64>);
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), smem, kAttrSlotRope + (sizeof(T) == 4 ? 0 : std::is_same_v<T, __half> ? 2 : 6) + (W == 8 ? 2 : 0) + (c.D == 128));
+    const int slot = kAttrSlotRope + (sizeof(T) == 4 ? 0 : std::is_same_v<T, __half> ? 2 : 6) + (W == 8 ? 2 : 0) + (c.D == 128);
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(fn), smem, slot);
     if (rc != MQ_OK) return rc;
     return cuda_error(launch_pdl(fn, dim3((unsigned)blocks), dim3(kTurnThreads), smem, s, c, r, gy, plan, pos, q, (unsigned)q_blocks, in, err), "mqkv_append_rope launch");
 }

@@ -75,8 +75,10 @@ __device__ __forceinline__ void norm8(float (&v)[8], float r, const float *w) {
 }
 
 // One row per group of WT = 2^wt_log2 warps, warp g of it holding chunks g, g + WT, .. of 256 values (at most NC; lane l: values
-// 8 l .. 8 l + 7 of each).  Bound by HBM for many rows: 333 rows .. thousands reach 5.5 TB/s of their algorithmic bytes (2048 rows of bf16, 4096 wide ADDFIG).  A quarter
-// of the registers of an SM (16-bit) or a third (f32) per block of eight warps, so that one group's sums hide under the others' loads.
+// 8 l .. 8 l + 7 of each).  Many rows are bound by HBM: 3314 rows of 3584 f32 values with all sections 26.6 us, 6.9 TB/s of the bytes that they move; 9001 rows of 8192 bf16
+// values 111 us, 6.3 TB/s; 4000 of 4096 33 us, 4.8 TB/s (scales and sums lie block-major, so that a row's are single words in as many sectors: 4% without their
+// stores).  Three blocks of eight warps an SM (f32) or four (16 bits), so that one row's sums hide under the others' loads; rows that follow one another in
+// a resident block, the next on its way, took 56 us for 40 and 175 for 165 (with the plane read back).
 template <typename T, int NC, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(T) == 4 ? 3 : 4) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {
     __shared__ float2 s_part[32];
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(T) == 4 ? 
 }
 
 // Rows too long for registers: a block per row, h written in the first pass and read again (from L2, by the warp that wrote it)
-// in the second.  4000 rows of 16384 f32 values take 185 us (the floor's bytes at 5.6 TB/s ADDLONG).
+// in the second.  4000 rows of 16384 f32 values take 184 us, 5.5 TB/s of the bytes without that second read.
 template <typename T>
 __global__ void __launch_bounds__(256) add_quantize_kernel(AddQuantize a, Plane p) {
     __shared__ float2 s_part[8];
@@ -199,7 +201,7 @@ int add_quantize_t(const AddQuantize &a, const Plane &p, cudaStream_t s) {
 }
 
 // A warp per row and up to four chunks of 256 values; the eight rows of a block are neighbours, so that a sector of the block-major
-// scales serves all of them.
+// scales serves all of them.  Bound by HBM: 8192 rows of 4096 values from q16 to f32 31 us (6.5 TB/s), from q8 to bf16 17 us (6.0 TB/s).
 template <typename T, bool Q16>
 __global__ void __launch_bounds__(256) dequantize_kernel(Plane p, int64_t M, int64_t K, T *y, int64_t ys, int groups) {
     grid_dep_launch();
