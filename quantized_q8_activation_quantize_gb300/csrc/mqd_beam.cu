@@ -405,7 +405,7 @@ __device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *l
 // the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a few k as a rule, whose
 // ranks are counted again.  (Taking the best of all heads k times cost 300 clocks each.)
 constexpr int kJoinThreads = 512;      // with 40 registers: room beside the scan's blocks, so that it waits on its SM when they end.  4 rows 9.3 us, 256 threads 10.1, 1024 9.4;
-                                       // 96 rows in groups of 16, two candidates each, 18.7, 22.2, 17.3; 128 in groups of 4 22.3, 22.4, 22.6
+                                       // 96 rows in groups of 16 (32 candidates) 18.7, 22.2, 17.3; 128 in groups of 4 22.3, 22.4, 22.6
 __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
                                                                  int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
                                                                  int32_t *next_token) {
