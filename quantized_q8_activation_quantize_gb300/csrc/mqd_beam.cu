@@ -4,10 +4,10 @@
 //
 // Two kernels.  The scan reads the logits once: a block takes a piece of a row, keeps the sum of exponentials relative to the largest value met
 // (online: a thread rescales its sum when a tile brings a larger one) and, beside it, the piece's best n_cand values, found by a threshold
-// that only few values pass.  The join has a block per group: the rows' sums, then ranks, first of the lists' heads and then of the entries that are left.
+// that only few values pass.  The join has a block per group: the rows' sums, then ranks, of many lists first of their heads and then of the entries that are left.
 // Within a row the order of the scores is that of the logits, so only the join needs the sums; it compares f32 pairs, 48 bits.
 //
-// 128 rows of 152064 f32 logits (77.9 MB) in groups of four, eight candidates: 22.3 us in a graph; their bytes alone are 11.5 at the copy rate.  What is above it: a first tile's
+// 128 rows of 152064 f32 logits (77.9 MB) in groups of four, eight candidates: 21.4 us in a graph; their bytes alone are 11.5 at the copy rate.  What is above it: a first tile's
 // threshold and list before any other tile counts, the ends of the pieces, and the join's chain (sums, heads, ranks).  4 rows: 9.3 us, the two chains.
 #include <cfloat>
 #include <type_traits>
@@ -401,11 +401,17 @@ __device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *l
     return in ? rank : k;
 }
 
+constexpr int kJoinThreads = 512;      // with 40 registers: room beside the scan's blocks, so that it waits on its SM when they end.  4 rows 9.3 us, 256 threads 10.1, 1024 9.4;
+                                       // 96 rows in groups of 16 (32 candidates) 18.7, 22.2, 17.3
+// Whether the join ranks every entry of a group's lists at once, a thread holding one: where four lanes of the block have each, or where no list would be left out.  32
+// groups of 12 lists of 8: 21.4 us and 22.5 by heads first; one of 8 of 2 6.1 and 7.1; 32 of 16 of 32 23.5 and 25.1; but one of 32 of 8 8.4 and 7.5.
+__host__ __device__ inline bool join_few(int lists, int k) { return lists * k <= kJoinThreads / 4 || (lists <= k && lists * k <= kJoinThreads); }
+// entries that the join ranks at the end
+__host__ __device__ inline int join_room(int lists, int k) { return ((join_few(lists, k) ? lists : k < lists ? k : lists) * k + 4) & ~3; }
+
 // A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted; lists come in
 // the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a few k as a rule, whose
 // ranks are counted again.  (Taking the best of all heads k times cost 300 clocks each.)
-constexpr int kJoinThreads = 512;      // with 40 registers: room beside the scan's blocks, so that it waits on its SM when they end.  4 rows 9.3 us, 256 threads 10.1, 1024 9.4;
-                                       // 96 rows in groups of 16 (32 candidates) 18.7, 22.2, 17.3; 128 in groups of 4 22.3, 22.4, 22.6
 __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
                                                                  int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
                                                                  int32_t *next_token) {
@@ -421,12 +427,15 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
     const int64_t g = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P, n4 = (lists + 3) & ~3;
     const float2 *list = ws.list + g * lists * k;
+    const bool few = join_few(lists, k);
     float head[kMaxLists / kJoinThreads];
+    float2 own;                                             // of few entries, a thread's
 #pragma unroll
     for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
         const int l = threadIdx.x + i * kJoinThreads;
         if (l < lists) s_len[l] = ws.piece[g * lists + l].n, head[i] = list[l * k].x;   // (not written where there is none)
     }
+    if (few && threadIdx.x < lists * k) own = list[threadIdx.x];
     if (threadIdx.x == 0) s_n = 0, s_lists = 0;
     for (int b = warp; b < B; b += warps) {                 // a warp per row: its sum of exponentials
         const float4 *piece = reinterpret_cast<const float4 *>(ws.piece + (g * B + b) * P);
@@ -459,47 +468,58 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
         }
     }
     __syncthreads();
-    uint32_t *his = s_keys, *los = his + n4;
+    const int room = join_room(lists, k);
+    uint32_t *his = s_keys, *los = his + n4, *ehi = few ? s_keys : los + n4, *elo = ehi + room, *etoken = elo + room, *eplace = etoken + room;  // (place: list, and where in it)
+    int n, all;                                             // entries, and how many of them are candidates
+    if (few) {
+        n = lists * k;
+        const int from = threadIdx.x / k, of = from / P, j = threadIdx.x - from * k;
+        const bool in = (int)threadIdx.x < n && j < s_len[from];
+        const uint64_t y = in ? score_key(s_cum[of], own.x, s_lh[of], s_ll[of]) : 0;
+        if ((int)threadIdx.x < n) ehi[threadIdx.x] = (uint32_t)(y >> 32), elo[threadIdx.x] = (uint32_t)y, etoken[threadIdx.x] = __float_as_uint(own.y), eplace[threadIdx.x] = from * kMaxCand + j;
+        all = __syncthreads_count(in);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
-        const int l = threadIdx.x + i * kJoinThreads, of = l < lists ? l / P : 0;
-        const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head[i], s_lh[of], s_ll[of]) : 0;
-        if (l < n4) his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
-        const int at = min(i, n4 - 1);
-        const int rank = rank_below(his, los, n4, n4, at, k, [](int a) { return (uint32_t)a; });
-        if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
-        s_list[atomicAdd(&s_lists, 1)] = i;
-        if (rank == k - 1) s_bar[0] = his[i], s_bar[1] = los[i], s_bar[2] = (uint32_t)i;
-    }
-    __syncthreads();
-    const int left = s_lists, room = (k * min(k, lists) + 4) & ~3;
-    // the k-th head, where there are as many
-    const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
-    const int at_bar = left == k ? (int)s_bar[2] : lists;
-    uint32_t *ehi = los + n4, *elo = ehi + room, *etoken = elo + room, *eplace = etoken + room;        // (place: list, and where in it)
-    for (int i = warp; i < left; i += warps) {
-        const int from = s_list[i], of = from / P;
-        for (int j = lane; j < s_len[from]; j += 32) {
-            const float2 x = list[from * k + j];
-            const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]);
-            // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
-            if ((y > bar) | ((y == bar) & (from <= at_bar))) {
-                const int c = atomicAdd(&s_n, 1);
-                ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), eplace[c] = from * kMaxCand + j;
+        for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
+            const int l = threadIdx.x + i * kJoinThreads, of = l < lists ? l / P : 0;
+            const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head[i], s_lh[of], s_ll[of]) : 0;
+            if (l < n4) his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
+            const int at = min(i, n4 - 1);
+            const int rank = rank_below(his, los, n4, n4, at, k, [](int a) { return (uint32_t)a; });
+            if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
+            s_list[atomicAdd(&s_lists, 1)] = i;
+            if (rank == k - 1) s_bar[0] = his[i], s_bar[1] = los[i], s_bar[2] = (uint32_t)i;
+        }
+        __syncthreads();
+        const int left = s_lists;
+        // the k-th head, where there are as many
+        const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
+        const int at_bar = left == k ? (int)s_bar[2] : lists;
+        for (int i = warp; i < left; i += warps) {
+            const int from = s_list[i], of = from / P;
+            for (int j = lane; j < s_len[from]; j += 32) {
+                const float2 x = list[from * k + j];
+                const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]);
+                // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
+                if ((y > bar) | ((y == bar) & (from <= at_bar))) {
+                    const int c = atomicAdd(&s_n, 1);
+                    ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), eplace[c] = from * kMaxCand + j;
+                }
             }
         }
+        __syncthreads();
+        n = all = s_n;
     }
-    __syncthreads();
-    const int all = s_n, all4 = (all + 3) & ~3;
-    if (threadIdx.x < all4 - all) ehi[all + threadIdx.x] = 0;
+    const int all4 = (n + 3) & ~3;
+    if (threadIdx.x < all4 - n) ehi[n + threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x >> 2; i < (all4 + 7 & ~7); i += kJoinThreads / 4) {
         const int at = min(i, all4 - 1);
-        const int rank = rank_below(ehi, elo, all, all4, at, k, [&](int a) { return eplace[a]; });
-        if (i < all && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = (int)(eplace[i] / kMaxCand) / P, s_token[rank] = (int)etoken[i];
+        const int rank = rank_below(ehi, elo, n, all4, at, k, [&](int a) { return eplace[a]; });
+        if (i < n && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = (int)(eplace[i] / kMaxCand) / P, s_token[rank] = (int)etoken[i];
     }
     __syncthreads();
     if (warp != 0) return;
@@ -576,7 +596,7 @@ int launch_beam_select(int dtype, const void *logits, int64_t stride, int64_t n_
              : dtype == MQD_F16 ? launch_scan<__half>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 1, s)
                                 : launch_scan<__nv_bfloat16>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 2, s);
     if (rc != MQ_OK) return rc;
-    const int lists = B * ws.pieces, words = 2 * (lists + 3) + 4 * (k * (k < lists ? k : lists) + 4);
+    const int lists = B * ws.pieces, words = (join_few(lists, k) ? 0 : 2 * (lists + 3)) + 4 * join_room(lists, k);
     rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (2 * (kMaxLists + 3) + 4 * (kMaxCand * kMaxCand + 4)) * 4, kAttrSlotBeam + 3);
     if (rc != MQ_OK) return rc;
     const cudaError_t e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(kJoinThreads), words * 4, s, ws, B, scores, k, stop, cand_score, cand_row,
