@@ -4,7 +4,7 @@
 //
 // Two kernels.  The scan reads the logits once: a block takes a piece of a row, keeps the sum of exponentials relative to the largest value met
 // (online: a thread rescales its sum when a tile brings a larger one) and, beside it, the piece's best n_cand values, found by a threshold
-// that only few values pass.  The join has a block per group: the rows' sums, then ranks, of many lists first of their heads and then of the entries that are left.
+// that only few values pass.  The join has a block per group: the rows' sums, then ranks, of many lists first of their heads and then of the entries that are left, or mergers of the lists.
 // Within a row the order of the scores is that of the logits, so only the join needs the sums; it compares f32 pairs, 48 bits.
 //
 // 128 rows of 152064 f32 logits (77.9 MB) in groups of four, eight candidates: 21.4 us in a graph; their bytes alone are 11.5 at the copy rate.  What is above it: a first tile's
@@ -403,21 +403,72 @@ __device__ __forceinline__ int rank_below(const uint32_t *his, const uint32_t *l
 
 constexpr int kJoinThreads = 512;      // with 40 registers: room beside the scan's blocks, so that it waits on its SM when they end.  4 rows 9.3 us, 256 threads 10.1, 1024 9.4;
                                        // 96 rows in groups of 16 (32 candidates) 18.7, 22.2, 17.3
-// Whether the join ranks every entry of a group's lists at once, a thread holding one: where four lanes of the block have each, or where no list would be left out.  32
-// groups of 12 lists of 8: 21.4 us and 22.5 by heads first; one of 8 of 2 6.1 and 7.1; 32 of 16 of 32 23.5 and 25.1; but one of 32 of 8 8.4 and 7.5.
-__host__ __device__ inline bool join_few(int lists, int k) { return lists * k <= kJoinThreads / 4 || (lists <= k && lists * k <= kJoinThreads); }
-// entries that the join ranks at the end
-__host__ __device__ inline int join_room(int lists, int k) { return ((join_few(lists, k) ? lists : k < lists ? k : lists) * k + 4) & ~3; }
+// Whether the join ranks every entry of a group's lists by all others: where four lanes of the block have each.  32 groups of 12 lists of 8: 21.4 us, by heads first
+// 22.5; one of 8 of 2 6.1 and 7.1.
+__host__ __device__ inline bool join_few(int lists, int k) { return lists * k <= kJoinThreads / 4; }
+constexpr int kJoinRanked = 256;       // entries that it still ranks so after a choice of lists, in two rounds
+// words of its shared memory: keys and tokens of few entries; else the heads' keys where there are more lists than k, and two buffers of entries (keys, places)
+__host__ __device__ inline int join_heads(int lists, int k) { return lists > k ? lists + 3 & ~3 : 0; }
+inline int join_words(int lists, int k) {
+    const int merged = 6 * (lists < k ? lists : k) * k;
+    return join_few(lists, k) ? 4 * (lists * k + 4) : 2 * join_heads(lists, k) + (merged > 4 * kJoinRanked ? merged : 4 * kJoinRanked);
+}
 
-// A block per group.  The lists are sorted, so of the lists only the k with the best heads can hold one of the k best (every rank counted; lists come in
-// the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: k^2 entries at most, a few k as a rule, whose
-// ranks are counted again.  (Taking the best of all heads k times cost 300 clocks each.)
+// Merges `left` lists of up to k entries, those of list_of(0), list_of(1) .. , until the k best are in order: their scores, rows and tokens; returns how many there are
+template <typename ListOf>
+__device__ __forceinline__ int join_merge(uint32_t *buffers, int room, int left, int k, int P, ListOf list_of, const float2 *list, const int *s_len, const float *s_cum, const float *s_lh,
+                                          const float *s_ll, float *s_score, int *s_row, int *s_token) {
+    uint64_t *key = reinterpret_cast<uint64_t *>(buffers), *key2 = key + room;
+    uint32_t *place = reinterpret_cast<uint32_t *>(key2 + room), *place2 = place + room;        // list, and where in it
+    for (int i = threadIdx.x; i < left * k; i += kJoinThreads) {
+        const int q = i / k, j = i - q * k, from = list_of(q), of = from / P;
+        key[i] = j < s_len[from] ? score_key(s_cum[of], list[from * k + j].x, s_lh[of], s_ll[of]) : 0;
+        place[i] = from * kMaxCand + j;
+    }
+    __syncthreads();
+    for (int s = 1, runs = left; s < left; s *= 2, runs = (runs + 1) / 2) {         // list a of this round lies at slot a * s
+        for (int i = threadIdx.x; i < runs * k; i += kJoinThreads) {
+            const int a = i / k, j = i - a * k;
+            const uint64_t x = key[a * s * k + j];
+            int lo = 0;
+            if ((a ^ 1) < runs) {
+                // before it in the other list: what is better, of an earlier list what is equal too
+                const uint64_t *other = key + (a ^ 1) * s * k, bar = x - (a & 1);
+                for (int hi = k - j; lo < hi;) {        // (past k - j it is out in any case)
+                    const int mid = (lo + hi) >> 1;
+                    if (other[mid] > bar) lo = mid + 1;
+                    else hi = mid;
+                }
+            }
+            if (j + lo < k && (x != 0 || (a & 1) == 0)) {       // (an earlier list's room without an entry is what is left)
+                const int to = (a & ~1) * s * k + j + lo;
+                key2[to] = x, place2[to] = place[a * s * k + j];
+            }
+        }
+        __syncthreads();
+        uint64_t *const old = key;
+        uint32_t *const oldp = place;
+        key = key2, key2 = old, place = place2, place2 = oldp;
+    }
+    const bool in = (int)threadIdx.x < k && key[threadIdx.x] != 0;
+    if (in) {
+        const int at = place[threadIdx.x], from = at / kMaxCand;
+        s_score[threadIdx.x] = from_ordered((uint32_t)(key[threadIdx.x] >> 32)), s_row[threadIdx.x] = from / P;
+        s_token[threadIdx.x] = __float_as_int(list[from * k + at % kMaxCand].y);
+    }
+    return __syncthreads_count(in);
+}
+
+// A block per group.  Few entries are ranked each by all others.  Of more lists, which are sorted, only the k with the best heads can hold one of the k best (the heads' ranks
+// are counted; lists come in the order of beams and tokens, which decides between equals), and of those only what is not below the k-th head: a few k entries as a rule, which are
+// ranked.  Many equal scores, or many candidates of few lists, can leave k^2: then the lists merge in pairs of neighbours, the k best of each pair, until one is left; an entry's
+// place is its own and what a binary search finds before it in the other list.  (Ranks alone took 143 us for 64 candidates of 4 rows of 50000 bf16 logits, 16.5 so, and 25 for 32
+// of 152 in pairs, 20.7 so; mergers alone 37 for 27 for 64 of 16 rows of 152064 in one group, 10.7 for 9.6 for 8 of 4.  The best of all heads k times cost 300 clocks each.)
 __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, int B, const float *scores, int k, int stop, float *cand_score_out,
                                                                  int32_t *cand_row, int32_t *cand_token, float *next_score, int32_t *next_row,
                                                                  int32_t *next_token) {
-    // of the heads, then of the entries (k * min(k, lists) of them): the upper halves of the keys, to compare, padded with zeros; the lower halves; the entries' places
-    extern __shared__ __align__(16) uint32_t s_keys[];
-    __shared__ uint32_t s_bar[3];
+    extern __shared__ __align__(16) uint32_t s_keys[];      // (join_words)
+    __shared__ uint32_t s_take[kMaxLists / 32], s_bar[3];   // lists that may hold one of the best; the worst of their heads, and its list
     __shared__ float s_score[kMaxCand];
     __shared__ int s_row[kMaxCand], s_token[kMaxCand], s_list[kMaxCand], s_n, s_lists;
     __shared__ float s_cum[kMaxCand], s_lh[kMaxCand], s_ll[kMaxCand];
@@ -425,7 +476,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
     grid_dep_launch();
     grid_dep_wait();
     const int64_t g = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P, n4 = (lists + 3) & ~3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32, P = ws.pieces, lists = B * P;
     const float2 *list = ws.list + g * lists * k;
     const bool few = join_few(lists, k);
     float head[kMaxLists / kJoinThreads];
@@ -436,6 +487,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
         if (l < lists) s_len[l] = ws.piece[g * lists + l].n, head[i] = list[l * k].x;   // (not written where there is none)
     }
     if (few && threadIdx.x < lists * k) own = list[threadIdx.x];
+    if (threadIdx.x < kMaxLists / 32) s_take[threadIdx.x] = 0;
     if (threadIdx.x == 0) s_n = 0, s_lists = 0;
     for (int b = warp; b < B; b += warps) {                 // a warp per row: its sum of exponentials
         const float4 *piece = reinterpret_cast<const float4 *>(ws.piece + (g * B + b) * P);
@@ -468,62 +520,85 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
         }
     }
     __syncthreads();
-    const int room = join_room(lists, k);
-    uint32_t *his = s_keys, *los = his + n4, *ehi = few ? s_keys : los + n4, *elo = ehi + room, *etoken = elo + room, *eplace = etoken + room;  // (place: list, and where in it)
-    int n, all;                                             // entries, and how many of them are candidates
+    int got;                                                // candidates
     if (few) {
-        n = lists * k;
-        const int from = threadIdx.x / k, of = from / P, j = threadIdx.x - from * k;
+        const int n = lists * k, n4 = (n + 3) & ~3, from = threadIdx.x / k, of = from / P, j = threadIdx.x - from * k;
+        uint32_t *hi = s_keys, *lo = hi + n4;               // (the upper halves padded with zeros)
         const bool in = (int)threadIdx.x < n && j < s_len[from];
         const uint64_t y = in ? score_key(s_cum[of], own.x, s_lh[of], s_ll[of]) : 0;
-        if ((int)threadIdx.x < n) ehi[threadIdx.x] = (uint32_t)(y >> 32), elo[threadIdx.x] = (uint32_t)y, etoken[threadIdx.x] = __float_as_uint(own.y), eplace[threadIdx.x] = from * kMaxCand + j;
-        all = __syncthreads_count(in);
+        if ((int)threadIdx.x < n4) hi[threadIdx.x] = (uint32_t)(y >> 32), lo[threadIdx.x] = (uint32_t)y;
+        float *token = reinterpret_cast<float *>(lo + n4);
+        if ((int)threadIdx.x < n) token[threadIdx.x] = own.y;
+        got = min(__syncthreads_count(in), k);
+        const int i = threadIdx.x >> 2, at = min(i, n4 - 1);
+        const int rank = rank_below(hi, lo, n, n4, at, k, [](int a) { return (uint32_t)a; });
+        if (i < n && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(hi[i]), s_row[rank] = i / k / P, s_token[rank] = __float_as_int(token[i]);
     } else {
+        const int n4 = join_heads(lists, k);
+        int left = lists, n = INT32_MAX;
+        uint32_t *buffers = s_keys + 2 * n4;
+        if (n4 != 0) {
+            uint32_t *hi = s_keys, *lo = hi + n4;
 #pragma unroll
-        for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
-            const int l = threadIdx.x + i * kJoinThreads, of = l < lists ? l / P : 0;
-            const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head[i], s_lh[of], s_ll[of]) : 0;
-            if (l < n4) his[l] = (uint32_t)(key >> 32), los[l] = (uint32_t)key;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
-            const int at = min(i, n4 - 1);
-            const int rank = rank_below(his, los, n4, n4, at, k, [](int a) { return (uint32_t)a; });
-            if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
-            s_list[atomicAdd(&s_lists, 1)] = i;
-            if (rank == k - 1) s_bar[0] = his[i], s_bar[1] = los[i], s_bar[2] = (uint32_t)i;
-        }
-        __syncthreads();
-        const int left = s_lists;
-        // the k-th head, where there are as many
-        const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
-        const int at_bar = left == k ? (int)s_bar[2] : lists;
-        for (int i = warp; i < left; i += warps) {
-            const int from = s_list[i], of = from / P;
-            for (int j = lane; j < s_len[from]; j += 32) {
-                const float2 x = list[from * k + j];
-                const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]);
-                // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
-                if ((y > bar) | ((y == bar) & (from <= at_bar))) {
-                    const int c = atomicAdd(&s_n, 1);
-                    ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), eplace[c] = from * kMaxCand + j;
+            for (int i = 0; i < kMaxLists / kJoinThreads; ++i) {
+                const int l = threadIdx.x + i * kJoinThreads, of = l < lists ? l / P : 0;
+                const uint64_t key = l < lists && s_len[l] > 0 ? score_key(s_cum[of], head[i], s_lh[of], s_ll[of]) : 0;
+                if (l < n4) hi[l] = (uint32_t)(key >> 32), lo[l] = (uint32_t)key;
+            }
+            __syncthreads();
+            for (int i = threadIdx.x >> 2; i < (n4 + 7 & ~7); i += kJoinThreads / 4) {   // (whole warps: eight items)
+                const int at = min(i, n4 - 1);
+                const int rank = rank_below(hi, lo, n4, n4, at, k, [](int a) { return (uint32_t)a; });
+                if (i >= lists || rank >= k || (threadIdx.x & 3) != 0) continue;
+                s_list[atomicAdd(&s_lists, 1)] = i;
+                atomicOr(&s_take[i / 32], 1u << i % 32);
+                if (rank == k - 1) s_bar[0] = hi[i], s_bar[1] = lo[i], s_bar[2] = (uint32_t)i;
+            }
+            __syncthreads();
+            left = s_lists;
+            // the k-th head, where there are as many
+            const uint64_t bar = left == k ? ((uint64_t)s_bar[0] << 32) | s_bar[1] : 0;
+            const int at_bar = left == k ? (int)s_bar[2] : lists;
+            uint32_t *ehi = buffers, *elo = ehi + kJoinRanked, *etoken = elo + kJoinRanked, *eplace = etoken + kJoinRanked;     // (place: list, and where in it)
+            for (int i = warp; i < left; i += warps) {
+                const int from = s_list[i], of = from / P;
+                for (int j = lane; j < s_len[from]; j += 32) {
+                    const float2 x = list[from * k + j];
+                    const uint64_t y = score_key(s_cum[of], x.x, s_lh[of], s_ll[of]);
+                    // (of equal scores all that lie in lists up to the bar's: of its own, k at most)
+                    if ((y > bar) | ((y == bar) & (from <= at_bar))) {
+                        const int c = atomicAdd(&s_n, 1);
+                        if (c < kJoinRanked) ehi[c] = (uint32_t)(y >> 32), elo[c] = (uint32_t)y, etoken[c] = __float_as_uint(x.y), eplace[c] = from * kMaxCand + j;
+                    }
                 }
             }
+            __syncthreads();
+            n = s_n;
+            if (n <= kJoinRanked) {
+                const int e4 = (n + 3) & ~3;
+                if (threadIdx.x < e4 - n) ehi[n + threadIdx.x] = 0;
+                __syncthreads();
+                for (int i = threadIdx.x >> 2; i < (e4 + 7 & ~7); i += kJoinThreads / 4) {
+                    const int rank = rank_below(ehi, elo, n, e4, min(i, e4 - 1), k, [&](int a) { return eplace[a]; });
+                    if (i < n && rank < k && (threadIdx.x & 3) == 0)
+                        s_score[rank] = from_ordered(ehi[i]), s_row[rank] = (int)(eplace[i] / kMaxCand) / P, s_token[rank] = (int)etoken[i];
+                }
+                got = min(n, k);
+            } else {                                        // the lists in their order (the buffers lie where the entries were)
+                for (int l = threadIdx.x; l < lists; l += kJoinThreads)
+                    if (s_take[l / 32] >> l % 32 & 1) {
+                        int at = __popc(s_take[l / 32] & ((1u << l % 32) - 1));
+                        for (int w = 0; w < l / 32; ++w) at += __popc(s_take[w]);
+                        s_list[at] = l;
+                    }
+                __syncthreads();
+            }
         }
-        __syncthreads();
-        n = all = s_n;
-    }
-    const int all4 = (n + 3) & ~3;
-    if (threadIdx.x < all4 - n) ehi[n + threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x >> 2; i < (all4 + 7 & ~7); i += kJoinThreads / 4) {
-        const int at = min(i, all4 - 1);
-        const int rank = rank_below(ehi, elo, n, all4, at, k, [&](int a) { return eplace[a]; });
-        if (i < n && rank < k && (threadIdx.x & 3) == 0) s_score[rank] = from_ordered(ehi[i]), s_row[rank] = (int)(eplace[i] / kMaxCand) / P, s_token[rank] = (int)etoken[i];
+        if (n > kJoinRanked)
+            got = join_merge(buffers, min(k, lists) * k, left, k, P, [&](int q) { return n4 != 0 ? s_list[q] : q; }, list, s_len, s_cum, s_lh, s_ll, s_score, s_row, s_token);
     }
     __syncthreads();
     if (warp != 0) return;
-    const int got = min(all, k);
     int live = 0;                                           // candidates so far that do not end
     for (int i = lane; i < k + lane; i += 32) {             // (all lanes as often)
         const bool in = i < got;
@@ -596,8 +671,8 @@ int launch_beam_select(int dtype, const void *logits, int64_t stride, int64_t n_
              : dtype == MQD_F16 ? launch_scan<__half>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 1, s)
                                 : launch_scan<__nv_bfloat16>(logits, stride, V, scores, k, ws, n, kAttrSlotBeam + 2, s);
     if (rc != MQ_OK) return rc;
-    const int lists = B * ws.pieces, words = (join_few(lists, k) ? 0 : 2 * (lists + 3)) + 4 * join_room(lists, k);
-    rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (2 * (kMaxLists + 3) + 4 * (kMaxCand * kMaxCand + 4)) * 4, kAttrSlotBeam + 3);
+    const int lists = B * ws.pieces, words = join_words(lists, k);
+    rc = ensure_smem_attr(reinterpret_cast<const void *>(beam_join_kernel), (2 * kMaxLists + 6 * kMaxCand * kMaxCand + 4) * 4, kAttrSlotBeam + 3);
     if (rc != MQ_OK) return rc;
     const cudaError_t e = launch_pdl(beam_join_kernel, dim3((unsigned)n_groups), dim3(kJoinThreads), words * 4, s, ws, B, scores, k, stop, cand_score, cand_row,
                                      cand_token, next_score, next_row, next_token);

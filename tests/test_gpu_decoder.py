@@ -517,6 +517,26 @@ def test_select_is_the_same_every_time_and_in_a_graph():
             assert np.array_equal(a.cpu().numpy(), b)
 
 
+@pytest.mark.parametrize("G, Bm, V, n_cand", [(1, 2, 50001, 64), (1, 1, 9000, 64), (3, 5, 4099, 33), (40, 4, 501, 32), (1, 64, 12289, 64), (2, 16, 20000, 17), (200, 3, 700, 43), (1, 1, 40, 64)])
+def test_select_of_many_equal_logits(G, Bm, V, n_cand):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(V + n_cand)
+    few = torch.randint(-3, 4, (G * Bm, V), generator=g, device="cuda").float()          # seven values
+    scores = -torch.rand((G, Bm), generator=g, device="cuda")
+    check_select(few.to(torch.bfloat16), scores, n_cand, stop=1)
+    few[:] = 1.5                                                                          # and one: the first tokens of the best beam
+    cand, _ = check_select(few.half(), scores, n_cand)
+    n = min(n_cand, V)
+    for i in range(G):
+        best = int(scores[i].argmax())
+        assert (cand[1][i][:n] == i * Bm + best).all() and np.array_equal(cand[2][i][:n], np.arange(n))
+    scores[:] = -0.25                                                                     # equal beams: the lowest row, then the lowest token
+    cand, _ = check_select(few.half(), scores, n_cand)
+    n = min(n_cand, Bm * V)
+    for i in range(G):
+        assert np.array_equal(cand[1][i][:n], i * Bm + np.arange(n) // V) and np.array_equal(cand[2][i][:n], np.arange(n) % V)
+
+
 def test_select_rows_past_32_bits_and_heads_of_one_row():
     import torch
     # rows 2^31 + 40 elements apart
