@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kScanThreads = 256, kScanPer = 16, kTile = kScanThreads * kScanPer;    // values of a thread, of a block at a time
 constexpr int kStages = 3;          // tiles of a block in flight or in work: 48 KB (f32), so that three blocks fit an SM.  128 rows: 22.3 us, two stages 22.7, four 28.5, through registers 27
-constexpr int kBuffer = 256, kPart = 2048, kMaxCand = 64, kMaxLists = 1024, kRoom = kPart + kMaxCand;     // room of a piece's list while it is made
+constexpr int kBuffer = 256, kMaxCand = 64, kMaxLists = 1024, kRoom = 2048 + kMaxCand;     // room of a piece's list while it is made
 
 // order of f32 values (no NaN; +-0 are to be made one before) as unsigned integers, and back
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -206,6 +206,44 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
             if (n < kRoom) s_buf[n] = entry(fminf(to_f32(from[(int)threadIdx.x * VEC + e]), FLT_MAX), t0 + e);
         }
     };
+    // (all threads) a bar that at least k values of a tile pass, where it has as many, and no more than 16 k: those above it, and of those equal to `tie` those up to token `last`
+    auto tile_bar = [&](const float(&v)[kScanPer], float top, int at, float &bar, float &tie, int &last) {
+        // every warp's ceil(k / 8)-th largest of its threads' largest values: at least k values are not below the least of these
+        const uint32_t own = top > -INFINITY ? ordered(top + 0.0f) : 0u;
+        uint32_t key = own, best = 0;
+        for (int j = 0; j < (k + 7) / 8; ++j) {
+            best = __reduce_max_sync(kFull, key);
+            if (lane == __ffs(__ballot_sync(kFull, key == best)) - 1) key = 0;
+        }
+        if (lane == 0) s_key[warp] = best;
+        __syncthreads();
+        uint32_t least = s_key[0];
+#pragma unroll
+        for (int w = 1; w < kScanThreads / 32; ++w) least = min(least, s_key[w]);
+        bar = least != 0 ? below(from_ordered(least)) : -INFINITY;
+        int hits = 0;
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i) hits += v[i] > bar;
+        // a warp has too few values (the end of a row, a mask) or many are equal: the k-th of all threads' largest, by value and token
+        if (__syncthreads_or(__reduce_add_sync(kFull, hits) > kBuffer / (kScanThreads / 32))) {
+            uint2 *s_all = reinterpret_cast<uint2 *>(s_buf + kMaxCand);       // (the list's own entries lie before)
+            int at_top = INT32_MAX;
+#pragma unroll
+            for (int i = kScanPer - 1; i >= 0; --i)
+                if (v[i] == top) at_top = at - first + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
+            s_all[threadIdx.x] = make_uint2(own, (uint32_t)at_top);
+            __syncthreads();
+            int rank = 0;
+#pragma unroll 8
+            for (int j = 0; j < kScanThreads; ++j) {
+                const uint2 o = s_all[j];
+                rank += (o.x > own) | ((o.x == own) & (o.y < (uint32_t)at_top));
+            }
+            const bool kth = own != 0 && rank == k - 1;
+            if (kth) s_bar = make_uint2(own, (uint32_t)at_top);
+            if (__syncthreads_or(kth)) bar = tie = from_ordered(s_bar.x), last = (int)s_bar.y;
+        }
+    };
     // (all threads, after a barrier) the best k of the list's n entries stay; what does not pass their last one is out
     auto settle = [&](int n) {
         if (n > have) {
@@ -245,65 +283,35 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
         int last = INT32_MIN;
         const bool begin = at == e0;
         if (begin) {
-            // every warp's ceil(k / 8)-th largest of its threads' largest values: at least k values are not below the least of these
-            const uint32_t own = top > -INFINITY ? ordered(top + 0.0f) : 0u;
-            uint32_t key = own, best = 0;
-            for (int j = 0; j < (k + 7) / 8; ++j) {
-                best = __reduce_max_sync(kFull, key);
-                if (lane == __ffs(__ballot_sync(kFull, key == best)) - 1) key = 0;
-            }
-            if (lane == 0) s_key[warp] = best;
-            __syncthreads();
-            uint32_t least = s_key[0];
-#pragma unroll
-            for (int w = 1; w < kScanThreads / 32; ++w) least = min(least, s_key[w]);
-            bar = least != 0 ? below(from_ordered(least)) : -INFINITY;
-            int hits = 0;
-#pragma unroll
-            for (int i = 0; i < kScanPer; ++i) hits += v[i] > bar;
-            // a warp has too few values (the end of a row, a mask) or many are equal: the k-th of all threads' largest, by value and token
-            if (__syncthreads_or(__reduce_add_sync(kFull, hits) > kBuffer / (kScanThreads / 32))) {
-                uint2 *s_all = reinterpret_cast<uint2 *>(s_buf);
-                int at_top = INT32_MAX;
-#pragma unroll
-                for (int i = kScanPer - 1; i >= 0; --i)
-                    if (v[i] == top) at_top = at - first + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
-                s_all[threadIdx.x] = make_uint2(own, (uint32_t)at_top);
-                __syncthreads();
-                int rank = 0;
-#pragma unroll 8
-                for (int j = 0; j < kScanThreads; ++j) {
-                    const uint2 o = s_all[j];
-                    rank += (o.x > own) | ((o.x == own) & (o.y < (uint32_t)at_top));
-                }
-                const bool kth = own != 0 && rank == k - 1;
-                if (kth) s_bar = make_uint2(own, (uint32_t)at_top);
-                if (__syncthreads_or(kth)) bar = tie = from_ordered(s_bar.x), last = (int)s_bar.y;
-            }
+            tile_bar(v, top, at, bar, tie, last);
         }
         if (top > bar || last != INT32_MIN) push(v, reinterpret_cast<const T *>(tile), at, bar, tie, last);
         if (!begin && at + kTile - span < tiles * kTile && at + kTile < stop) continue;
         __syncthreads();
         const int n = s_n;
         if (n > kRoom) {
-            // more than the list has room for: the span again, one vector of each thread at a time
+            // more than the list has room for (rows that rise): the span again, a tile at a time, each by a bar of its own (128 rising rows 145 us; settled after every
+            // 2048 values, of which all passed, 8.6 ms)
             __syncthreads();
             if (threadIdx.x == 0) s_n = have;
 #pragma unroll 1
-            for (int again = span; again <= at; again += kTile)
-#pragma unroll 1
-                for (int part = 0; part < kTile / kPart; ++part) {
-                    __syncthreads();
-                    float z[kScanPer];
+            for (int again = span; again <= at; again += kTile) {
+                __syncthreads();
+                float z[kScanPer];
 #pragma unroll
-                    for (int i = 0; i < kScanPer; ++i) {
-                        const int e = again + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
-                        z[i] = e >= first && e < stop && i / (kPart / kScanThreads) == part ? to_f32(base[e]) : -INFINITY;
-                    }
-                    if (clean(z) > thr) push(z, base + again, again, thr, 0.0f, INT32_MIN);
-                    __syncthreads();
-                    settle(s_n);
+                for (int i = 0; i < kScanPer; ++i) {
+                    const int e = again + ((i / VEC) * kScanThreads + (int)threadIdx.x) * VEC + i % VEC;
+                    z[i] = e >= first && e < stop ? to_f32(base[e]) : -INFINITY;
                 }
+                const float most = clean(z);
+                float own_bar = -INFINITY, own_tie = 0.0f;
+                int own_last = INT32_MIN;
+                tile_bar(z, most, again, own_bar, own_tie, own_last);
+                if (own_bar < thr) own_bar = thr, own_last = INT32_MIN;
+                if (most > own_bar || own_last != INT32_MIN) push(z, base + again, again, own_bar, own_tie, own_last);
+                __syncthreads();
+                settle(s_n);
+            }
         } else {
             settle(n);
         }

@@ -537,6 +537,17 @@ def test_select_of_many_equal_logits(G, Bm, V, n_cand):
         assert np.array_equal(cand[1][i][:n], i * Bm + np.arange(n) // V) and np.array_equal(cand[2][i][:n], np.arange(n) % V)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n_cand", [2, 8, 61, 64])
+def test_select_of_rows_that_rise(n_cand, dtype):
+    import torch
+    # pieces of several tiles, each better than all before it
+    x = (torch.arange(60013, device="cuda") * 1e-4).repeat(240, 1)
+    x[::3] += 0.3 * torch.rand((80, 60013), generator=torch.Generator(device="cuda").manual_seed(n_cand), device="cuda")
+    x[5, ::7], x[6, 1000::1001], x[7, :50000] = float("nan"), float("inf"), -float("inf")
+    check_select(x.to(ttype(dtype)), torch.zeros((60, 4), device="cuda") - torch.rand((60, 4), device="cuda"), n_cand, stop=60012)
+
+
 def test_select_rows_past_32_bits_and_heads_of_one_row():
     import torch
     # rows 2^31 + 40 elements apart
