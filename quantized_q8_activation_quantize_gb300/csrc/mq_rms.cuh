@@ -6,6 +6,7 @@
 
 #include "mq_device.cuh"
 #include "mq_internal.h"
+#include "mq_pair.h"
 
 namespace mq {
 
@@ -23,13 +24,6 @@ __device__ __forceinline__ void add_square(float v, float &hi, float &lo) {
     const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bv)), __fsub_rn(p, bv));
     hi = s;
     lo = __fadd_rn(lo, __fadd_rn(err, e));
-}
-
-// Error-free sum a + b = s + e (Knuth's two-sum, branch-free, any order of magnitudes).
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
-    s = __fadd_rn(a, b);
-    const float bv = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bv)), __fsub_rn(b, bv));
 }
 
 // (ah, al) += (bh, bl) for pairs of f32 (a value and its small correction): the high parts add

@@ -14,6 +14,7 @@
 
 #include "mq_rms.cuh"
 #include "mqd.cuh"
+#include "mqd_beam_merge.h"
 
 namespace mq {
 namespace {
@@ -21,13 +22,6 @@ namespace {
 constexpr int kScanThreads = 256, kScanPer = 16, kTile = kScanThreads * kScanPer;    // values of a thread, of a block at a time
 constexpr int kStages = 3;          // tiles of a block in flight or in work: 48 KB (f32), so that three blocks fit an SM.  128 rows: 22.3 us, two stages 22.7, four 28.5, through registers 27
 constexpr int kBuffer = 256, kMaxCand = 64, kMaxLists = 1024, kRoom = 2048 + kMaxCand;     // room of a piece's list while it is made
-
-// order of f32 values (no NaN; +-0 are to be made one before) as unsigned integers, and back
-__device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -340,40 +334,6 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
     }
 }
 
-// ln(sh + sl) of a positive normal number, as a pair: 2^n f with f in [0.7, 1.42), ln f = 2 (t + t^3 / 3 + .. ) with t = (f - 1) / (f + 1) as a pair; the
-// series through t^11 leaves out 2e-11.  (The f64 pipe of this GPU issues ~1.7 operations per clock per SM: log() of a double for every row, with scores in f64
-// below, took ten times the rest of this kernel.)
-__device__ __forceinline__ void pair_log(float sh, float sl, float &h, float &l) {
-    const int n = (int)((__float_as_uint(sh) - 0x3f333333u) >> 23) - (__float_as_uint(sh) < 0x3f333333u ? 512 : 0);
-    const float scale = __uint_as_float((uint32_t)(127 - n) << 23);
-    const float fh = sh * scale, fl = sl * scale, num = fh - 1.0f;
-    float dh, de;
-    two_sum(fh, 1.0f, dh, de);
-    const float t = __fdiv_rn(num, dh);
-    const float r = __fadd_rn(__fmaf_rn(-t, dh, num), __fmaf_rn(-t, __fadd_rn(de, fl), fl));
-    const float t1 = __fdiv_rn(r, dh), z = t * t;
-    float p = 1.0f / 11.0f;
-    p = __fmaf_rn(p, z, 1.0f / 9.0f);
-    p = __fmaf_rn(p, z, 1.0f / 7.0f);
-    p = __fmaf_rn(p, z, 1.0f / 5.0f);
-    p = __fmaf_rn(p, z, 1.0f / 3.0f);
-    const float nf = (float)n;
-    two_sum(nf * 0.693145751953125f, 2.0f * t, h, l);           // ln 2 in two parts, the product with the first exact
-    l = __fadd_rn(l, __fmaf_rn(nf, 1.42860682e-6f, 2.0f * __fmaf_rn(t * z, p, t1)));
-}
-
-// a candidate's score cum + x - (lh + ll) as an f32 pair (the rounded sum, the rest: 48 bits) in the order of unsigned integers (0: none)
-__device__ __forceinline__ uint64_t score_key(float cum, float x, float lh, float ll) {
-    float d, e, h, l;
-    two_sum(x, -lh, d, e);                                      // (|x| and the logarithm may be far apart either way)
-    e = __fsub_rn(e, ll);
-    two_sum(cum, d, h, l);
-    const bool fits = fabsf(h) <= FLT_MAX;                      // (past f32 there is no rest)
-    l = fits ? __fadd_rn(l, e) : 0.0f;
-    const float s = __fadd_rn(h, l);
-    l = fits ? __fsub_rn(l, __fsub_rn(s, h)) : 0.0f;
-    return ((uint64_t)ordered(s + 0.0f) << 32) | ordered(l + 0.0f);
-}
 // How many of the n (a multiple of 4) numbers are larger than this one (EQUAL: or the same).  Four lanes share the count; all of them get it.
 template <bool EQUAL>
 __device__ __forceinline__ int rank_of(const uint32_t *his, int n, uint32_t hi) {
@@ -428,30 +388,30 @@ __device__ __forceinline__ int join_merge(uint32_t *buffers, int room, int left,
                                           const float *s_ll, float *s_score, int *s_row, int *s_token) {
     uint64_t *key = reinterpret_cast<uint64_t *>(buffers), *key2 = key + room;
     uint32_t *place = reinterpret_cast<uint32_t *>(key2 + room), *place2 = place + room;        // list, and where in it
-    for (int i = threadIdx.x; i < left * k; i += kJoinThreads) {
-        const int q = i / k, j = i - q * k, from = list_of(q), of = from / P;
-        key[i] = j < s_len[from] ? score_key(s_cum[of], list[from * k + j].x, s_lh[of], s_ll[of]) : 0;
-        place[i] = from * kMaxCand + j;
+    // A list is in the order of its logits, its keys nearly so (score_key): each is taken as no larger than those before it.  Both buffers begin with places of the lists,
+    // so that whatever a slot holds leads to memory of the call.
+    const int lane = threadIdx.x & 31;
+    for (int q = threadIdx.x >> 5; q < left; q += kJoinThreads / 32) {
+        const int from = list_of(q), of = from / P, n = s_len[from];
+        uint64_t least = ~(uint64_t)0;
+        for (int j0 = 0; j0 < k; j0 += 32) {
+            const int j = j0 + lane;
+            uint64_t x = j < n ? score_key(s_cum[of], list[from * k + j].x, s_lh[of], s_ll[of]) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o && y < x) x = y;
+            }
+            x = x < least ? x : least;
+            least = __shfl_sync(kFull, x, 31);
+            if (j < k) key[q * k + j] = x, key2[q * k + j] = 0, place[q * k + j] = place2[q * k + j] = from * kMaxCand + j;
+        }
     }
     __syncthreads();
     for (int s = 1, runs = left; s < left; s *= 2, runs = (runs + 1) / 2) {         // list a of this round lies at slot a * s
         for (int i = threadIdx.x; i < runs * k; i += kJoinThreads) {
-            const int a = i / k, j = i - a * k;
-            const uint64_t x = key[a * s * k + j];
-            int lo = 0;
-            if ((a ^ 1) < runs) {
-                // before it in the other list: what is better, of an earlier list what is equal too
-                const uint64_t *other = key + (a ^ 1) * s * k, bar = x - (a & 1);
-                for (int hi = k - j; lo < hi;) {        // (past k - j it is out in any case)
-                    const int mid = (lo + hi) >> 1;
-                    if (other[mid] > bar) lo = mid + 1;
-                    else hi = mid;
-                }
-            }
-            if (j + lo < k && (x != 0 || (a & 1) == 0)) {       // (an earlier list's room without an entry is what is left)
-                const int to = (a & ~1) * s * k + j + lo;
-                key2[to] = x, place2[to] = place[a * s * k + j];
-            }
+            const int a = i / k, j = i - a * k, to = merge_slot(key, runs, s, k, a, j);
+            if (to >= 0) key2[to] = key[a * s * k + j], place2[to] = place[a * s * k + j];
         }
         __syncthreads();
         uint64_t *const old = key;

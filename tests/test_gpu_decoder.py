@@ -548,6 +548,18 @@ def test_select_of_rows_that_rise(n_cand, dtype):
     check_select(x.to(ttype(dtype)), torch.zeros((60, 4), device="cuda") - torch.rand((60, 4), device="cuda"), n_cand, stop=60012)
 
 
+@pytest.mark.parametrize("Bm,V,n_cand", [(3, 967, 64), (16, 4001, 32), (5, 2049, 33), (2, 200, 64)])
+def test_select_of_neighbouring_logits(Bm, V, n_cand):
+    # f32 logits one step apart near half a step of the row's logarithm, equal beams: the keys of a list are not in the order of its logits, and lists merge
+    import torch
+    for up in (2, 5, 9, 30):
+        for half in (0.5, 1.0):
+            x = np.float32(half * np.spacing(np.float32(np.log(V))))
+            row = (np.array(x, np.float32).view(np.int32) + up - np.arange(V)).astype(np.int32).view(np.float32)
+            cand, _ = check_select(dev(np.tile(row, (Bm, 1))), torch.full((1, Bm), -1.5, device="cuda"), n_cand)
+            assert (cand[1][0] >= 0).all()
+
+
 def test_select_rows_past_32_bits_and_heads_of_one_row():
     import torch
     # rows 2^31 + 40 elements apart
