@@ -106,7 +106,7 @@ MQ_API int mqd_rope(const mqd_rope_plan *plan, int32_t dtype, const void *x, int
  *
  *   logits     [n_groups * n_beams][vocab] of dtype, rows row_stride >= vocab apart, aligned to one element.  A NaN counts as
  *              -inf, +inf as the largest finite f32
- *   scores     f32 [n_groups][n_beams], the beams' own; -inf (or a NaN): a beam that is not alive
+ *   scores     f32 [n_groups][n_beams], the beams' own; -inf (or a NaN): a beam that is not alive; of one of +inf every candidate has +inf
  *   n_cand     candidates per group, 1 .. 64
  *   cand_*     [n_groups][n_cand]: the best continuations of each group, the best first: score, row, token.  Of equal scores the lowest
  *              row, then the lowest token comes first; tokens of -inf and rows without a finite logit continue nothing; where there are

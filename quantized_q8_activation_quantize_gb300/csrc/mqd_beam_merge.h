@@ -67,6 +67,7 @@ MQ_PAIR uint64_t score_key(float cum, float x, float lh, float ll) {
     two_sum(cum, d, h, l);
     const bool fits = fabsf(h) <= FLT_MAX;                      // (past f32 there is no rest)
     l = fits ? add_rn(l, e) : 0.0f;
+    h = fabsf(cum) <= FLT_MAX ? h : cum;                        // (+inf, a beam's own, stays beside a difference past f32)
     const float s = add_rn(h, l);
     l = fits ? sub_rn(l, sub_rn(s, h)) : 0.0f;
     return ((uint64_t)ordered(add_rn(s, 0.0f)) << 32) | ordered(add_rn(l, 0.0f));

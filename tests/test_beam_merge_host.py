@@ -115,6 +115,16 @@ def test_logarithms(lib):
         assert abs(float(h) + float(l) - math.log(float(F(s)))) <= 7 * 2.0 ** -24 * 0.0038 + 2 * 0.0312 * 7.5e-9 + 2.6e-11 + abs(float(h)) * 2.0 ** -44
 
 
+def test_scores_past_f32(lib):
+    big, inf = float(np.finfo(F).max), float("inf")
+    low, top = keys(lib, 0.0, [-inf], 0.0, 0.0)[0], keys(lib, inf, [0.0], 1.0, 0.0)[0]
+    # a beam of +inf stays there, also beside a logit and a logarithm at the two ends of f32; a score below f32 is -inf
+    assert (keys(lib, inf, [big, 1.0, -1.0, -big], big, 0.0) == top).all()
+    assert keys(lib, 0.0, [-big], big, 0.0)[0] == low and keys(lib, -big, [-big], 0.0, 0.0)[0] == low
+    finite = keys(lib, 0.0, [big, 0.0, -big], 1.0, 0.0)
+    assert low < finite[2] < finite[1] < finite[0] < top
+
+
 def test_a_larger_logit_can_have_the_smaller_key(lib):
     x = np.array([4.7683716e-7, 4.7683713e-7], F)                 # falling
     k = keys(lib, -37.7, x, 10.317374, 4.1082e-7)

@@ -560,6 +560,21 @@ def test_select_of_neighbouring_logits(Bm, V, n_cand):
             assert (cand[1][0] >= 0).all()
 
 
+def test_select_scores_past_f32():
+    import torch
+    big, inf = torch.finfo(torch.float32).max, float("inf")
+    logits = torch.full((2, 4000), -big, device="cuda")   # (one piece a row: equal scores in the order of their logits)
+    logits[0, 7], logits[1, 3000:3003] = big, torch.tensor([1.0, 3.0, 2.0], device="cuda")
+    for n_cand in (4, 64):                                     # (entries ranked, lists merged)
+        # the second beam, of +inf, keeps it: its tokens in the order of their logits come before all of the first's
+        cand, nxt = select(logits, torch.tensor([[0.0, inf]], device="cuda"), n_cand)
+        assert (cand[0] == inf).all() and (cand[1] == 1).all() and cand[2][0][:4].tolist() == [3001, 3002, 3000, 0]
+        assert (nxt[0] == inf).all() and nxt[2][0].tolist() == [3001, 3002]
+        # and where its logits lie 2 FLT_MAX apart
+        cand, _ = select(logits, torch.tensor([[inf, 0.0]], device="cuda"), n_cand)
+        assert (cand[0] == inf).all() and (cand[1] == 0).all() and cand[2][0][:4].tolist() == [7, 0, 1, 2]
+
+
 def test_select_rows_past_32_bits_and_heads_of_one_row():
     import torch
     # rows 2^31 + 40 elements apart
