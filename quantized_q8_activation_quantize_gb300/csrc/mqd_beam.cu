@@ -388,30 +388,47 @@ __device__ __forceinline__ int join_merge(uint32_t *buffers, int room, int left,
                                           const float *s_ll, float *s_score, int *s_row, int *s_token) {
     uint64_t *key = reinterpret_cast<uint64_t *>(buffers), *key2 = key + room;
     uint32_t *place = reinterpret_cast<uint32_t *>(key2 + room), *place2 = place + room;        // list, and where in it
-    // A list is in the order of its logits, its keys nearly so (score_key): each is taken as no larger than those before it.  Both buffers begin with places of the lists,
-    // so that whatever a slot holds leads to memory of the call.
-    const int lane = threadIdx.x & 31;
-    for (int q = threadIdx.x >> 5; q < left; q += kJoinThreads / 32) {
-        const int from = list_of(q), of = from / P, n = s_len[from];
-        uint64_t least = ~(uint64_t)0;
-        for (int j0 = 0; j0 < k; j0 += 32) {
-            const int j = j0 + lane;
-            uint64_t x = j < n ? score_key(s_cum[of], list[from * k + j].x, s_lh[of], s_ll[of]) : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o && y < x) x = y;
-            }
-            x = x < least ? x : least;
-            least = __shfl_sync(kFull, x, 31);
-            if (j < k) key[q * k + j] = x, key2[q * k + j] = 0, place[q * k + j] = place2[q * k + j] = from * kMaxCand + j;
-        }
+    const int dq = kJoinThreads / k, dj = kJoinThreads - dq * k, q0 = threadIdx.x / k, j0 = threadIdx.x - q0 * k;       // (entry i of list i / k, without a division each)
+    // (both buffers begin with places of the lists: whatever a slot holds leads to memory of the call)
+    for (int i = threadIdx.x, q = q0, j = j0; i < left * k; i += kJoinThreads) {
+        const int from = list_of(q), of = from / P;
+        key[i] = j < s_len[from] ? score_key(s_cum[of], list[from * k + j].x, s_lh[of], s_ll[of]) : 0;
+        place[i] = place2[i] = from * kMaxCand + j;
+        q += dq, j += dj;
+        if (j >= k) j -= k, ++q;
     }
     __syncthreads();
+    // A list is in the order of its logits, its keys only nearly so (score_key): where one is not, each is taken as no larger than those before it, a warp a list
+    bool rises = false;
+    for (int i = threadIdx.x, j = j0; i < left * k; i += kJoinThreads) {
+        rises |= j != 0 && key[i] > key[i - 1];
+        j += dj;
+        if (j >= k) j -= k;
+    }
+    if (__syncthreads_or(rises)) {
+        const int lane = threadIdx.x & 31;
+        for (int q = threadIdx.x >> 5; q < left; q += kJoinThreads / 32) {
+            uint64_t least = ~(uint64_t)0;
+            for (int j = lane; j < k + lane; j += 32) {     // (all lanes as often)
+                uint64_t x = j < k ? key[q * k + j] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint64_t y = __shfl_up_sync(kFull, x, o);
+                    if (lane >= o && y < x) x = y;
+                }
+                x = x < least ? x : least;
+                least = __shfl_sync(kFull, x, 31);
+                if (j < k) key[q * k + j] = x;
+            }
+        }
+        __syncthreads();
+    }
     for (int s = 1, runs = left; s < left; s *= 2, runs = (runs + 1) / 2) {         // list a of this round lies at slot a * s
-        for (int i = threadIdx.x; i < runs * k; i += kJoinThreads) {
-            const int a = i / k, j = i - a * k, to = merge_slot(key, runs, s, k, a, j);
+        for (int i = threadIdx.x, a = q0, j = j0; i < runs * k; i += kJoinThreads) {
+            const int to = merge_slot(key, runs, s, k, a, j);
             if (to >= 0) key2[to] = key[a * s * k + j], place2[to] = place[a * s * k + j];
+            a += dq, j += dj;
+            if (j >= k) j -= k, ++a;
         }
         __syncthreads();
         uint64_t *const old = key;
