@@ -2,8 +2,8 @@
 //
 //   score(b, t) = s_b + x_bt - ln sum_t' exp(x_bt')
 //
-// Two kernels.  The scan reads the logits once: a block takes a piece of a row, keeps the sum of exponentials relative to the largest value met
-// (online: a thread rescales its sum when a tile brings a larger one) and, beside it, the piece's best n_cand values, found by a threshold
+// Two kernels.  The scan reads the logits once: a block takes a piece of a row, keeps the sum of exponentials relative to a value met
+// (online: a thread rescales its sum when a tile brings a much larger one) and, beside it, the piece's best n_cand values, found by a threshold
 // that only few values pass.  The join has a block per group: the rows' sums, then ranks, of many lists first of their heads and then of the entries that are left, or mergers of the lists.
 // Within a row the order of the scores is that of the logits, so only the join needs the sums; it compares f32 pairs, 48 bits.
 //
@@ -29,10 +29,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float kLog2e = 1.44269504f;
+constexpr float kLag = 4.0f;            // how far above a thread's reference its values may rise before its sum is rescaled
 __device__ __forceinline__ float exp_neg(float x) { return ex2(x * kLog2e); }
 
 struct BeamPiece {
-    float m;            // largest value (-inf: none)
+    float m;            // what the sum is relative to, a value of the piece (-inf: it has none)
     int32_t n;          // candidates in the list
     float s, e;         // sum of exp(x - m), and what its roundings left out
 };
@@ -117,18 +118,22 @@ __device__ __forceinline__ int keep_best(uint64_t *s_buf, uint64_t *s_best, int 
     return n;
 }
 
-// sum of exp(v - m)
+// sum of exp(v - m), added up as a tree
 __device__ __forceinline__ float tile_sum(const float (&v)[kScanPer], float m) {
     const uint64_t neg = f2_pack(-m, -m), l = f2_pack(kLog2e, kLog2e);
-    uint64_t sum = f2_pack(0.0f, 0.0f);
+    uint64_t sum[kScanPer / 2];
 #pragma unroll
-    for (int i = 0; i < kScanPer; i += 2) {
+    for (int i = 0; i < kScanPer / 2; ++i) {
         float a, b;
-        f2_unpack(f2_mul(f2_add(f2_pack(v[i], v[i + 1]), neg), l), a, b);
-        sum = f2_add(sum, f2_pack(ex2(a), ex2(b)));
+        f2_unpack(f2_mul(f2_add(f2_pack(v[2 * i], v[2 * i + 1]), neg), l), a, b);
+        sum[i] = f2_pack(ex2(a), ex2(b));
     }
+#pragma unroll
+    for (int o = kScanPer / 4; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) sum[i] = f2_add(sum[i], sum[i + o]);
     float a, b;
-    f2_unpack(sum, a, b);
+    f2_unpack(sum[0], a, b);
     return a + b;
 }
 
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
         ask_done();
     }
     if (threadIdx.x == 0) s_n = 0;
-    float m = -INFINITY, s = 0.0f, thr = -INFINITY;
+    float m = -INFINITY, high = -INFINITY, s = 0.0f, rest = 0.0f, thr = -INFINITY;     // high: m + kLag; the sum relative to m, and what its last rounding left out
     int have = 0;
 
     // NaN and +inf as what they count as; the largest
@@ -263,16 +268,21 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
         slot = slot == kStages - 1 ? 0 : slot + 1;
 #pragma unroll
         for (int i = 0; i < kScanPer; ++i) top = fmaxf(top, v[i]);                                      // (NaN aside)
-        float sum = tile_sum(v, fmaxf(top, m));
+        // A sum that was rescaled with every tile of a rising row would take that factor's error as often; so only where values rise by kLag, and the running
+        // sum keeps its roundings: what a row's logarithm is off by does not grow with the row (460 rows of 2^22 equal logits below a peak were off by 1.9e-5 so, by 6e-7 now).
+        float ref = top > high ? top : m, sum = tile_sum(v, ref);
         if (!(sum <= FLT_MAX)) {                            // a NaN or +inf, or nothing yet but -inf
             top = clean(v);
-            sum = fmaxf(top, m) > -INFINITY ? tile_sum(v, fmaxf(top, m)) : 0.0f;
+            ref = top > high ? top : m;
+            sum = ref > -INFINITY ? tile_sum(v, ref) : 0.0f;
         }
-        if (top > m) {
-            s *= exp_neg(m - top);                          // (m = -inf: zero)
-            m = top;
+        if (ref > m) {
+            const float f = exp_neg(m - ref);               // (m = -inf: zero)
+            s *= f, rest *= f, m = ref, high = m + kLag;
         }
-        s += sum;
+        const float more = __fadd_rn(sum, rest), next_s = __fadd_rn(s, more);   // (Kahan)
+        rest = __fsub_rn(more, __fsub_rn(next_s, s));
+        s = next_s;
         float bar = thr, tie = 0.0f;                        // (of equals the first, which the list holds)
         int last = INT32_MIN;
         const bool begin = at == e0;
@@ -317,20 +327,20 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
     float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    if (m > -INFINITY) s *= exp_neg(m - top);
+    s = m > -INFINITY ? (s + rest) * exp_neg(m - top) : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
     if (lane == 0) s_m[warp] = top, s_s[warp] = s;
     __syncthreads();
     if (warp == 0) {
         const float part = lane < kScanThreads / 32 ? s_m[lane] : -INFINITY;
-        float all = part, sum = 0.0f, rest = 0.0f;
+        float all = part, sum = 0.0f, left = 0.0f;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
         if (part > -INFINITY) sum = s_s[lane] * exp_neg(part - all);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) pair_add(sum, rest, __shfl_xor_sync(kFull, sum, o), __shfl_xor_sync(kFull, rest, o));
-        if (lane == 0) *out = {all, have, sum, rest};
+        for (int o = 4; o > 0; o >>= 1) pair_add(sum, left, __shfl_xor_sync(kFull, sum, o), __shfl_xor_sync(kFull, left, o));
+        if (lane == 0) *out = {all, have, sum, left};
     }
 }
 

@@ -575,6 +575,46 @@ def test_select_scores_past_f32():
         assert (cand[0] == inf).all() and (cand[1] == 0).all() and cand[2][0][:4].tolist() == [7, 0, 1, 2]
 
 
+def log_bound(V):
+    """What a row's logarithm may be off by.  A value's distance to the largest is passed in up to five steps (its thread's reference, a warp's, a block's, two among
+    the pieces) and one for each time its thread's values rose by 4 after it, which is ceil(ln(V / 256) / 4) times at most for what still counts.  Each step's exponential is good to 2^-22 (ex2)
+    and its factor rounds by 2^-24; the arguments together are the distance and at most twice 4 more, off by 2^-24 in the difference, 2^-24 in the product and 1.35e-8 in log2(e).
+    What lies further than ln V + 1 from the largest has not the weight to count for more.  Sums of 16 in a tree 4 roundings, a warp's 6, a thread's running sum 2 (it keeps its
+    roundings, but for tiles that are larger than all before them, each of which doubles it); the others are pairs."""
+    steps = 5 + max(0, int(np.ceil(np.log(V / 256) / 4)))
+    return (np.log(V) + 9) * (2 * 2.0 ** -24 + 1.35e-8) + steps * (2.0 ** -22 + 2.0 ** -24) + 12 * 2.0 ** -24
+
+
+def log_error(logits):
+    """of every row; the beams' scores are such that the result is near zero and its own rounding does not count"""
+    import torch
+    R, V = logits.shape
+    top, lse = (torch.empty(R, dtype=torch.float64, device="cuda") for _ in range(2))
+    for r in range(R):
+        x = logits[r].double()
+        top[r], lse[r] = x.max(), torch.logsumexp(x, 0)
+    cum = (lse - top).float().view(R, 1)
+    cand, _ = select(logits, cum, 1, next=False)
+    return float(np.abs(cand[0].astype(np.float64).ravel() - (cum.double().view(R) + top - lse).cpu().numpy()).max())
+
+
+@pytest.mark.parametrize("R,V", [(2, 5000), (4, 152064), (460, 30000), (460, 1 << 22)])       # (460 rows: one block each)
+def test_select_logarithms(R, V):
+    import torch
+    x = torch.empty((R, V), device="cuda")
+    for value in (-11.109375, -1.0, -0.3, -5.7, -8.3, -12.3, -16.1, -17.7):   # one peak over many equal logits, whose errors all go the same way
+        x.fill_(value)
+        x[:, V // 3] = 0
+        assert log_error(x) <= log_bound(V), value
+    ramp = torch.arange(V, device="cuda") / V
+    for rise in (1e-3, 0.1, 1.0, 10.0, 60.0):                                  # every tile a little above the last one
+        x.copy_(ramp * rise)
+        assert log_error(x) <= log_bound(V), rise
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(V))
+    assert log_error(x.mul_(3)) <= log_bound(V)
+    assert log_error(x.bfloat16()) <= log_bound(V)
+
+
 def test_select_rows_past_32_bits_and_heads_of_one_row():
     import torch
     # rows 2^31 + 40 elements apart
