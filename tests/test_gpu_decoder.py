@@ -787,6 +787,51 @@ def test_reorder_matches_the_model(groups, beams, page, max_pages):
         s.check()
 
 
+def test_reorder_of_more_columns_than_a_block_holds():
+    """4096 rows of up to 86 pages: each of the cluster's eight blocks takes 10 or 11 columns of the table and holds 8 at a time, so that every phase reads it in pieces."""
+    groups, beams, page = 16, 256, 32
+    r = np.random.default_rng(11)
+    s = Beams(groups, beams, r.integers(2300, 2700, groups).tolist(), r.integers(1, 40, groups).tolist(), page, heads=1, layers=1, seed=5)
+    most = max(-(-n // page) for n in s.p.len)
+    assert groups * beams == 4096 and -(-most // 8) > 32768 // 4096
+    base = np.repeat(np.arange(groups) * beams, beams)
+    for step in range(4):
+        parent = base + r.integers(0, beams, groups * beams)
+        if step == 1:
+            parent[r.random(len(parent)) < 0.2] = -1
+        if step == 3:
+            parent = r.permutation(groups * beams)             # any map of the rows, across groups
+        assert s.reorder(parent) is not None
+        status()
+        s.check()
+    # a bad entry in a column of the second piece of the last block: nothing changes
+    keep = s.table.clone()
+    b = int(np.argmax(s.p.len))
+    s.table[b, -(-s.p.len[b] // page) - 1] = -7
+    kv.mqkv_reorder(s.cache, s.seqs, i32(parent), s.ws)
+    status("page table")
+    s.table.copy_(keep)
+    s.check()
+    # too few pages: the counts of all columns go back.  One row ends whose own pages are named elsewhere too, another is continued twice, and no page is free
+    parent = r.permutation(groups * beams)
+    here, twice = [i for i in range(len(parent)) if s.p.len[parent[i]] % page][:2]
+    ends, parent[here] = parent[here], parent[twice]
+    own = [x for x in s.p.table[ends] if s.p.refs[x] == 1]
+    for x in s.p.free():
+        s.p.refs[x] = 1
+    for x in own:
+        s.p.refs[x] += 1
+    s.refs.copy_(i32(s.p.refs))
+    assert own and s.reorder(parent) is None
+    status("too few free pages")
+    s.check()
+    s.p.refs[own[0]] -= 1                                      # this one comes free in the call, and takes the copy
+    s.refs.copy_(i32(s.p.refs))
+    assert [d for _, d, _ in s.reorder(parent)] == own[:1]
+    status()
+    s.check()
+
+
 def test_reorder_takes_pages_that_end_in_the_same_call():
     # no page is free before: what row 1 leaves holds the copy of row 0's last page
     s = Beams(1, 2, [32], [40], 64, spare=0, seed=1)
