@@ -74,7 +74,8 @@ typedef enum {
 
 /* Fills turns[rot_dim / 2] (HOST memory) with F_i; the caller copies it to the device.  rot_dim: a multiple of 8 from 8 to 1024; base > 1;
  * factor >= 1; original > 0 and 0 < low < high for the last two.  factors: NULL or HOST [rot_dim / 2] > 0, by which f_i is divided at the
- * end (a model's own table).  MQ_ERR_ARG for other values, or where a pair would turn a whole turn or more per position.
+ * end (a model's own table).  MQ_ERR_ARG for other values, where MQD_ROPE_BASE's base passes the
+ * range of a double, or where a pair would turn a whole turn or more per position.
  * Host-only. */
 MQ_API int mqd_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor, double original, double low, double high,
                           const double *factors, uint64_t *turns);

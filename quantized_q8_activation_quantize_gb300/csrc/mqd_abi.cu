@@ -171,6 +171,7 @@ int mqd_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor,
         return set_error(MQ_ERR_ARG, "%s: original=%g must be positive, and 0 < low=%g < high=%g", fn, original, low, high);
     const double two_pi = 6.283185307179586476925286766559, n = rot_dim;
     if (scaling == MQD_ROPE_BASE) base *= std::pow(factor, n / (n - 2.0));
+    if (!std::isfinite(base)) return set_error(MQ_ERR_ARG, "%s: factor=%g takes the base past the range of a double", fn, factor);
     const auto pair_of = [&](double t) { return n * std::log(original / (two_pi * t)) / (2.0 * std::log(base)); };
     double i0 = 0.0, i1 = 0.0;
     if (scaling == MQD_ROPE_INDEX) {

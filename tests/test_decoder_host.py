@@ -121,6 +121,13 @@ def test_turns_refusals(L):
         dec.mqd_rope_turns(128, factors=[1.0])
 
 
+def test_a_stretched_base_stays_a_number(L):
+    out = (ctypes.c_uint64 * 4)()
+    rc = caller(L.mqd_rope_turns, [8, 1e300, 2, 1e7, 0.0, 1.0, 4.0, None, out])
+    assert rc(_3=1e10) == ARG and "range of a double" in B.last_error()                   # (all pairs but the first would stand still)
+    assert rc(_3=1e5) == OK
+
+
 TURNS, POS = 6 << 20, 7 << 20
 
 
