@@ -158,6 +158,8 @@ def rope_plan(rot_dim: int, base: float = 10000.0, interleaved: bool = False, am
     """The description of a rotation (``scaling`` as in mqd_rope_turns), with its table on the device."""
     import torch
     table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in mqd_rope_turns(rot_dim, base, **scaling)], dtype=torch.int64, device=device)
+    if not table.is_cuda:
+        _bad(f"the table of a rotation is read by kernels: device {device} is not a CUDA device")
     p = RopePlan(table.data_ptr(), rot_dim, interleaved, amplitude)
     p.tensors = (table,)
     return p

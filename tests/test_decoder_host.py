@@ -219,6 +219,11 @@ def test_binding_refusals(L):
         dec.mqd_beam_select(t, t[0], (t, t, t), None, -1, t)
 
 
+def test_a_plan_lies_on_the_device(L):
+    with pytest.raises(B.MQError, match="not a CUDA"):
+        dec.rope_plan(64, device="cpu")
+
+
 def cos_sin_model(pos, F):
     """rope_cos_sin of csrc/mqd_rope.cuh in numpy float32 (fused multiply-adds through f64 products)"""
     f = np.float32
