@@ -116,6 +116,7 @@ class Search:
         self.scores = torch.full((1, beams), -torch.inf, device="cuda")
         self.row, self.token = (torch.zeros((1, beams), dtype=torch.int32, device="cuda") for _ in range(2))
         self.cand = [torch.empty((1, 2 * beams), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+        self.rows = torch.arange(beams, dtype=torch.int32, device="cuda")
         self.ws = decoder.alloc_beam_workspace(1, beams, vocab, 2 * beams)
 
     def select(self):
@@ -133,8 +134,10 @@ class Search:
         x.copy_(self.table[self.token.view(-1).clamp(min=0).long()])
 
     def run(self, prompt, steps):
-        """prompt: token ids.  The beams' tokens (a list each, without the prompt; shorter where a search has run out) and their scores."""
+        """prompt: token ids.  The beams' tokens (a list each, without the prompt; shorter where a search has run out) and their scores.  The
+        first `beams` rows of the cache are the search's: what they hold is released first."""
         m = self.model
+        kv.mqkv_release(m.cache, m.seqs(self.beams), self.rows)
         first = self.table[torch.as_tensor(prompt, device="cuda")]
         m.step(first, 1)
         plane = B.alloc_plane(1, m.hidden)
@@ -142,6 +145,7 @@ class Search:
         B.mq_quantize_q8_ex(last, 1, m.hidden, m.norm, 1e-6, m.sections(1), plane)
         B.matmul("q4k", self.head, self.vocab, m.hidden, plane, 1, self.logits[:1])
         self.logits.mul_(self.scale)
+        self.scores.fill_(-torch.inf)                          # one beam is alive
         self.scores[0, 0] = 0
         self.select()
         taken = [(self.row.view(-1).clone(), self.token.view(-1).clone())]

@@ -957,3 +957,21 @@ def test_captured_search_step_equals_the_same_calls():
         got.append([t.clone() for t in (x, s.scores, s.row, s.token, m.table, m.len, m.refs, m.pool)])
     for a, b in zip(*got):
         same(a, b)
+
+
+def test_a_search_serves_one_prompt_after_another():
+    import torch
+    from examples import kv_decode
+    m = kv_decode.Attention(2, 512, 4, 2, 64, 3, 60, 32)
+    s = kv_decode.Search(m, 3, 300)
+    r = np.random.default_rng(4)
+    prompts = [r.integers(0, 300, n).tolist() for n in (30, 7, 30)]
+    prompts[2] = prompts[0]
+    paths = [s.run(p, 12) for p in prompts]
+    status()
+    assert paths[0] == paths[2] and paths[0] != paths[1]      # (the same calls on the same pages: bit for bit)
+    assert m.len.tolist() == [41] * 3
+    other = kv_decode.Search(kv_decode.Attention(2, 512, 4, 2, 64, 3, 60, 32), 3, 300)
+    assert other.run(prompts[1], 12) == paths[1]
+    names = torch.bincount(m.table[m.table >= 0].long(), minlength=len(m.refs))
+    assert torch.equal(names.int(), m.refs)
