@@ -30,9 +30,9 @@ struct TurnedRows {
 };
 
 // One block of 32 slots of a sequence and `each` pairs of its 2 H vectors (half, head), from pair y0 on: the angles once for all heads, then two vectors at a time, four
-// warps each, all of a lane's values in registers between the maximum and the codes, the next vectors on their way into shared memory.  Bound by instructions (17 a value) at 16
-// warps an SM: 40960 tokens of 8 heads of 128 take 67 us from bf16 (3.7 TB/s) and 78 from f32 (5.4 TB/s); one vector at a time by eight warps, half the registers, 91 and 105
-// for 86 and 102 then.  A lane holds two quads of a row that
+// warps each, all of a lane's values in registers between the maximum and the codes, the next vectors on their way into shared memory.  Bound by latency at 16 warps
+// an SM (17 instructions a value in 54 % of the issue slots, a quarter of the warps): 40960 tokens of 8 heads of 128 take 67 us from bf16 (3.7 TB/s) and 78 from f32 (5.4 TB/s).
+// Before the ring took the loads off its path, one vector at a time by eight warps, half the registers, took 91 and 105 for 86 and 102.  A lane holds two quads of a row that
 // are turned with one another (quads j and j + half / 4, or neighbours), so that a turn needs no exchange.  Unit u belongs to the last sequence b with U(b) <= u,
 // U(b) = begin(b) / 32 + 2 b, as in mqkv_append, whose arithmetic this is.
 template <typename T, int D>

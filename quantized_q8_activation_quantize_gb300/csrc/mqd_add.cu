@@ -76,8 +76,9 @@ __device__ __forceinline__ void norm8(float (&v)[8], float r, const float *w) {
 
 // One row per group of WT = 2^wt_log2 warps, warp g of it holding chunks g, g + WT, .. of 256 values (at most NC; lane l: values
 // 8 l .. 8 l + 7 of each).  Many rows are bound by HBM: 3314 rows of 3584 f32 values with all sections 26.6 us, 6.9 TB/s of the bytes that they move; 9001 rows of 8192 bf16
-// values 111 us, 6.3 TB/s; 4000 of 4096 33 us, 4.8 TB/s (scales and sums lie block-major, so that a row's are single words in as many sectors: 4% without their
-// stores).  Three blocks of eight warps an SM (f32) or four (16 bits), so that one row's sums hide under the others' loads; rows that follow one another in
+// values 111 us, 6.3 TB/s.  Fewer 16-bit values are bound by the latency of a row's chain, at 46 % of the warps and 64 % of the issue slots: with all sections about 6 us
+// and 6.6 for every 4 M values (4000 rows of 4096 32.6 us, 4.8 TB/s; 16000 112, 5.6; 2000 of 8192 32.4; from 3648 to 4864 rows, 3 to 4 waves, on one line), with q8 alone,
+// a quarter of the bytes less, 6.1 (4000 30.0).  The stores of scales and sums, single words in as many sectors, are 4 %.  Three blocks of eight warps an SM (f32) or four (16 bits), so that one row's sums hide under the others' loads; rows that follow one another in
 // a resident block, the next on its way, took 56 us for 40 and 175 for 165 (with the plane read back).
 template <typename T, int NC, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(T) == 4 ? 3 : 4) add_quantize_regs_kernel(AddQuantize a, Plane p, int wt_log2) {

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
             if (n < kRoom) s_buf[n] = entry(fminf(to_f32(from[(int)threadIdx.x * VEC + e]), FLT_MAX), t0 + e);
         }
     };
-    // (all threads) a bar that at least k values of a tile pass, where it has as many, and no more than 16 k: those above it, and of those equal to `tie` those up to token `last`
+    // (all threads) a bar that at least k values of a tile pass, where it has as many, and no more than the larger of kBuffer and 16 k: those above it, and of those equal to `tie` those up to token `last`
     auto tile_bar = [&](const float(&v)[kScanPer], float top, int at, float &bar, float &tie, int &last) {
         // every warp's ceil(k / 8)-th largest of its threads' largest values: at least k values are not below the least of these
         const uint32_t own = top > -INFINITY ? ordered(top + 0.0f) : 0u;
@@ -624,8 +624,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) beam_join_kernel(BeamWs ws, i
 // pieces of a row, and their length: some for every SM, none longer than the others (a piece of a few values would have no threshold)
 void beam_split(int64_t rows, int B, int64_t V, BeamWs *ws) {
     const int64_t all = (V + 7 + kTile - 1) / kTile;        // (a row begins up to seven places past a boundary)
-    const int64_t most = kMaxLists / B;                     // lists of a group: one per thread of the join
+    const int64_t most = kMaxLists / B;                     // lists of a group: up to two a thread of the join
     int64_t n = 3 * sm_count() / rows;                      // one wave of blocks, three to an SM (128 rows: 22.3 us, with 2 25.1, 4 26.6, 6 25.5)
+    // (where that whole number changes, rows of 50000 bf16 logits, two candidates a beam: 152 rows, three pieces each, 14.1 us; 228, two, 14.3; 229, one, 16.8; 300 18.3; 456 18.0; 457, a
+    // second wave, 23.8)
     if (n > all) n = all;
     if (n < 1) n = 1;
     if (n > most) n = most;

@@ -31,11 +31,6 @@ __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, uint64_t F, float am
     return make_float2(__fmul_rn(x, ax), __fmul_rn(y, ay));
 }
 
-__device__ __forceinline__ void rope_turn(float2 cs, float &u, float &v) {
-    const float a = __fmaf_rn(u, cs.x, -__fmul_rn(v, cs.y)), b = __fmaf_rn(v, cs.x, __fmul_rn(u, cs.y));
-    u = a, v = b;
-}
-
 constexpr int kRopeThreads = 256, kRopePairs = 512;         // pairs whose (cos, sin) a block holds
 
 template <typename T, int W>
@@ -62,7 +57,7 @@ __device__ __forceinline__ void store_w(T *p, const float (&x)[W]) {
     else store8(p, pack8(x, T()));
 }
 
-// two neighbouring pairs of different halves, u = (u0, u1) and v = (v0, v1), as rope_turn on each: c = (c0, c1), s = (s0, s1)
+// (u, v) -> (u c - v s, v c + u s) of two neighbouring pairs, the products with s rounded, the sums fused: u = (u0, u1) and v = (v0, v1), c = (c0, c1), s = (s0, s1)
 __device__ __forceinline__ void rope_turn2(uint64_t c, uint64_t s, uint64_t minus_s, uint64_t &u, uint64_t &v) {
     const uint64_t a = f2_fma(u, c, f2_mul(v, minus_s)), b = f2_fma(v, c, f2_mul(u, s));
     u = a, v = b;
